@@ -21,8 +21,8 @@ OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libfcp.so")
 OUT_DIR_CHECKED = os.path.join(HERE, "_lib_checked")
 LIB_CHECKED = os.path.join(OUT_DIR_CHECKED, "libfcp.so")
-SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "copy_kernels.cu", "noalloc.cu", "plan.cpp",
-           "tables.cpp"]
+SOURCES = ["api.cu", "attn_fwd.cu", "attn_bwd.cu", "copy_kernels.cu", "noalloc.cu", "norm_rope.cu",
+           "plan.cpp", "tables.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -271,11 +271,13 @@ int fcp_plan_upload(const fcp_plan_t* plan, void* dev_buf, int64_t bytes, void* 
 // 0) and the persistent kernels' work counter (byte kWorkCounterOff); D_i
 // (fp32 [Hq][T]); fp16 copies of Q and dO ([T][Hq][d] each, backward); fp16
 // copies of V ([T][Hkv][d]) and of the received V rows ([R][Hkv][d], R = all
-// shards' remote rows of the plan), the forward's P*V operands.
+// shards' remote rows of the plan), the forward's P*V operands; e4m3 copies
+// of Q, K and the received K rows; the tickets (zero between calls) and
+// partial sums of the norm weights' gradients.
 constexpr int64_t kWorkCounterOff = 64;
 
 struct WsLayout {
-  int64_t delta, q16, do16, v16, vb16, q8, k8, kb8, total;
+  int64_t delta, q16, do16, v16, vb16, q8, k8, kb8, tickets, partial, total;
 };
 
 // Header words of the e4m3 Q K^T forward: amax bits of Q and K, then their
@@ -301,7 +303,10 @@ static WsLayout ws_layout(const fcp_dims& d, int64_t remote_rows) {
   w.q8 = w.vb16 + ws_align(R * hkv * dd * 2);
   w.k8 = w.q8 + ws_align(T * hq * dd);
   w.kb8 = w.k8 + ws_align(T * hkv * dd);
-  w.total = w.kb8 + ws_align(R * hkv * dd);
+  w.tickets = w.kb8 + ws_align(R * hkv * dd);
+  constexpr int64_t groups = (fcp::kNormRopeMaxCtas + fcp::kNormRopeGroup - 1) / fcp::kNormRopeGroup;
+  w.partial = w.tickets + ws_align((1 + groups) * 4);
+  w.total = w.partial + ws_align((fcp::kNormRopeMaxCtas + groups) * 2 * dd * 4);
   return w;
 }
 
@@ -587,6 +592,173 @@ int fcp_attn_bwd(const void* q, const void* k, const void* v, const void* kbuf, 
   a.d = dims.d;
   a.num_sms = num_sms();
   return fcp::launch_attn_bwd(a, s);
+}
+
+// Rows of a strided operand: T rows of `len` bytes, `stride` bytes apart.
+struct RowSpan {
+  uintptr_t at;
+  int64_t stride, len;
+};
+
+// Whether a byte lies in a row of both. Spans with one stride are compared
+// row by row (slices of one fused tensor interleave without sharing a byte);
+// others by their whole extent.
+static bool spans_meet(const RowSpan& a, const RowSpan& b, int64_t rows) {
+  const int64_t ext_a = (rows - 1) * a.stride + a.len, ext_b = (rows - 1) * b.stride + b.len;
+  if (a.at + (uintptr_t)ext_a <= b.at || b.at + (uintptr_t)ext_b <= a.at) return false;
+  if (a.stride != b.stride) return true;
+  const int64_t off = ((int64_t)(b.at - a.at) % a.stride + a.stride) % a.stride;  // b's start inside a row of a
+  return off < a.len || off + b.len > a.stride;
+}
+
+static int check_norm_rope(const fcp_norm_rope* nr, const void* wq, const void* wk, const float* inv_freq,
+                           const fcp_dims& dims) {
+  if (!nr || (nr->norm != 0 && nr->norm != 1) || (nr->interleaved != 0 && nr->interleaved != 1) ||
+      (nr->w_dtype != FCP_OUT_BF16 && nr->w_dtype != FCP_OUT_F32))
+    return FCP_ERR_INVALID_ARG;
+  if (nr->norm && !(nr->eps >= 0.f && nr->eps <= 3.4e38f)) return FCP_ERR_INVALID_ARG;
+  if (!nr->norm && (wq || wk)) return FCP_ERR_INVALID_ARG;
+  if (nr->rot_dim < 0 || nr->rot_dim > dims.d) return FCP_ERR_INVALID_ARG;
+  if (nr->rot_dim % 16) return FCP_ERR_UNSUPPORTED;
+  if (nr->rot_dim > 0 && (!inv_freq || (reinterpret_cast<uintptr_t>(inv_freq) & 3))) return FCP_ERR_INVALID_ARG;
+  const uintptr_t wmask = nr->w_dtype == FCP_OUT_F32 ? 3 : 1;
+  if ((reinterpret_cast<uintptr_t>(wq) & wmask) || (reinterpret_cast<uintptr_t>(wk) & wmask))
+    return FCP_ERR_INVALID_ARG;
+  return FCP_OK;
+}
+
+// The launch's tiles, weights and options; the operands are set by the callers.
+static fcp::NormRopeLaunch norm_rope_launch(const fcp_norm_rope* nr, const void* wq, const void* wk,
+                                            const float* inv_freq, const fcp_dev_plan* plan, int32_t shard,
+                                            const fcp_dims& dims) {
+  const Plan* p = plan->host;
+  fcp::NormRopeLaunch a;
+  std::memset(&a, 0, sizeof(a));
+  int32_t t0 = 0, t1 = plan->counts[fcp::TB_FTILES];
+  a.rows = p->T;
+  if (shard >= 0) {
+    t0 = host_at(p, fcp::TB_FSHARD, shard);
+    t1 = host_at(p, fcp::TB_FSHARD, shard + 1);
+    a.rows = p->shards[shard].tokens;
+  }
+  a.n_tiles = t1 - t0;
+  a.d = dims.d;
+  a.interleaved = nr->interleaved != 0;
+  a.num_sms = num_sms();
+  a.p.pieces = table(plan, fcp::TB_PIECES);
+  a.p.tiles = table(plan, fcp::TB_FTILES) + 4 * (int64_t)t0;
+  a.p.n_pieces = plan->counts[fcp::TB_PIECES];
+  a.p.T = dims.T;
+  a.p.hq = dims.hq;
+  a.p.hkv = dims.hkv;
+  a.p.norm = nr->norm;
+  a.p.eps = nr->eps;
+  a.p.rot_dim = nr->rot_dim;
+  a.p.w_f32 = nr->w_dtype == FCP_OUT_F32;
+  a.p.inv_freq = inv_freq;
+  a.p.wq = wq;
+  a.p.wk = wk;
+  return a;
+}
+
+// A strided operand of `heads` heads: 16-byte aligned rows that hold them.
+static bool strided_ok(const void* ptr, int64_t stride, int64_t heads, const fcp_dims& dims) {
+  return ptr && aligned16(ptr) && stride % 8 == 0 && stride >= heads * dims.d &&
+         stride <= INT64_MAX / 4 / std::max(dims.T, 1);
+}
+
+int fcp_qk_norm_rope(const void* q_in, int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
+                     int64_t v_stride, const void* wq, const void* wk, const float* inv_freq,
+                     const fcp_norm_rope* nr, const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, void* q, void* k,
+                     void* v, void* stream) {
+  int st = check_dev_plan(plan, shard);
+  if (st) return st;
+  if ((st = check_dims(dims, plan->host))) return st;
+  if ((st = check_norm_rope(nr, wq, wk, inv_freq, dims))) return st;
+  if (!strided_ok(q_in, q_stride, dims.hq, dims) || !strided_ok(k_in, k_stride, dims.hkv, dims)) return FCP_ERR_INVALID_ARG;
+  if (!v != !v_in || (v && !strided_ok(v_in, v_stride, dims.hkv, dims))) return FCP_ERR_INVALID_ARG;
+  if (!q || !k || !aligned16(q) || !aligned16(k) || !aligned16(v)) return FCP_ERR_INVALID_ARG;
+  const int64_t lq = (int64_t)dims.hq * dims.d * 2, lk = (int64_t)dims.hkv * dims.d * 2;
+  const RowSpan in[3] = {{(uintptr_t)q_in, q_stride * 2, lq}, {(uintptr_t)k_in, k_stride * 2, lk}, {(uintptr_t)v_in, v_stride * 2, lk}};
+  const RowSpan out[3] = {{(uintptr_t)q, lq, lq}, {(uintptr_t)k, lk, lk}, {(uintptr_t)v, lk, lk}};
+  const int n = v ? 3 : 2;
+  for (int o = 0; o < n; ++o) {
+    for (int i = 0; i < n; ++i) {
+      const bool in_place = i == o && in[i].at == out[o].at && in[i].stride == out[o].stride;
+      if (!in_place && spans_meet(out[o], in[i], dims.T)) return FCP_ERR_INVALID_ARG;
+      if (i < o && spans_meet(out[o], out[i], dims.T)) return FCP_ERR_INVALID_ARG;
+    }
+  }
+  fcp::NormRopeLaunch a = norm_rope_launch(nr, wq, wk, inv_freq, plan, shard, dims);
+  a.p.q_in = static_cast<const __nv_bfloat16*>(q_in);
+  a.p.k_in = static_cast<const __nv_bfloat16*>(k_in);
+  a.p.v_in = static_cast<const __nv_bfloat16*>(v_in);
+  a.p.q_in_stride = q_stride;
+  a.p.k_in_stride = k_stride;
+  a.p.v_in_stride = v_stride;
+  a.p.q = static_cast<__nv_bfloat16*>(q);
+  a.p.k = static_cast<__nv_bfloat16*>(k);
+  a.p.v = static_cast<__nv_bfloat16*>(v);
+  return fcp::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
+}
+
+int fcp_qk_norm_rope_bwd(const float* dq, const float* dk, const float* dv, const void* q_in, int64_t q_stride,
+                         const void* k_in, int64_t k_stride, const void* wq, const void* wk, const float* inv_freq,
+                         const fcp_norm_rope* nr, const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, void* dq_in,
+                         int64_t dq_stride, void* dk_in, int64_t dk_stride, void* dv_in, int64_t dv_stride, float* dwq,
+                         float* dwk, void* ws, int64_t ws_bytes, void* stream) {
+  int st = check_dev_plan(plan, shard);
+  if (st) return st;
+  if ((st = check_dims(dims, plan->host))) return st;
+  if ((st = check_norm_rope(nr, wq, wk, inv_freq, dims))) return st;
+  if (!dq || !dk || !aligned16(dq) || !aligned16(dk) || !aligned16(dv)) return FCP_ERR_INVALID_ARG;
+  if (nr->norm && (!strided_ok(q_in, q_stride, dims.hq, dims) || !strided_ok(k_in, k_stride, dims.hkv, dims)))
+    return FCP_ERR_INVALID_ARG;
+  if (!strided_ok(dq_in, dq_stride, dims.hq, dims) || !strided_ok(dk_in, dk_stride, dims.hkv, dims))
+    return FCP_ERR_INVALID_ARG;
+  if (!dv != !dv_in || (dv && !strided_ok(dv_in, dv_stride, dims.hkv, dims))) return FCP_ERR_INVALID_ARG;
+  if (!nr->norm && (dwq || dwk)) return FCP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(dwq) & 3) || (reinterpret_cast<uintptr_t>(dwk) & 3)) return FCP_ERR_INVALID_ARG;
+  if (!ws || !aligned16(ws)) return FCP_ERR_INVALID_ARG;
+  const WsLayout wl = ws_layout(dims, plan->host->total_remote);
+  if (ws_bytes < wl.total) return FCP_ERR_CAPACITY;
+  const int64_t lq = (int64_t)dims.hq * dims.d, lk = (int64_t)dims.hkv * dims.d;
+  const RowSpan out[3] = {{(uintptr_t)dq_in, dq_stride * 2, lq * 2}, {(uintptr_t)dk_in, dk_stride * 2, lk * 2}, {(uintptr_t)dv_in, dv_stride * 2, lk * 2}};
+  const RowSpan grad[3] = {{(uintptr_t)dq, lq * 4, lq * 4}, {(uintptr_t)dk, lk * 4, lk * 4}, {(uintptr_t)dv, lk * 4, lk * 4}};
+  const RowSpan x[2] = {{(uintptr_t)q_in, q_stride * 2, lq * 2}, {(uintptr_t)k_in, k_stride * 2, lk * 2}};
+  const int n = dv ? 3 : 2;
+  for (int o = 0; o < n; ++o) {
+    for (int i = 0; i < n; ++i) {
+      if (spans_meet(out[o], grad[i], dims.T)) return FCP_ERR_INVALID_ARG;
+      if (i < o && spans_meet(out[o], out[i], dims.T)) return FCP_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < 2 && nr->norm; ++i) {
+      const bool in_place = i == o && x[i].at == out[o].at && x[i].stride == out[o].stride;
+      if (!in_place && spans_meet(out[o], x[i], dims.T)) return FCP_ERR_INVALID_ARG;
+    }
+  }
+  fcp::NormRopeLaunch a = norm_rope_launch(nr, wq, wk, inv_freq, plan, shard, dims);
+  a.backward = true;
+  a.p.q_in = static_cast<const __nv_bfloat16*>(q_in);
+  a.p.k_in = static_cast<const __nv_bfloat16*>(k_in);
+  a.p.q_in_stride = q_stride;
+  a.p.k_in_stride = k_stride;
+  a.p.dq = dq;
+  a.p.dk = dk;
+  a.p.dv = dv;
+  a.p.dq_in = static_cast<__nv_bfloat16*>(dq_in);
+  a.p.dk_in = static_cast<__nv_bfloat16*>(dk_in);
+  a.p.dv_in = static_cast<__nv_bfloat16*>(dv_in);
+  a.p.dq_in_stride = dq_stride;
+  a.p.dk_in_stride = dk_stride;
+  a.p.dv_in_stride = dv_stride;
+  a.p.dwq = dwq;
+  a.p.dwk = dwk;
+  char* wsb = static_cast<char*>(ws);
+  a.p.partial = reinterpret_cast<float*>(wsb + wl.partial);
+  a.p.tickets = reinterpret_cast<int*>(wsb + wl.tickets);
+  a.p.err = static_cast<int*>(ws);
+  return fcp::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
 }
 
 int fcp_get_device_status(void* ws, void* stream) {

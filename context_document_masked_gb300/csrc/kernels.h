@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -131,5 +132,56 @@ int launch_gather(const void* k, const void* v, const int32_t* tasks, int32_t n_
 
 int launch_merge(const float* o_parts, const float* lse_parts, int32_t B, int64_t rows, int32_t hq,
                  int32_t d, void* out, float* lse_out, int num_sms, cudaStream_t st);
+
+// Head norm and rotation, and their gradient (norm_rope.cu). At most
+// kNormRopeMaxCtas CTAs write partial sums of the weight gradients, summed in
+// groups of kNormRopeGroup.
+constexpr int kNormRopeMaxCtas = 512;
+constexpr int kNormRopeGroup = 16;
+
+struct NormRopeParams {
+  const int32_t* pieces;   // plan piece table
+  const int32_t* tiles;    // query tiles of the launch (piece, q_start, q_rows, cost)
+  int32_t n_pieces;        // table size (checked build)
+  int32_t n_units, chunk, chunks;  // units of `chunk` rows, `chunks` of them a tile (set by the launch)
+  int32_t T, hq, hkv;
+  int32_t norm;            // 0: rotation alone
+  float eps;
+  int32_t rot_dim;
+  int32_t w_f32;           // weights: 1 fp32, 0 bf16
+  const float* inv_freq;   // [rot_dim / 2]
+  const void* wq;          // [d] or null (all ones)
+  const void* wk;
+  const __nv_bfloat16* q_in;  // rows of heads x d values, strides in elements
+  const __nv_bfloat16* k_in;
+  const __nv_bfloat16* v_in;
+  int64_t q_in_stride, k_in_stride, v_in_stride;
+  __nv_bfloat16* q;        // forward: contiguous outputs
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;        // null: no V rows
+  const float* dq;         // backward: contiguous fp32 gradients
+  const float* dk;
+  const float* dv;         // null: no V rows
+  __nv_bfloat16* dq_in;
+  __nv_bfloat16* dk_in;
+  __nv_bfloat16* dv_in;
+  int64_t dq_in_stride, dk_in_stride, dv_in_stride;
+  float* dwq;              // [d], accumulated, or null
+  float* dwk;
+  float* partial;          // [kNormRopeMaxCtas + their groups][2][d]
+  int* tickets;            // 1 + number of groups, zero at launch and at its end
+  int* err;                // error word (checked build) or null
+};
+
+struct NormRopeLaunch {
+  NormRopeParams p;
+  int32_t n_tiles;
+  int64_t rows;            // rows of those tiles
+  int d;
+  bool interleaved, backward;
+  int num_sms;
+};
+
+int launch_norm_rope(const NormRopeLaunch& a, cudaStream_t st);
 
 }  // namespace fcp

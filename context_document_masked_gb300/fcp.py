@@ -28,7 +28,8 @@ EXPORTED = (
     "fcp_workspace_bytes", "fcp_gather_kv", "fcp_attn_fwd", "fcp_merge", "fcp_attn_bwd",
     "fcp_get_device_status", "fcp_debug_set_wait_limit", "fcp_attn_fwd_noalloc", "fcp_attn_fwd_ring",
     "fcp_attn_fwd_qk8", "fcp_quant_e4m3", "fcp_plan_device_image", "fcp_plan_bind",
-    "fcp_debug_rescale_events", "fcp_round_bf16", "fcp_merge_ring",
+    "fcp_debug_rescale_events", "fcp_round_bf16", "fcp_merge_ring", "fcp_qk_norm_rope",
+    "fcp_qk_norm_rope_bwd",
 )
 
 
@@ -75,6 +76,11 @@ class Dims(C.Structure):
                 ("scale", C.c_float)]
 
 
+class NormRope(C.Structure):
+    _fields_ = [("norm", C.c_int32), ("eps", C.c_float), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("w_dtype", C.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libfcp.so is not built ({LIB_PATH}); run __graft_entry__.build()")
@@ -112,6 +118,11 @@ def _load():
         "fcp_round_bf16": (C.c_int, [vp, i64, vp, vp]),
         "fcp_merge_ring": (C.c_int, [C.POINTER(DevPlan), vp, vp, C.POINTER(C.c_int32), i32, i32, i32, vp, vp,
                                      vp]),
+        "fcp_qk_norm_rope": (C.c_int, [vp, i64, vp, i64, vp, i64, vp, vp, vp, C.POINTER(NormRope), C.POINTER(DevPlan),
+                                       i32, Dims, vp, vp, vp, vp]),
+        "fcp_qk_norm_rope_bwd": (C.c_int, [vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, C.POINTER(NormRope),
+                                           C.POINTER(DevPlan), i32, Dims, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64,
+                                           vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -457,6 +468,115 @@ def attn_bwd(q, k, v, kbuf, vbuf, out, lse, dout, dplan: DevicePlan, shard: int,
                              _ptr(lse), _ptr(dout), C.byref(dplan.c), shard, dm, _ptr(dq), _ptr(dk),
                              _ptr(dv), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
            "fcp_attn_bwd")
+
+
+# ------------------------------------------------- head norm and rotation
+
+
+def _on(*tensors):
+    """Makes the tensors' device the current one for a call (the library
+    launches on the current device); all tensors on that device."""
+    import torch
+    dev = next(t for t in tensors if t is not None).device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return torch.cuda.device(dev)
+
+
+def _rows(t, name, T, heads, d):
+    """A bf16 [T][heads][d] tensor whose rows of heads * d values are contiguous
+    and `stride` elements apart (a slice of a fused projection): the stride."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d or heads not in (None, t.shape[1]):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, heads, d)}")
+    n = t.shape[1] * d
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    stride = n if T == 1 else t.stride(0)
+    if stride % 8 or stride < n:
+        raise ValueError(f"{name}: row stride {stride}, expected a multiple of 8 of at least {n}")
+    return stride
+
+
+def _norm_rope_opts(wq, wk, inv_freq, d, norm, eps, interleaved):
+    import torch
+    for t, n in ((wq, "wq"), (wk, "wk")):
+        if t is not None:
+            _t(t, n, (torch.bfloat16, torch.float32), (d,))
+    if wq is not None and wk is not None and wq.dtype != wk.dtype:
+        raise ValueError(f"wq and wk: dtypes {wq.dtype} and {wk.dtype}, expected one for both")
+    w = wq if wq is not None else wk
+    rot = 0
+    if inv_freq is not None:
+        _t(inv_freq, "inv_freq", (torch.float32,), (None,))
+        rot = 2 * inv_freq.numel()
+    return NormRope(int(norm), eps, rot, int(interleaved), OUT_BF16 if w is not None and w.dtype == torch.bfloat16 else OUT_F32)
+
+
+def qk_norm_rope(q_in, k_in, v_in, dplan: DevicePlan, shard: int, q, k, v, wq=None, wk=None, inv_freq=None,
+                 norm: bool = True, eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """fcp_qk_norm_rope: q, k, v (contiguous) = the heads of q_in and k_in
+    normed and turned by their document positions, and v_in's rows; the inputs
+    may be slices of a fused projection. inv_freq (fp32, rot_dim / 2 values)
+    None: no rotation. v_in and v may be None."""
+    import torch
+    _t(q, "q", (torch.bfloat16,), (None, None, None))
+    T, hq, d = q.shape
+    _t(k, "k", (torch.bfloat16,), (T, None, d))
+    hkv = k.shape[1]
+    sq, sk = _rows(q_in, "q_in", T, hq, d), _rows(k_in, "k_in", T, hkv, d)
+    if (v_in is None) != (v is None):
+        raise ValueError("v_in and v: both or neither")
+    sv = 0
+    if v is not None:
+        _t(v, "v", (torch.bfloat16,), (T, hkv, d))
+        sv = _rows(v_in, "v_in", T, hkv, d)
+    nr = _norm_rope_opts(wq, wk, inv_freq, d, norm, eps, interleaved)
+    with _on(q, k, v, q_in, k_in, v_in, wq, wk, inv_freq):
+        _check(_lib.fcp_qk_norm_rope(_ptr(q_in), sq, _ptr(k_in), sk, _ptr(v_in), sv, _ptr(wq), _ptr(wk), _ptr(inv_freq),
+                                     C.byref(nr), C.byref(dplan.c), shard, Dims(T, hq, hkv, d, 0.0), _ptr(q), _ptr(k),
+                                     _ptr(v), _stream(stream)), "fcp_qk_norm_rope")
+
+
+def qk_norm_rope_bwd(dq, dk, dv, q_in, k_in, dplan: DevicePlan, shard: int, dq_in, dk_in, dv_in, dwq, dwk, ws, wq=None,
+                     wk=None, inv_freq=None, norm: bool = True, eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """fcp_qk_norm_rope_bwd: from the attention's fp32 dq, dk, dv the bf16
+    gradients of qk_norm_rope's inputs (dq_in, dk_in, dv_in may be slices of one
+    fused gradient); dwq and dwk (fp32 [d]) are accumulated."""
+    import torch
+    _t(dq, "dq", (torch.float32,), (None, None, None))
+    T, hq, d = dq.shape
+    _t(dk, "dk", (torch.float32,), (T, None, d))
+    hkv = dk.shape[1]
+    sq = sk = sdv = 0
+    if norm:
+        sq, sk = _rows(q_in, "q_in", T, hq, d), _rows(k_in, "k_in", T, hkv, d)
+    else:
+        q_in = k_in = None
+    sdq, sdk = _rows(dq_in, "dq_in", T, hq, d), _rows(dk_in, "dk_in", T, hkv, d)
+    if (dv_in is None) != (dv is None):
+        raise ValueError("dv and dv_in: both or neither")
+    if dv is not None:
+        _t(dv, "dv", (torch.float32,), (T, hkv, d))
+        sdv = _rows(dv_in, "dv_in", T, hkv, d)
+    for t, n in ((dwq, "dwq"), (dwk, "dwk")):
+        if t is not None:
+            _t(t, n, (torch.float32,), (d,))
+    _t(ws, "ws")
+    nr = _norm_rope_opts(wq, wk, inv_freq, d, norm, eps, interleaved)
+    with _on(dq, dk, dv, q_in, k_in, dq_in, dk_in, dv_in, dwq, dwk, ws, wq, wk, inv_freq):
+        _check(_lib.fcp_qk_norm_rope_bwd(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(q_in), sq, _ptr(k_in), sk, _ptr(wq),
+                                         _ptr(wk), _ptr(inv_freq), C.byref(nr), C.byref(dplan.c), shard,
+                                         Dims(T, hq, hkv, d, 0.0), _ptr(dq_in), sdq, _ptr(dk_in), sdk, _ptr(dv_in), sdv,
+                                         _ptr(dwq), _ptr(dwk), _ptr(ws), ws.numel() * ws.element_size(),
+                                         _stream(stream)), "fcp_qk_norm_rope_bwd")
 
 
 def device_status(ws, stream=None) -> int:

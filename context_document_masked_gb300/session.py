@@ -109,5 +109,41 @@ class CPAttention:
                      self.ws, scale=self.scale, stream=stream)
         return dq, dk, dv
 
+    def qk_norm_rope(self, q_in, k_in, v_in=None, wq=None, wk=None, inv_freq=None, norm: bool = True,
+                     eps: float = 1e-6, interleaved: bool = False, shard: int = -1, q=None, k=None, v=None, stream=None):
+        """Q, K (and V) for the attention from a layer's projection: every query
+        and key head normed (weights wq, wk) and turned by its position inside
+        its document (inv_freq; None: not turned). The inputs are [T][heads][d]
+        tensors or slices of one fused tensor."""
+        if q is None:
+            q = torch.empty(self.T, self.hq, self.d, dtype=torch.bfloat16, device=self.device)
+        if k is None:
+            k = torch.empty(self.T, self.hkv, self.d, dtype=torch.bfloat16, device=self.device)
+        if v is None and v_in is not None:
+            v = torch.empty_like(k)
+        fcp.qk_norm_rope(q_in, k_in, v_in, self.dplan, shard, q, k, v, wq=wq, wk=wk, inv_freq=inv_freq, norm=norm,
+                         eps=eps, interleaved=interleaved, stream=stream)
+        return q, k, v
+
+    def qk_norm_rope_backward(self, dq, dk, dv, q_in, k_in, wq=None, wk=None, inv_freq=None, norm: bool = True,
+                              eps: float = 1e-6, interleaved: bool = False, shard: int = -1, dq_in=None, dk_in=None,
+                              dv_in=None, dwq=None, dwk=None, stream=None):
+        """Gradient of qk_norm_rope from backward()'s dq, dk and dv (None: no V):
+        the bf16 gradients of its inputs, written into dq_in, dk_in and dv_in
+        (slices of one fused gradient, for instance) or new tensors, and the fp32
+        gradients of the weights, added to dwq and dwk where they are given."""
+        def rows(heads):
+            return torch.empty(self.T, heads, self.d, dtype=torch.bfloat16, device=self.device)
+        dq_in = rows(self.hq) if dq_in is None else dq_in
+        dk_in = rows(self.hkv) if dk_in is None else dk_in
+        dv_in = rows(self.hkv) if dv_in is None and dv is not None else dv_in
+        if dwq is None and wq is not None:
+            dwq = torch.zeros(self.d, dtype=torch.float32, device=self.device)
+        if dwk is None and wk is not None:
+            dwk = torch.zeros(self.d, dtype=torch.float32, device=self.device)
+        fcp.qk_norm_rope_bwd(dq, dk, dv, q_in, k_in, self.dplan, shard, dq_in, dk_in, dv_in, dwq, dwk, self.ws, wq=wq,
+                             wk=wk, inv_freq=inv_freq, norm=norm, eps=eps, interleaved=interleaved, stream=stream)
+        return dq_in, dk_in, dv_in, dwq, dwk
+
     def device_status(self) -> int:
         return fcp.device_status(self.ws)

@@ -220,7 +220,8 @@ typedef struct {
  * of Q, K and the received K rows with their scales (fcp_attn_fwd_qk8), the
  * backward's row statistics D_i = <dO_i, O_i> ([Hq][T] fp32), fp16 copies of
  * Q and dO ([T][Hq][d] each, the backward's tensor-core operands) and of V and
- * the plan's received V rows (the forward's P*V operands). The caller
+ * the plan's received V rows (the forward's P*V operands), and the partial
+ * sums of the norm weights' gradients (fcp_qk_norm_rope_bwd). The caller
  * zero-fills a new workspace once before its first call: the error word must
  * start at zero (fcp_get_device_status clears it after reporting an error),
  * and a one-shard backward reads the fp16 Q and dO rows of whole 128-row
@@ -384,6 +385,69 @@ int fcp_attn_bwd(const void* q, const void* k, const void* v, const void* kbuf,
                  const void* vbuf, const void* out, int32_t out_dtype, const float* lse,
                  const void* dout, const fcp_dev_plan* plan, int32_t shard, fcp_dims dims,
                  float* dq, float* dk, float* dv, void* ws, int64_t ws_bytes, void* stream);
+
+/* Options of the head norm and rotation. */
+typedef struct {
+  int32_t norm;         /* 1: RMS norm of every query and key head; 0: rotation alone         */
+  float eps;            /* added to the mean square, >= 0 (norm = 1)                          */
+  int32_t rot_dim;      /* leading dimensions of a head that turn: 0, 16, 32, ... up to d     */
+  int32_t interleaved;  /* pairs of dimensions: 0 (i, i + rot_dim/2), 1 (2i, 2i + 1)          */
+  int32_t w_dtype;      /* type of wq and wk: FCP_OUT_BF16 or FCP_OUT_F32                     */
+} fcp_norm_rope;
+
+/*
+ * fcp_qk_norm_rope -- norm and rotation of the query and key heads before the
+ * attention, at the positions of a packed sequence ([CPGuide] "RoPE and
+ * position_ids follow the sharding": a shard's tokens keep their own
+ * positions; here a token's position is its index inside its document, taken
+ * from the plan). For every token t of the shard (of all shards for shard ==
+ * -1) and every head x of its query and key rows:
+ *   n = x / sqrt(mean(x^2) + eps) * w           (norm = 1; else n = x)
+ *   y = n with pair i of its first rot_dim dimensions turned by the angle
+ *       (t - start of t's document) * inv_freq[i].
+ * Sums, norm and rotation are in fp32, angles exact to fp32 at any position;
+ * y is rounded to bf16 once.
+ *   q_in, k_in, v_in  bf16 rows of hq, hkv and hkv heads of d values, row t at
+ *             t * stride elements (the slices of a fused projection, for
+ *             instance): strides multiples of 8 and at least the row's length.
+ *             v_in and v may both be NULL; V rows are copied as they are.
+ *   wq, wk    [d] norm weights of type w_dtype, or NULL for ones (norm = 0
+ *             needs NULL).
+ *   inv_freq  fp32 [rot_dim / 2], radians a position, finite (rot_dim > 0).
+ *   q, k, v   contiguous bf16 [T][hq][d] and [T][hkv][d], as the attention
+ *             calls read them; written only at the shard's rows. q may be
+ *             q_in itself where that is contiguous (and k, v likewise); no
+ *             other overlap of an output with an input or an output.
+ * Errors, before any launch: FCP_ERR_INVALID_ARG (also an overlap),
+ * FCP_ERR_UNSUPPORTED (d, heads, rot_dim not a multiple of 16).
+ */
+int fcp_qk_norm_rope(const void* q_in, int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
+                     int64_t v_stride, const void* wq, const void* wk, const float* inv_freq,
+                     const fcp_norm_rope* nr, const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, void* q, void* k,
+                     void* v, void* stream);
+
+/*
+ * fcp_qk_norm_rope_bwd -- gradient of fcp_qk_norm_rope, from the fp32
+ * gradients that fcp_attn_bwd writes. With r = 1 / sqrt(mean(x^2) + eps), z
+ * the gradient of y turned back, g = z w:
+ *   dx = r (g - x r^2 mean(g x)),  dw = sum over the shard's tokens and heads of z x r.
+ *   dq, dk, dv  fp32, contiguous [T][hq][d] and [T][hkv][d]; dv and dv_in may
+ *             both be NULL.
+ *   q_in, k_in  the forward's inputs with their strides (norm = 1; unused and
+ *             may be NULL for norm = 0).
+ *   dq_in, dk_in, dv_in  bf16 rows with their own strides (elements), as
+ *             q_in; written only at the shard's rows. dq_in may be q_in itself
+ *             (same stride), dk_in k_in; no other overlap.
+ *   dwq, dwk  fp32 [d], ACCUMULATED (+=), or NULL. Summed in a fixed order:
+ *             equal inputs give equal bits.
+ *   ws        workspace of fcp_workspace_bytes(dims, plan) bytes.
+ * Errors as fcp_qk_norm_rope; FCP_ERR_CAPACITY if the workspace is too small.
+ */
+int fcp_qk_norm_rope_bwd(const float* dq, const float* dk, const float* dv, const void* q_in, int64_t q_stride,
+                         const void* k_in, int64_t k_stride, const void* wq, const void* wk, const float* inv_freq,
+                         const fcp_norm_rope* nr, const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, void* dq_in,
+                         int64_t dq_stride, void* dk_in, int64_t dk_stride, void* dv_in, int64_t dv_stride, float* dwq,
+                         float* dwk, void* ws, int64_t ws_bytes, void* stream);
 
 /* Size of the device array that fcp_attn_fwd_noalloc uses as its scratch. */
 #define FCP_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)

@@ -9,4 +9,6 @@ Modules:
              plain definitions (numpy).
   plan       the sharding policies (Llama3 2xCP, Per-Doc, Whole-Doc, hybrid
              Algorithm 1), the workload model and the communication volumes.
+  positions  head norm with rotation by document positions, attention with a
+             bucketed distance bias, and their gradients.
 """
