@@ -335,6 +335,26 @@ int fcp_gather_kv(const void* k, const void* v, const fcp_dev_plan* plan, int32_
                             static_cast<cudaStream_t>(stream));
 }
 
+// The table's pointer and the bucket starts (host): the first distance of the
+// first bucket is 0 and none is below the one before.
+static int check_bias(const fcp_rel_bias* b) {
+  if (!b || !b->bias || !b->starts || (reinterpret_cast<uintptr_t>(b->bias) & 3)) return FCP_ERR_INVALID_ARG;
+  if (b->n_buckets < 1) return FCP_ERR_INVALID_ARG;
+  if (b->n_buckets > FCP_MAX_BUCKETS) return FCP_ERR_UNSUPPORTED;
+  if (b->starts[0] != 0) return FCP_ERR_INVALID_ARG;
+  for (int32_t u = 1; u < b->n_buckets; ++u)
+    if (b->starts[u] < b->starts[u - 1]) return FCP_ERR_INVALID_ARG;
+  return FCP_OK;
+}
+
+static void set_bias(fcp::BiasParams* p, const fcp_rel_bias* b, float* dbias) {
+  static_assert(FCP_MAX_BUCKETS == fcp::kMaxBuckets, "bucket count");
+  p->bias = b->bias;
+  p->dbias = dbias;
+  p->n = b->n_buckets;
+  std::copy(b->starts, b->starts + b->n_buckets, p->starts);
+}
+
 // Forward over the plan's gathered key layout (ring < -1: own rows from K/V,
 // received rows from kbuf/vbuf) or in ring order (ring >= -1: every needed key
 // from its owner's rows of K/V, owners visited by ring distance; ring = -1 all
@@ -342,7 +362,8 @@ int fcp_gather_kv(const void* k, const void* v, const fcp_dev_plan* plan, int32_
 static int attn_fwd_impl(const void* q, const void* k, const void* v, const void* kbuf, const void* vbuf,
                          const fcp_dev_plan* plan, int32_t shard, int32_t kv_lo, int32_t kv_hi,
                          fcp_dims dims, int32_t out_dtype, void* out, float* lse, void* ws,
-                         int64_t ws_bytes, void* stream, int32_t ring, bool qk8 = false) {
+                         int64_t ws_bytes, void* stream, int32_t ring, bool qk8 = false,
+                         const fcp_rel_bias* bias = nullptr) {
   const bool ring_order = ring >= -1;
   int st = check_dev_plan(plan, shard);
   if (st) return st;
@@ -438,6 +459,7 @@ static int attn_fwd_impl(const void* q, const void* k, const void* v, const void
   fp.wait_ns = g_wait_ns;
   a.d = dims.d;
   a.num_sms = num_sms();
+  if ((a.has_bias = bias != nullptr)) set_bias(&a.bias, bias, nullptr);
   return fcp::launch_attn_fwd(a, cs);
 }
 
@@ -454,6 +476,31 @@ int fcp_attn_fwd_qk8(const void* q, const void* k, const void* v, const void* kb
                      int32_t out_dtype, void* out, float* lse, void* ws, int64_t ws_bytes, void* stream) {
   return attn_fwd_impl(q, k, v, kbuf, vbuf, plan, shard, kv_lo, kv_hi, dims, out_dtype, out, lse, ws,
                        ws_bytes, stream, -2, true);
+}
+
+int fcp_attn_fwd_bias(const void* q, const void* k, const void* v, const void* kbuf, const void* vbuf,
+                      const fcp_rel_bias* bias, const fcp_dev_plan* plan, int32_t shard, int32_t kv_lo, int32_t kv_hi,
+                      fcp_dims dims, int32_t out_dtype, void* out, float* lse, void* ws, int64_t ws_bytes,
+                      void* stream) {
+  const int st = check_bias(bias);
+  if (st) return st;
+  return attn_fwd_impl(q, k, v, kbuf, vbuf, plan, shard, kv_lo, kv_hi, dims, out_dtype, out, lse, ws, ws_bytes, stream,
+                       -2, false, bias);
+}
+
+int fcp_rel_buckets(int32_t n_buckets, int32_t max_distance, int32_t* starts) {
+  if (!starts || n_buckets < 2) return FCP_ERR_INVALID_ARG;
+  if (n_buckets > FCP_MAX_BUCKETS) return FCP_ERR_UNSUPPORTED;
+  const int32_t exact = n_buckets / 2, far = n_buckets - exact;
+  if (max_distance <= exact) return FCP_ERR_INVALID_ARG;
+  for (int32_t u = 0; u < n_buckets; ++u) {
+    // The smallest distance x with floor(far ln(x / exact) / ln(max / exact)) >= u - exact.
+    const double x = u <= exact ? u : exact * std::pow((double)max_distance / exact, (double)(u - exact) / far);
+    const double near = std::nearbyint(x);  // a distance that the power meets but for its rounding
+    starts[u] = (int32_t)(std::fabs(x - near) <= 1e-9 * x ? near : std::ceil(x));
+    if (u > 0) starts[u] = std::max(starts[u], starts[u - 1]);
+  }
+  return FCP_OK;
 }
 
 int fcp_quant_e4m3(const void* x, int64_t n, void* out, float* scale_out, void* scratch, void* stream) {
@@ -511,10 +558,11 @@ int fcp_merge_ring(const fcp_dev_plan* plan, const float* o_parts, const float* 
   return fcp_merge(o_parts, lse_parts, B, plan->T, hq, d, out, lse_out, stream);
 }
 
-int fcp_attn_bwd(const void* q, const void* k, const void* v, const void* kbuf, const void* vbuf,
-                 const void* out, int32_t out_dtype, const float* lse, const void* dout,
-                 const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, float* dq, float* dk,
-                 float* dv, void* ws, int64_t ws_bytes, void* stream) {
+static int attn_bwd_impl(const void* q, const void* k, const void* v, const void* kbuf, const void* vbuf,
+                         const void* out, int32_t out_dtype, const float* lse, const void* dout,
+                         const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, float* dq, float* dk,
+                         float* dv, void* ws, int64_t ws_bytes, void* stream, const fcp_rel_bias* bias,
+                         float* dbias) {
   int st = check_dev_plan(plan, shard);
   if (st) return st;
   const Plan* p = plan->host;
@@ -591,7 +639,27 @@ int fcp_attn_bwd(const void* q, const void* k, const void* v, const void* kbuf, 
   bp.wait_ns = g_wait_ns;
   a.d = dims.d;
   a.num_sms = num_sms();
+  if ((a.has_bias = bias != nullptr)) set_bias(&a.bias, bias, dbias);
   return fcp::launch_attn_bwd(a, s);
+}
+
+int fcp_attn_bwd(const void* q, const void* k, const void* v, const void* kbuf, const void* vbuf,
+                 const void* out, int32_t out_dtype, const float* lse, const void* dout,
+                 const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, float* dq, float* dk,
+                 float* dv, void* ws, int64_t ws_bytes, void* stream) {
+  return attn_bwd_impl(q, k, v, kbuf, vbuf, out, out_dtype, lse, dout, plan, shard, dims, dq, dk, dv, ws, ws_bytes, stream,
+                       nullptr, nullptr);
+}
+
+int fcp_attn_bwd_bias(const void* q, const void* k, const void* v, const void* kbuf, const void* vbuf,
+                      const fcp_rel_bias* bias, const void* out, int32_t out_dtype, const float* lse, const void* dout,
+                      const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, float* dq, float* dk, float* dv,
+                      float* dbias, void* ws, int64_t ws_bytes, void* stream) {
+  const int st = check_bias(bias);
+  if (st) return st;
+  if (!dbias || (reinterpret_cast<uintptr_t>(dbias) & 3)) return FCP_ERR_INVALID_ARG;
+  return attn_bwd_impl(q, k, v, kbuf, vbuf, out, out_dtype, lse, dout, plan, shard, dims, dq, dk, dv, ws, ws_bytes, stream,
+                       bias, dbias);
 }
 
 // Rows of a strided operand: T rows of `len` bytes, `stride` bytes apart.

@@ -43,6 +43,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
+#include "bias.cuh"
 #include "kernels.h"
 #include "sm103.cuh"
 
@@ -167,14 +170,16 @@ __device__ __forceinline__ bool drain_group_all(bool ok) {
   return out != 0;
 }
 
-template <int D>
+template <int D, class Bias>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_kb, const __grid_constant__ CUtensorMap tm_vb,
                     const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
-                    const __grid_constant__ CUtensorMap tm_dv, const BwdParams p) {
+                    const __grid_constant__ CUtensorMap tm_dv, const BwdParams p,
+                    const __grid_constant__ Bias bp) {
   using C = BwdCfg<D>;
+  constexpr bool kBias = std::is_same_v<Bias, BiasParams>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar_kv_full, bar_kv_conv, bar_kv_empty, bar_drain;
   __shared__ __align__(8) uint64_t bar_q_full[2], bar_q_empty[2], bar_do_full, bar_do_empty;
@@ -184,8 +189,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ WorkRing<4> ring;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
+  __shared__ int bias_starts[kBias ? kMaxBuckets : 1];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if constexpr (kBias) {
+    if (tid < bp.n) bias_starts[tid] = bp.starts[tid];
+  }
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need 1024-byte alignment
     if (tid == 0) atomicOr(p.err, 2);
     return;
@@ -247,7 +256,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kv_items = 0, qc = 0, dc = 0;
     uint32_t issued_q[2] = {0, 0};
     bool ok = true;
-    const float kLog2e = 1.4426950408889634f;
     uint32_t k = 0;
     for (int w = blockIdx.x; ok;) {
       if (lane == 0) ok = ring.put(k, w, wc);
@@ -306,7 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool valid = r < q_rows;
           // Stored negated (-LSE log2 e, -D): the compute warps add them with
           // packed f32x2 arithmetic. Rows past the piece get P = 0.
-          st[r] = valid ? -__ldg(p.lse + (size_t)h * p.T + q0 + r) * kLog2e : -INFINITY;
+          if constexpr (kBias) {  // a row whose buckets are all masked (LSE = -inf) gets P = 0 too
+            const float lse = valid ? __ldg(p.lse + (size_t)h * p.T + q0 + r) : -INFINITY;
+            st[r] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+          } else {
+            st[r] = valid ? -__ldg(p.lse + (size_t)h * p.T + q0 + r) * kLog2e : -INFINITY;
+          }
           st[128 + r] = valid ? -__ldg(p.delta + (size_t)h * p.T + q0 + r) : 0.f;
         }
         __syncwarp();
@@ -485,9 +498,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nsteps = G * it.nq;
       const bool key_valid = kr < it.n;
       const int key = it.key0 + kr;
+      BucketRun run{0, 0, 0, 0.f};  // the bucket of the tiles far from the diagonal
+      float run_sum = 0.f;          // this lane's dS in that bucket
+      int run_head = 0;
       for (int j = 0; j < nsteps; ++j, ++gstep) {
         const uint32_t c = qc + j, s = c & 1;
-        const int q0 = step_rows(it, G, j).q0;
+        const StepRows sr = step_rows(it, G, j);
+        const int q0 = sr.q0;
+        // Bias of the 32 keys x 64 queries of this warp: distance of element
+        // (lane, e) is base + 31 + e - lane; entry x of the window has base + x.
+        const int base = q0 + 64 * half - it.key0 - 32 * (warp & 3) - 31;
+        bool spread = false, below = true;  // below: some of the distances are >= 0
+        float win[kBias ? 3 : 1];
+        if constexpr (kBias) {
+          below = base + 94 >= 0;
+          if (below) {
+            const float* bias_row = bp.bias + (size_t)sr.h * bp.n;
+            const int near = max(base, 0);
+            if (run_head != sr.h || near < run.lo || near >= run.hi) {
+              add_run(bp.dbias + (size_t)run_head * bp.n + run.bucket, run_sum, lane);
+              run_head = sr.h;
+              bucket_run(run, bias_starts, bp.n, bias_row, near);
+            }
+            spread = base + 94 >= run.hi;
+            if (spread) {
+#pragma unroll
+              for (int w3 = 0; w3 < 3; ++w3) {
+                const int dist = base + lane + 32 * w3;
+                win[w3] = dist >= 0 ? bias_log2(bias_row, bucket_of(bias_starts, bp.n, dist)) : 0.f;
+              }
+            }
+          }
+        }
         const int lim = key - q0 - 64 * half;  // local columns below lim cannot see this key
         // Whole tile below the diagonal with 128 keys: no element needs a mask
         // (query rows past the piece end have LSE = +inf, hence P = 0).
@@ -507,7 +549,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             const float* v = e < 32 ? va + e : vb + (e - 32);
-            const float4 l4 = st4[e >> 2];  // -LSE log2 e of the four query columns
+            float4 l4 = st4[e >> 2];  // -LSE log2 e of the four query columns
+            if constexpr (kBias) {
+              if (spread) {
+                l4.x += window_at(win, e, lane);
+                l4.y += window_at(win, e + 1, lane);
+                l4.z += window_at(win, e + 2, lane);
+                l4.w += window_at(win, e + 3, lane);
+              } else {
+                l4.x += run.value;
+                l4.y += run.value;
+                l4.z += run.value;
+                l4.w += run.value;
+              }
+            }
             float p0, p1, p2, p3;
             f2_split(f2_fma(f2(v[0], v[1]), c2, f2(l4.x, l4.y)), p0, p1);
             f2_split(f2_fma(f2(v[2], v[3]), c2, f2(l4.z, l4.w)), p2, p3);
@@ -569,8 +624,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&bar_ds_ready);
+        // The bias's gradient: sums of the dS just stored, this lane's own row
+        // read back (fp16, the operands of the dK and dQ products) and added
+        // in fp32, after the MMA thread has been let go on.
+        if constexpr (kBias) {
+          if (below) {
+            float diag[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+              uint32_t d[4];
+              ld_shared_v4(ds_panel + sw128_offset(kr, ch), d);
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&d[u]));
+                if (spread) {
+                  window_add(diag, ch * 8 + 2 * u, lane, x.x);
+                  window_add(diag, ch * 8 + 2 * u + 1, lane, x.y);
+                } else {
+                  run_sum += x.x + x.y;
+                }
+              }
+            }
+            if (spread) {
+              float* row = bp.dbias + (size_t)sr.h * bp.n;
+#pragma unroll
+              for (int w3 = 0; w3 < 3; ++w3) {
+                const int dist = base + lane + 32 * w3;
+                add_by_bucket(row, dist >= 0 ? bucket_of(bias_starts, bp.n, dist) : 0, diag[w3], lane);
+              }
+            }
+          }
+        }
       }
       if (!ok) break;
+      if constexpr (kBias) add_run(bp.dbias + (size_t)run_head * bp.n + run.bucket, run_sum, lane);
       qc += nsteps;
       // dV (columns-0 group) or dK (columns-64 group) of this key tile ->
       // global rows: 32-column chunks staged in this group's half of the dS
@@ -715,14 +802,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-template <int D>
-static int launch_bwd_impl(const BwdLaunch& a, cudaStream_t st) {
+template <int D, class Bias>
+static int launch_bwd_impl(const BwdLaunch& a, const Bias& bias, cudaStream_t st) {
   using C = BwdCfg<D>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(attn_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(attn_bwd_kernel<D, Bias>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmem) != cudaSuccess)
       return FCP_ERR_CUDA;
     attr_set[dev] = true;
@@ -734,14 +821,14 @@ static int launch_bwd_impl(const BwdLaunch& a, cudaStream_t st) {
   // together stream the same query rows (Q, dO, dQ) of that head group.
   BwdParams p = a.p;
   p.order_block = grid;
-  attn_bwd_kernel<D><<<grid, kThreads, C::kSmem, st>>>(a.tm_q, a.tm_do, a.tm_k, a.tm_v, a.tm_kb,
-                                                      a.tm_vb, a.tm_dq, a.tm_dk, a.tm_dv, p);
+  attn_bwd_kernel<D, Bias><<<grid, kThreads, C::kSmem, st>>>(a.tm_q, a.tm_do, a.tm_k, a.tm_v, a.tm_kb,
+                                                      a.tm_vb, a.tm_dq, a.tm_dk, a.tm_dv, p, bias);
   return cudaGetLastError() == cudaSuccess ? FCP_OK : FCP_ERR_CUDA;
 }
 
 int launch_attn_bwd(const BwdLaunch& a, cudaStream_t st) {
-  if (a.d == 128) return launch_bwd_impl<128>(a, st);
-  if (a.d == 64) return launch_bwd_impl<64>(a, st);
+  if (a.d == 128) return a.has_bias ? launch_bwd_impl<128>(a, a.bias, st) : launch_bwd_impl<128>(a, NoBias{}, st);
+  if (a.d == 64) return a.has_bias ? launch_bwd_impl<64>(a, a.bias, st) : launch_bwd_impl<64>(a, NoBias{}, st);
   return FCP_ERR_UNSUPPORTED;
 }
 

@@ -40,6 +40,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
+#include "bias.cuh"
 #include "kernels.h"
 #include "sm103.cuh"
 
@@ -190,12 +193,13 @@ __device__ __forceinline__ WorkItem decode(const FwdParams& p, int w) {
   return it;
 }
 
-template <int D, bool QK8, bool ODD>
+template <int D, bool QK8, bool ODD, class Bias>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kb,
-                    const __grid_constant__ CUtensorMap tm_vb, const FwdParams p) {
+                    const __grid_constant__ CUtensorMap tm_vb, const FwdParams p, const __grid_constant__ Bias bp) {
   using C = FwdCfg<D>;
+  constexpr bool kBias = std::is_same_v<Bias, BiasParams>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -205,10 +209,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ WorkRing<4> ring;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
+  __shared__ int bias_starts[kBias ? kMaxBuckets : 1];
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
+  if constexpr (kBias) {
+    if (tid < bp.n) bias_starts[tid] = bp.starts[tid];
+  }
 
   if (tid == 0) {
     mbar_init(&bar_q_full, 1);
@@ -425,12 +433,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool row_valid = r < it.q_rows;
       int head = it.h0 + i;
       float m_run = -INFINITY, l = 0.f;
+      const float* bias_row = nullptr;
+      const int q_warp = it.q_start + 32 * (warp & 3);  // this warp's first row
+      BucketRun run{0, 0, 0, 0.f};
+      if constexpr (kBias) bias_row = bp.bias + (size_t)(i ? it.h1 : it.h0) * bp.n;
       if (nt > 0) {
         Walker wk;
         wk.init(p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.kbuf_shift, p.seg_filter);
         int src, row, key, n;
         for (int t = 0; t < nt; ++t) {
           wk.next(src, row, key, n);
+          // Bias of the tile: one bucket for all the warp's visible
+          // distances, or the window of entries this lane keeps.
+          bool spread = false;
+          float win[kBias ? 5 : 1];
+          if constexpr (kBias) {
+            const int far = q_warp + 31 - key, near = max(q_warp - key - 127, 0);
+            if (far >= 0) {
+              if (near < run.lo || near >= run.hi) bucket_run(run, bias_starts, bp.n, bias_row, near);
+              spread = far >= run.hi;
+              if (spread) {
+#pragma unroll
+                for (int w5 = 0; w5 < 5; ++w5) {
+                  const int dist = q_warp - key - 127 + lane + 32 * w5;
+                  win[w5] = dist >= 0 ? bias_log2(bias_row, bucket_of(bias_starts, bp.n, dist)) : 0.f;
+                }
+              }
+            }
+          }
           ok = mbar_wait_inline(&bar_s_full[i], s_cnt & 1, wc);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           ++s_cnt;
@@ -444,6 +474,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j) s[c * 32 + j] = v[j];
           }
           tmem_ld_wait();
+          // The scores' factor and addend to log2 units: the tile's bucket, or
+          // 1 and 0 where the window's biases are added element by element.
+          float mul = scale_log2, add = 0.f;
+          if constexpr (kBias) {
+            add = run.value;
+            if (spread) {
+              mul = 1.f;
+              add = 0.f;
+#pragma unroll
+              for (int c = 0; c < 128; ++c) {  // window entry lane + 127 - c
+                const int k0 = (127 - c) >> 5, r0 = (127 - c) & 31;
+                const float mine = lane >= r0 ? win[k0] : win[k0 + 1];
+                s[c] = fmaf(s[c], scale_log2, __shfl_sync(0xffffffffu, mine, lane + 127 - c));
+              }
+            }
+          }
           if (key + 127 > it.q_start || n < 128) {
             const int lim = min(n, q - key + 1);  // keys [key, key+lim) are visible to row q
 #pragma unroll
@@ -460,8 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = j + 16; c < 128; c += 16) m = fmax3(m, s[c], s[c + 8]);
             mx8[j] = m;
           }
-          const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], fmax3(mx8[5], mx8[6], mx8[7]))) *
-                           scale_log2;
+          float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], fmax3(mx8[5], mx8[6], mx8[7]))) *
+                     mul;
+          if constexpr (kBias) mx += add;
           const float m_new = fmaxf(m_run, mx);
           const bool rescale = m_new > m_run + kRescaleThreshold;
           float alpha = 1.f;
@@ -473,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // P = exp2(s * scale * log2e - m): fp16 pairs straight into TMEM columns
           // [0, 64) of S_i, 64 score columns at a time. The scaling and the row
           // sum run on packed pairs; sums of column c go to accumulator c mod 8.
-          const uint64_t c2 = f2(scale_log2, scale_log2), nm2 = f2(-m_use, -m_use);
+          const uint64_t c2 = f2(mul, mul), nm2 = kBias ? f2(add - m_use, add - m_use) : f2(-m_use, -m_use);
           uint64_t rs2[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {  // 32 score columns -> 16 TMEM columns of P
@@ -588,14 +635,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-template <int D, bool QK8, bool ODD>
-static int launch_fwd_impl(const FwdLaunch& a, cudaStream_t st) {
+template <int D, bool QK8, bool ODD, class Bias>
+static int launch_fwd_impl(const FwdLaunch& a, const Bias& bias, cudaStream_t st) {
   using C = FwdCfg<D>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(attn_fwd_kernel<D, QK8, ODD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(attn_fwd_kernel<D, QK8, ODD, Bias>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::kSmemAlloc) != cudaSuccess)
       return FCP_ERR_CUDA;
     attr_set[dev] = true;
@@ -608,16 +655,22 @@ static int launch_fwd_impl(const FwdLaunch& a, cudaStream_t st) {
   FwdParams p = a.p;
   const int pairs_per_kv = head_pairs(p.hq, p.hkv) / p.hkv;
   p.order_block = grid / pairs_per_kv > 0 ? grid / pairs_per_kv : 1;
-  attn_fwd_kernel<D, QK8, ODD><<<grid, kThreads, C::kSmemAlloc, st>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_kb, a.tm_vb,
-                                                                p);
+  attn_fwd_kernel<D, QK8, ODD, Bias><<<grid, kThreads, C::kSmemAlloc, st>>>(a.tm_q, a.tm_k, a.tm_v, a.tm_kb, a.tm_vb,
+                                                                p, bias);
   return cudaGetLastError() == cudaSuccess ? FCP_OK : FCP_ERR_CUDA;
 }
 
 template <bool ODD>
 static int launch_fwd_any(const FwdLaunch& a, cudaStream_t st) {
-  if (a.qk8) return a.d == 128 ? launch_fwd_impl<128, true, ODD>(a, st) : FCP_ERR_UNSUPPORTED;
-  if (a.d == 128) return launch_fwd_impl<128, false, ODD>(a, st);
-  if (a.d == 64) return launch_fwd_impl<64, false, ODD>(a, st);
+  if (a.has_bias) {
+    if (a.qk8) return FCP_ERR_UNSUPPORTED;
+    if (a.d == 128) return launch_fwd_impl<128, false, ODD>(a, a.bias, st);
+    if (a.d == 64) return launch_fwd_impl<64, false, ODD>(a, a.bias, st);
+    return FCP_ERR_UNSUPPORTED;
+  }
+  if (a.qk8) return a.d == 128 ? launch_fwd_impl<128, true, ODD>(a, NoBias{}, st) : FCP_ERR_UNSUPPORTED;
+  if (a.d == 128) return launch_fwd_impl<128, false, ODD>(a, NoBias{}, st);
+  if (a.d == 64) return launch_fwd_impl<64, false, ODD>(a, NoBias{}, st);
   return FCP_ERR_UNSUPPORTED;
 }
 

@@ -48,12 +48,26 @@ struct FwdParams {
   int64_t wait_ns;
 };
 
+// Learned bias of the attention by buckets of the distance i - j: bucket u
+// holds the distances from starts[u] to starts[u + 1] - 1 (the last one all
+// from starts[u] on).
+constexpr int kMaxBuckets = 128;
+struct BiasParams {
+  const float* bias;       // [hq][n]
+  float* dbias;            // backward: [hq][n], accumulated
+  int32_t n;
+  int32_t starts[kMaxBuckets];
+};
+struct NoBias {};          // kernels without a bias take this in its place
+
 struct FwdLaunch {
   CUtensorMap tm_q, tm_k, tm_v, tm_kb, tm_vb;
   FwdParams p;
   int d;
   int num_sms;
   bool qk8;                // Q, K, received K as e4m3 (boxes of 128 bytes x 1 x 128)
+  bool has_bias;
+  BiasParams bias;
 };
 
 struct BwdParams {
@@ -84,6 +98,8 @@ struct BwdLaunch {
   BwdParams p;
   int d;
   int num_sms;
+  bool has_bias;
+  BiasParams bias;
 };
 
 int launch_attn_fwd(const FwdLaunch& a, cudaStream_t st);

@@ -29,8 +29,9 @@ EXPORTED = (
     "fcp_get_device_status", "fcp_debug_set_wait_limit", "fcp_attn_fwd_noalloc", "fcp_attn_fwd_ring",
     "fcp_attn_fwd_qk8", "fcp_quant_e4m3", "fcp_plan_device_image", "fcp_plan_bind",
     "fcp_debug_rescale_events", "fcp_round_bf16", "fcp_merge_ring", "fcp_qk_norm_rope",
-    "fcp_qk_norm_rope_bwd",
+    "fcp_qk_norm_rope_bwd", "fcp_rel_buckets", "fcp_attn_fwd_bias", "fcp_attn_bwd_bias",
 )
+MAX_BUCKETS = 128
 
 
 class FcpError(RuntimeError):
@@ -81,6 +82,10 @@ class NormRope(C.Structure):
                 ("w_dtype", C.c_int32)]
 
 
+class RelBias(C.Structure):
+    _fields_ = [("bias", C.c_void_p), ("starts", C.POINTER(C.c_int32)), ("n_buckets", C.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libfcp.so is not built ({LIB_PATH}); run __graft_entry__.build()")
@@ -118,6 +123,11 @@ def _load():
         "fcp_round_bf16": (C.c_int, [vp, i64, vp, vp]),
         "fcp_merge_ring": (C.c_int, [C.POINTER(DevPlan), vp, vp, C.POINTER(C.c_int32), i32, i32, i32, vp, vp,
                                      vp]),
+        "fcp_rel_buckets": (C.c_int, [i32, i32, C.POINTER(C.c_int32)]),
+        "fcp_attn_fwd_bias": (C.c_int, [vp, vp, vp, vp, vp, C.POINTER(RelBias), C.POINTER(DevPlan), i32, i32, i32, Dims,
+                                        i32, vp, vp, vp, i64, vp]),
+        "fcp_attn_bwd_bias": (C.c_int, [vp, vp, vp, vp, vp, C.POINTER(RelBias), vp, i32, vp, vp, C.POINTER(DevPlan), i32,
+                                        Dims, vp, vp, vp, vp, vp, i64, vp]),
         "fcp_qk_norm_rope": (C.c_int, [vp, i64, vp, i64, vp, i64, vp, vp, vp, C.POINTER(NormRope), C.POINTER(DevPlan),
                                        i32, Dims, vp, vp, vp, vp]),
         "fcp_qk_norm_rope_bwd": (C.c_int, [vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, C.POINTER(NormRope),
@@ -468,6 +478,72 @@ def attn_bwd(q, k, v, kbuf, vbuf, out, lse, dout, dplan: DevicePlan, shard: int,
                              _ptr(lse), _ptr(dout), C.byref(dplan.c), shard, dm, _ptr(dq), _ptr(dk),
                              _ptr(dv), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
            "fcp_attn_bwd")
+
+
+# ----------------------------------------------- bias by distance buckets
+
+
+def rel_buckets(n_buckets: int, max_distance: int) -> np.ndarray:
+    """fcp_rel_buckets: first distance of each bucket (int32), one distance a
+    bucket up to n_buckets // 2, then spaced by logarithms up to max_distance."""
+    out = np.zeros(max(1, n_buckets), dtype=np.int32)
+    _check(_lib.fcp_rel_buckets(n_buckets, max_distance, out.ctypes.data_as(C.POINTER(C.c_int32))), "fcp_rel_buckets")
+    return out
+
+
+def _rel_bias(bias, starts, hq):
+    """The C struct, and the host array it points to (kept for the call)."""
+    import torch
+    s = np.asarray(starts)
+    if s.ndim != 1 or s.size == 0 or not np.issubdtype(s.dtype, np.integer):
+        raise ValueError("starts: one whole number a bucket")
+    if s.min() < 0 or s.max() > np.iinfo(np.int32).max:
+        raise ValueError("starts: distances of 0 to 2^31 - 1")
+    s = np.ascontiguousarray(s, dtype=np.int32)
+    _t(bias, "bias", (torch.float32,), (hq, s.size))
+    return RelBias(_ptr(bias), s.ctypes.data_as(C.POINTER(C.c_int32)), s.size), s
+
+
+def attn_fwd_bias(q, k, v, kbuf, vbuf, bias, starts, dplan: DevicePlan, shard: int, out, lse, ws, kv_lo: int = 0,
+                  kv_hi: int | None = None, scale: float = 0.0, stream=None):
+    """fcp_attn_fwd_bias: attn_fwd with bias[h, bucket(i - j)] (fp32 [hq][n])
+    added to the scores; starts (host, n whole numbers) are the buckets' first
+    distances."""
+    import torch
+    T, hq, hkv, d = _qkv(q, k, v)
+    _kbuf(kbuf, vbuf, dplan, shard, hkv, d)
+    _out_lse(out, lse, T, hq, d)
+    _t(ws, "ws")
+    rb, keep = _rel_bias(bias, starts, hq)
+    out_dtype = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
+    with _on(q, k, v, kbuf, vbuf, bias, out, lse, ws):
+        _check(_lib.fcp_attn_fwd_bias(_ptr(q), _ptr(k), _ptr(v), _ptr(kbuf), _ptr(vbuf), C.byref(rb), C.byref(dplan.c),
+                                      shard, kv_lo, T if kv_hi is None else kv_hi, Dims(T, hq, hkv, d, scale), out_dtype,
+                                      _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+               "fcp_attn_fwd_bias")
+
+
+def attn_bwd_bias(q, k, v, kbuf, vbuf, bias, starts, out, lse, dout, dplan: DevicePlan, shard: int, dq, dk, dv, dbias, ws,
+                  scale: float = 0.0, stream=None):
+    """fcp_attn_bwd_bias: attn_bwd of attn_fwd_bias; dbias (fp32 [hq][n]) is
+    accumulated like dk and dv."""
+    import torch
+    T, hq, hkv, d = _qkv(q, k, v)
+    _kbuf(kbuf, vbuf, dplan, shard, hkv, d)
+    _out_lse(out, lse, T, hq, d)
+    _t(dout, "dout", (torch.bfloat16,), (T, hq, d))
+    _t(dq, "dq", (torch.float32,), (T, hq, d))
+    _t(dk, "dk", (torch.float32,), (T, hkv, d))
+    _t(dv, "dv", (torch.float32,), (T, hkv, d))
+    _t(ws, "ws")
+    rb, keep = _rel_bias(bias, starts, hq)
+    _t(dbias, "dbias", (torch.float32,), tuple(bias.shape))
+    out_dtype = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
+    with _on(q, k, v, kbuf, vbuf, bias, out, lse, dout, dq, dk, dv, dbias, ws):
+        _check(_lib.fcp_attn_bwd_bias(_ptr(q), _ptr(k), _ptr(v), _ptr(kbuf), _ptr(vbuf), C.byref(rb), _ptr(out),
+                                      out_dtype, _ptr(lse), _ptr(dout), C.byref(dplan.c), shard,
+                                      Dims(T, hq, hkv, d, scale), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(ws),
+                                      ws.numel() * ws.element_size(), _stream(stream)), "fcp_attn_bwd_bias")
 
 
 # ------------------------------------------------- head norm and rotation

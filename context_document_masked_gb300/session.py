@@ -11,6 +11,14 @@ import torch
 from . import fcp
 
 
+def _on_stream(stream):
+    """The stream of a call (a torch stream, a raw handle or None: the current
+    one) as a context: what torch does for the call runs in its order."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
 class CPAttention:
     def __init__(self, doclens, cp: int, policy: str, hq: int, hkv: int, d: int,
                  device="cuda", target_imbalance: float = 1.05, scale: float = 0.0):
@@ -93,6 +101,39 @@ class CPAttention:
                           stream=stream)
         return out, lse
 
+    def forward_bias(self, q, k, v, bias, starts, shard: int = -1, out=None, lse=None, kv_block=None,
+                     out_dtype=torch.bfloat16, stream=None):
+        """forward() with the learned bias[h, bucket(i - j)] (fp32 [hq][buckets])
+        added to the scores; starts: the buckets' first distances (host), for
+        instance fcp.rel_buckets(n, max_distance)."""
+        with _on_stream(stream):
+            if out is None:
+                out = torch.empty(self.T, self.hq, self.d, dtype=out_dtype, device=self.device)
+            if lse is None:
+                lse = torch.empty(self.hq, self.T, dtype=torch.float32, device=self.device)
+        lo, hi = (0, self.T) if kv_block is None else kv_block
+        fcp.attn_fwd_bias(q, k, v, self.kbuf, self.vbuf, bias, starts, self.dplan, shard, out, lse, self.ws, kv_lo=lo,
+                          kv_hi=hi, scale=self.scale, stream=stream)
+        return out, lse
+
+    def backward_bias(self, q, k, v, out, lse, dout, bias, starts, shard: int = -1, dq=None, dk=None, dv=None,
+                      dbias=None, zero_grads: bool = True, stream=None):
+        """backward() of forward_bias(); also returns the bias's gradient
+        (zero_grads: dk, dv and dbias are set to zero first, else added to)."""
+        with _on_stream(stream):
+            if dq is None:
+                dq = torch.empty(self.T, self.hq, self.d, dtype=torch.float32, device=self.device)
+            new = [torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device) if x is None else x
+                   for x in (dk, dv)]
+            new.append(torch.zeros_like(bias) if dbias is None else dbias)
+            for given, x in zip((dk, dv, dbias), new):
+                if given is not None and zero_grads:
+                    x.zero_()
+            dk, dv, dbias = new
+        fcp.attn_bwd_bias(q, k, v, self.kbuf, self.vbuf, bias, starts, out, lse, dout, self.dplan, shard, dq, dk, dv, dbias,
+                          self.ws, scale=self.scale, stream=stream)
+        return dq, dk, dv, dbias
+
     def backward(self, q, k, v, out, lse, dout, shard: int = -1, dq=None, dk=None, dv=None,
                  zero_kv_grads: bool = True, stream=None):
         if dq is None:
@@ -115,12 +156,13 @@ class CPAttention:
         and key head normed (weights wq, wk) and turned by its position inside
         its document (inv_freq; None: not turned). The inputs are [T][heads][d]
         tensors or slices of one fused tensor."""
-        if q is None:
-            q = torch.empty(self.T, self.hq, self.d, dtype=torch.bfloat16, device=self.device)
-        if k is None:
-            k = torch.empty(self.T, self.hkv, self.d, dtype=torch.bfloat16, device=self.device)
-        if v is None and v_in is not None:
-            v = torch.empty_like(k)
+        with _on_stream(stream):
+            if q is None:
+                q = torch.empty(self.T, self.hq, self.d, dtype=torch.bfloat16, device=self.device)
+            if k is None:
+                k = torch.empty(self.T, self.hkv, self.d, dtype=torch.bfloat16, device=self.device)
+            if v is None and v_in is not None:
+                v = torch.empty_like(k)
         fcp.qk_norm_rope(q_in, k_in, v_in, self.dplan, shard, q, k, v, wq=wq, wk=wk, inv_freq=inv_freq, norm=norm,
                          eps=eps, interleaved=interleaved, stream=stream)
         return q, k, v
@@ -134,13 +176,14 @@ class CPAttention:
         gradients of the weights, added to dwq and dwk where they are given."""
         def rows(heads):
             return torch.empty(self.T, heads, self.d, dtype=torch.bfloat16, device=self.device)
-        dq_in = rows(self.hq) if dq_in is None else dq_in
-        dk_in = rows(self.hkv) if dk_in is None else dk_in
-        dv_in = rows(self.hkv) if dv_in is None and dv is not None else dv_in
-        if dwq is None and wq is not None:
-            dwq = torch.zeros(self.d, dtype=torch.float32, device=self.device)
-        if dwk is None and wk is not None:
-            dwk = torch.zeros(self.d, dtype=torch.float32, device=self.device)
+        with _on_stream(stream):
+            dq_in = rows(self.hq) if dq_in is None else dq_in
+            dk_in = rows(self.hkv) if dk_in is None else dk_in
+            dv_in = rows(self.hkv) if dv_in is None and dv is not None else dv_in
+            if dwq is None and wq is not None:
+                dwq = torch.zeros(self.d, dtype=torch.float32, device=self.device)
+            if dwk is None and wk is not None:
+                dwk = torch.zeros(self.d, dtype=torch.float32, device=self.device)
         fcp.qk_norm_rope_bwd(dq, dk, dv, q_in, k_in, self.dplan, shard, dq_in, dk_in, dv_in, dwq, dwk, self.ws, wq=wq,
                              wk=wk, inv_freq=inv_freq, norm=norm, eps=eps, interleaved=interleaved, stream=stream)
         return dq_in, dk_in, dv_in, dwq, dwk

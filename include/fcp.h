@@ -386,6 +386,59 @@ int fcp_attn_bwd(const void* q, const void* k, const void* v, const void* kbuf,
                  const void* dout, const fcp_dev_plan* plan, int32_t shard, fcp_dims dims,
                  float* dq, float* dk, float* dv, void* ws, int64_t ws_bytes, void* stream);
 
+/* A learned bias of the attention scores by buckets of the distance i - j
+ * between a query and a key of its document. Bucket u holds the distances
+ * starts[u] <= i - j < starts[u + 1]; the last one all from its start on. */
+#define FCP_MAX_BUCKETS 128
+typedef struct {
+  const float* bias;      /* device fp32 [hq][n_buckets], 4-byte aligned               */
+  const int32_t* starts;  /* host int32[n_buckets]: starts[0] = 0, none below the last */
+  int32_t n_buckets;      /* 1 .. FCP_MAX_BUCKETS                                      */
+} fcp_rel_bias;
+
+/*
+ * fcp_rel_buckets -- starts of the usual buckets of a causal model: one
+ * distance each up to n_buckets / 2, the others spaced by logarithms up to
+ * max_distance, from which on every distance is in the last one:
+ *   bucket(x) = x for x < E = n_buckets / 2, else
+ *   min(n_buckets - 1, E + floor((n_buckets - E) ln(x / E) / ln(max_distance / E))).
+ * A bucket that holds no whole number starts where the next one does. Host
+ * only. Errors: FCP_ERR_INVALID_ARG (null, n_buckets < 2, max_distance <= E),
+ * FCP_ERR_UNSUPPORTED (n_buckets > FCP_MAX_BUCKETS).
+ */
+int fcp_rel_buckets(int32_t n_buckets, int32_t max_distance, int32_t* starts);
+
+/*
+ * fcp_attn_fwd_bias -- fcp_attn_fwd with a learned bias by distance:
+ *   s_ij = scale <q_ih, k_jg> + bias[h][bucket(i - j)].
+ * Distances are of documents' tokens, so the result does not depend on the
+ * plan. Arguments, layouts, key blocks, workspace and results as
+ * fcp_attn_fwd (its partials merge with fcp_merge); `starts` is read during
+ * the call, `bias` when the kernel runs. Biases are finite with |b| < 1e30, or
+ * at or below -1e30 (the lowest fp32 value and -inf included): such a one
+ * masks its bucket. A row with nothing left gets O = 0 and LSE = -inf.
+ * Values of q, k, v that no query may see are computed with all the same and
+ * have to be finite.
+ */
+int fcp_attn_fwd_bias(const void* q, const void* k, const void* v, const void* kbuf, const void* vbuf,
+                      const fcp_rel_bias* bias, const fcp_dev_plan* plan, int32_t shard, int32_t kv_lo, int32_t kv_hi,
+                      fcp_dims dims, int32_t out_dtype, void* out, float* lse, void* ws, int64_t ws_bytes,
+                      void* stream);
+
+/*
+ * fcp_attn_bwd_bias -- exact gradient of fcp_attn_fwd_bias (full key set).
+ * Arguments and results as fcp_attn_bwd, and
+ *   dbias  fp32 [hq][n_buckets], ACCUMULATED (+=): dbias[h][u] = sum of dS_ij
+ *          over the pairs whose distance is in bucket u (0 for a masked one);
+ *          zero it before the first shard. Its terms are the fp16 dS that the
+ *          dQ and dK products take, added in fp32; like dq, dk and dv it is
+ *          added up by atomics, whose order can change its last bits.
+ */
+int fcp_attn_bwd_bias(const void* q, const void* k, const void* v, const void* kbuf, const void* vbuf,
+                      const fcp_rel_bias* bias, const void* out, int32_t out_dtype, const float* lse, const void* dout,
+                      const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, float* dq, float* dk, float* dv,
+                      float* dbias, void* ws, int64_t ws_bytes, void* stream);
+
 /* Options of the head norm and rotation. */
 typedef struct {
   int32_t norm;         /* 1: RMS norm of every query and key head; 0: rotation alone         */
