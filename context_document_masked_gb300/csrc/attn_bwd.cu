@@ -67,7 +67,9 @@ struct BwdCfg {
   static constexpr int kDO = 4 * kTile;          // 1 stage
   static constexpr int kStage = 5 * kTile;       // 2 x [128 rows][32 fp32] dQ chunks
   static constexpr int kDS = kStage + 2 * 16384; // 128 x 128 fp16 (two 64-column panels)
-  static constexpr int kStat = kDS + 128 * 128 * 2;  // [stage][lse2 | delta][128] fp32
+  // [stage][lse2 | delta][128] fp32; with a bias one stage, and the 256 entries
+  // of the step's bias window in the place of the other.
+  static constexpr int kStat = kDS + 128 * 128 * 2;
   static constexpr int kSmem = kStat + 2 * 2 * 128 * 4;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;           // S^T; P^T (fp16) in cols [0,32) and [64,96)
@@ -186,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_s_full, bar_dp_full, bar_p_ready, bar_ds_ready, bar_ds_free;
   __shared__ __align__(8) uint64_t bar_dq_full, bar_dq_free, bar_dkdv_full, bar_dkdv_free;
   __shared__ __align__(8) uint64_t bar_stg_full[2], bar_stg_free[2];  // dV / dK staging, per half
+  __shared__ __align__(8) uint64_t bar_stat_full;  // bias: the step's statistics and window
   __shared__ WorkRing<4> ring;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
@@ -205,9 +208,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar_kv_empty, 1);
     mbar_init(&bar_drain, 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar_q_full[s], 2);
+      mbar_init(&bar_q_full[s], kBias ? 1 : 2);
       mbar_init(&bar_q_empty[s], 1);
     }
+    mbar_init(&bar_stat_full, 1);
     mbar_init(&bar_do_full, 1);
     mbar_init(&bar_do_empty, 1);
     mbar_init(&bar_s_full, 1);
@@ -256,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kv_items = 0, qc = 0, dc = 0;
     uint32_t issued_q[2] = {0, 0};
     bool ok = true;
+    const float inv_scale = 1.f / p.scale;
     uint32_t k = 0;
     for (int w = blockIdx.x; ok;) {
       if (lane == 0) ok = ring.put(k, w, wc);
@@ -307,23 +312,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(smem + C::kQ + s * C::kTile + pn * 16384, &tm_q, &bar_q_full[s], pn * 64, h, q0);
           ++issued_q[s];
         }
-        float* st = stat + s * 256;
+        float st_lse[kBias ? 4 : 1], st_delta[kBias ? 4 : 1];
+        if constexpr (kBias) {
+          // Into registers: the one stage is written when the step before is
+          // done with it. A row whose buckets are all masked (LSE = -inf) gets
+          // P = 0, as the rows past the piece do.
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = lane + 32 * u;
-          const bool valid = r < q_rows;
-          // Stored negated (-LSE log2 e, -D): the compute warps add them with
-          // packed f32x2 arithmetic. Rows past the piece get P = 0.
-          if constexpr (kBias) {  // a row whose buckets are all masked (LSE = -inf) gets P = 0 too
+          for (int u = 0; u < 4; ++u) {
+            const int r = lane + 32 * u;
+            const bool valid = r < q_rows;
             const float lse = valid ? __ldg(p.lse + (size_t)h * p.T + q0 + r) : -INFINITY;
-            st[r] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-          } else {
-            st[r] = valid ? -__ldg(p.lse + (size_t)h * p.T + q0 + r) * kLog2e : -INFINITY;
+            st_lse[u] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+            st_delta[u] = valid ? -__ldg(p.delta + (size_t)h * p.T + q0 + r) : 0.f;
           }
-          st[128 + r] = valid ? -__ldg(p.delta + (size_t)h * p.T + q0 + r) : 0.f;
+        } else {
+          float* st = stat + s * 256;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int r = lane + 32 * u;
+            const bool valid = r < q_rows;
+            // Stored negated (-LSE log2 e, -D): the compute warps add them with
+            // packed f32x2 arithmetic. Rows past the piece get P = 0.
+            st[r] = valid ? -__ldg(p.lse + (size_t)h * p.T + q0 + r) * kLog2e : -INFINITY;
+            st[128 + r] = valid ? -__ldg(p.delta + (size_t)h * p.T + q0 + r) : 0.f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_q_full[s]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_q_full[s]);
         ++qc;
         // dO tile into the single dO buffer once dV of the previous step is done.
         if (dc >= 1) {
@@ -334,6 +349,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&bar_do_full, C::kTile);
           for (int pn = 0; pn < C::kPanels; ++pn)
             tma_load_3d(smem + C::kDO + pn * 16384, &tm_do, &bar_do_full, pn * 64, h, q0);
+        }
+        if constexpr (kBias) {
+          // The window: entry y is the bias of query q0 + y - 127 less key
+          // key0, over the scale; element (key row, column) of the tile takes
+          // entry column + 127 - row.
+          const float* bias_row = bp.bias + (size_t)h * bp.n;
+          float win[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            win[u] = bias_over_scale(bias_row, bucket_of(bias_starts, bp.n, max(q0 - it.key0 - 127 + lane + 32 * u, 0)),
+                                     inv_scale);
+          if (dc >= 1) {
+            ok = mbar_wait(&bar_ds_ready, (dc - 1) & 1, wc);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; ++dc; break; }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            stat[lane + 32 * u] = st_lse[u];
+            stat[128 + lane + 32 * u] = st_delta[u];
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) stat[256 + lane + 32 * u] = win[u];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_stat_full);
         }
         ++dc;
       }
@@ -498,46 +537,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nsteps = G * it.nq;
       const bool key_valid = kr < it.n;
       const int key = it.key0 + kr;
-      BucketRun run{0, 0, 0, 0.f};  // the bucket of the tiles far from the diagonal
+      BucketRun run{0, 0, 0};       // the bucket of the tiles far from the diagonal
       float run_sum = 0.f;          // this lane's dS in that bucket
       int run_head = 0;
       for (int j = 0; j < nsteps; ++j, ++gstep) {
         const uint32_t c = qc + j, s = c & 1;
         const StepRows sr = step_rows(it, G, j);
         const int q0 = sr.q0;
-        // Bias of the 32 keys x 64 queries of this warp: distance of element
-        // (lane, e) is base + 31 + e - lane; entry x of the window has base + x.
-        const int base = q0 + 64 * half - it.key0 - 32 * (warp & 3) - 31;
-        bool spread = false, below = true;  // below: some of the distances are >= 0
-        float win[kBias ? 3 : 1];
-        if constexpr (kBias) {
-          below = base + 94 >= 0;
-          if (below) {
-            const float* bias_row = bp.bias + (size_t)sr.h * bp.n;
-            const int near = max(base, 0);
-            if (run_head != sr.h || near < run.lo || near >= run.hi) {
-              add_run(bp.dbias + (size_t)run_head * bp.n + run.bucket, run_sum, lane);
-              run_head = sr.h;
-              bucket_run(run, bias_starts, bp.n, bias_row, near);
-            }
-            spread = base + 94 >= run.hi;
-            if (spread) {
-#pragma unroll
-              for (int w3 = 0; w3 < 3; ++w3) {
-                const int dist = base + lane + 32 * w3;
-                win[w3] = dist >= 0 ? bias_log2(bias_row, bucket_of(bias_starts, bp.n, dist)) : 0.f;
-              }
-            }
-          }
-        }
         const int lim = key - q0 - 64 * half;  // local columns below lim cannot see this key
         // Whole tile below the diagonal with 128 keys: no element needs a mask
         // (query rows past the piece end have LSE = +inf, hence P = 0).
         const bool unmasked = it.n == 128 && it.key0 + 127 <= q0;
-        ok = mbar_wait(&bar_s_full, gstep & 1, wc) && mbar_wait(&bar_q_full[s], (c >> 1) & 1, wc);
+        ok = mbar_wait(&bar_s_full, gstep & 1, wc) &&
+             (kBias ? mbar_wait(&bar_stat_full, gstep & 1, wc) : mbar_wait(&bar_q_full[s], (c >> 1) & 1, wc));
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
-        const float4* st4 = reinterpret_cast<const float4*>(stat + s * 256 + 64 * half);
+        const float4* st4 = reinterpret_cast<const float4*>(stat + (kBias ? 0 : s * 256) + 64 * half);
         uint32_t pk[32];
         {
           // Both 32-column halves of this group's S^T in flight together.
@@ -549,23 +564,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             const float* v = e < 32 ? va + e : vb + (e - 32);
-            float4 l4 = st4[e >> 2];  // -LSE log2 e of the four query columns
-            if constexpr (kBias) {
-              if (spread) {
-                l4.x += window_at(win, e, lane);
-                l4.y += window_at(win, e + 1, lane);
-                l4.z += window_at(win, e + 2, lane);
-                l4.w += window_at(win, e + 3, lane);
-              } else {
-                l4.x += run.value;
-                l4.y += run.value;
-                l4.z += run.value;
-                l4.w += run.value;
-              }
+            const float4 l4 = st4[e >> 2];  // -LSE log2 e of the four query columns
+            float v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
+            if constexpr (kBias) {  // every tile takes its window: no second path to fetch
+              const float* w = stat + 256 + 64 * half + 127 - kr + e;
+              f2_split(f2_add(f2(v0, v1), f2(w[0], w[1])), v0, v1);
+              f2_split(f2_add(f2(v2, v3), f2(w[2], w[3])), v2, v3);
             }
             float p0, p1, p2, p3;
-            f2_split(f2_fma(f2(v[0], v[1]), c2, f2(l4.x, l4.y)), p0, p1);
-            f2_split(f2_fma(f2(v[2], v[3]), c2, f2(l4.z, l4.w)), p2, p3);
+            f2_split(f2_fma(f2(v0, v1), c2, f2(l4.x, l4.y)), p0, p1);
+            f2_split(f2_fma(f2(v2, v3), c2, f2(l4.z, l4.w)), p2, p3);
             p0 = ex2(p0);
             p1 = ex2(p1);
             p2 = ex2(p2);
@@ -624,34 +632,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&bar_ds_ready);
-        // The bias's gradient: sums of the dS just stored, this lane's own row
-        // read back (fp16, the operands of the dK and dQ products) and added
-        // in fp32, after the MMA thread has been let go on.
+        // The bias's gradient: sums of the dS just stored (fp16, the operands of
+        // the dK and dQ products), read back and added in fp32 after the MMA
+        // thread has been let go on. The distance of the warp's element (row
+        // r, column e) is base + 31 + e - r.
         if constexpr (kBias) {
-          if (below) {
-            float diag[3] = {0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-              uint32_t d[4];
-              ld_shared_v4(ds_panel + sw128_offset(kr, ch), d);
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&d[u]));
-                if (spread) {
-                  window_add(diag, ch * 8 + 2 * u, lane, x.x);
-                  window_add(diag, ch * 8 + 2 * u + 1, lane, x.y);
-                } else {
-                  run_sum += x.x + x.y;
-                }
-              }
+          const int base = q0 + 64 * half - it.key0 - 32 * (warp & 3) - 31, near = max(base, 0);
+          if (base + 94 >= 0) {
+            float* row = bp.dbias + (size_t)sr.h * bp.n;
+            if (run_head != sr.h || near < run.lo || near >= run.hi) {
+              add_run(bp.dbias + (size_t)run_head * bp.n + run.bucket, run_sum, lane);
+              run_head = sr.h;
+              bucket_run(run, bias_starts, bp.n, near);
             }
-            if (spread) {
-              float* row = bp.dbias + (size_t)sr.h * bp.n;
+            if (base + 94 < run.hi) {
+              run_sum += row_sum(ds_panel, kr);
+            } else {
+              __syncwarp();  // the warp's rows are stored
+              float sum[3];
+              diagonal_sums(ds_panel, 32 * (warp & 3), lane, sum);
+              __syncwarp();  // and read by all lanes
 #pragma unroll
-              for (int w3 = 0; w3 < 3; ++w3) {
-                const int dist = base + lane + 32 * w3;
-                add_by_bucket(row, dist >= 0 ? bucket_of(bias_starts, bp.n, dist) : 0, diag[w3], lane);
-              }
+              for (int w = 0; w < 3; ++w)
+                add_by_bucket(row, bucket_of(bias_starts, bp.n, max(base + lane + 32 * w, 0)), sum[w], lane);
             }
           }
         }

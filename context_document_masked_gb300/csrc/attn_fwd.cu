@@ -55,14 +55,17 @@ namespace {
 constexpr int kThreads = 320;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: rescale O when the max grows by > 2^8
 
-template <int D>
+template <int D, bool BIAS>
 struct FwdCfg {
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  // With a bias, d = 128 keeps four stages and the room of a fifth for the
+  // warps' windows (four stages measured as fast as five without one).
+  static constexpr int kStages = D == 128 ? (BIAS ? 4 : 5) : 8;
   static constexpr int kPanels = D / 64;                 // 64-column swizzle panels per row
   static constexpr int kTileBytes = 128 * D * 2;         // one Q/K/V tile
   static constexpr int kQOff = 0;
   static constexpr int kKVOff = 2 * kTileBytes;
-  static constexpr int kSmem = kKVOff + kStages * kTileBytes;
+  static constexpr int kWinOff = kKVOff + kStages * kTileBytes;
+  static constexpr int kSmem = kWinOff + (BIAS ? 8 * kWindowFloats * 4 : 0);
   static constexpr int kSmemAlloc = kSmem + 1024;        // slack for 1024-byte alignment
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0;                   // S_i at i*128; P_i (fp16) over its first 64
@@ -198,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kb,
                     const __grid_constant__ CUtensorMap tm_vb, const FwdParams p, const __grid_constant__ Bias bp) {
-  using C = FwdCfg<D>;
   constexpr bool kBias = std::is_same_v<Bias, BiasParams>;
+  using C = FwdCfg<D, kBias>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -417,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const bool out_v8 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
     // e4m3 Q K^T: S comes out scaled by 2^kq 2^kk (powers of two, exact).
+    float* window = reinterpret_cast<float*>(smem + C::kWinOff) + (kBias ? (warp - 2) * kWindowFloats : 0);
+    const float inv_scale = kBias ? kLog2e / p.scale_log2 : 0.f;
     const float scale_log2 = QK8 ? p.scale_log2 / (p.qk_scale[0] * p.qk_scale[1]) : p.scale_log2;
     for (uint32_t k = 0; ok; ++k) {
       int w = 0;
@@ -435,7 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_run = -INFINITY, l = 0.f;
       const float* bias_row = nullptr;
       const int q_warp = it.q_start + 32 * (warp & 3);  // this warp's first row
-      BucketRun run{0, 0, 0, 0.f};
+      BucketRun run{0, 0, 0};  // the bucket of the tiles far from the diagonal, and its bias
+      float run_bias = 0.f;
       if constexpr (kBias) bias_row = bp.bias + (size_t)(i ? it.h1 : it.h0) * bp.n;
       if (nt > 0) {
         Walker wk;
@@ -443,22 +449,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         int src, row, key, n;
         for (int t = 0; t < nt; ++t) {
           wk.next(src, row, key, n);
-          // Bias of the tile: one bucket for all the warp's visible
-          // distances, or the window of entries this lane keeps.
-          bool spread = false;
-          float win[kBias ? 5 : 1];
+          // Bias of the tile: one bucket for all the warp's distances, or the
+          // window of them. Set up before S is waited for, so its latency is
+          // hidden.
+          bool windowed = false;
           if constexpr (kBias) {
             const int far = q_warp + 31 - key, near = max(q_warp - key - 127, 0);
             if (far >= 0) {
-              if (near < run.lo || near >= run.hi) bucket_run(run, bias_starts, bp.n, bias_row, near);
-              spread = far >= run.hi;
-              if (spread) {
-#pragma unroll
-                for (int w5 = 0; w5 < 5; ++w5) {
-                  const int dist = q_warp - key - 127 + lane + 32 * w5;
-                  win[w5] = dist >= 0 ? bias_log2(bias_row, bucket_of(bias_starts, bp.n, dist)) : 0.f;
-                }
+              if (near < run.lo || near >= run.hi) {
+                bucket_run(run, bias_starts, bp.n, near);
+                run_bias = bias_log2(bias_row, run.bucket);
               }
+              windowed = far >= run.hi;
+              if (windowed) fill_window(window, bias_starts, bp.n, bias_row, far, inv_scale, lane);
             }
           }
           ok = mbar_wait_inline(&bar_s_full[i], s_cnt & 1, wc);
@@ -474,20 +477,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j) s[c * 32 + j] = v[j];
           }
           tmem_ld_wait();
-          // The scores' factor and addend to log2 units: the tile's bucket, or
-          // 1 and 0 where the window's biases are added element by element.
-          float mul = scale_log2, add = 0.f;
+          float add = 0.f;  // the tile's bias in log2 units, where it is one
           if constexpr (kBias) {
-            add = run.value;
-            if (spread) {
-              mul = 1.f;
-              add = 0.f;
+            if (windowed) {
+              const float4* w4 = window_row(window, lane);
 #pragma unroll
-              for (int c = 0; c < 128; ++c) {  // window entry lane + 127 - c
-                const int k0 = (127 - c) >> 5, r0 = (127 - c) & 31;
-                const float mine = lane >= r0 ? win[k0] : win[k0 + 1];
-                s[c] = fmaf(s[c], scale_log2, __shfl_sync(0xffffffffu, mine, lane + 127 - c));
+              for (int c = 0; c < 32; ++c) {
+                const float4 b = w4[c];
+                f2_split(f2_add(f2(s[4 * c], s[4 * c + 1]), f2(b.x, b.y)), s[4 * c], s[4 * c + 1]);
+                f2_split(f2_add(f2(s[4 * c + 2], s[4 * c + 3]), f2(b.z, b.w)), s[4 * c + 2], s[4 * c + 3]);
               }
+            } else {
+              add = run_bias;
             }
           }
           if (key + 127 > it.q_start || n < 128) {
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx8[j] = m;
           }
           float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], fmax3(mx8[5], mx8[6], mx8[7]))) *
-                     mul;
+                     scale_log2;
           if constexpr (kBias) mx += add;
           const float m_new = fmaxf(m_run, mx);
           const bool rescale = m_new > m_run + kRescaleThreshold;
@@ -520,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // P = exp2(s * scale * log2e - m): fp16 pairs straight into TMEM columns
           // [0, 64) of S_i, 64 score columns at a time. The scaling and the row
           // sum run on packed pairs; sums of column c go to accumulator c mod 8.
-          const uint64_t c2 = f2(mul, mul), nm2 = kBias ? f2(add - m_use, add - m_use) : f2(-m_use, -m_use);
+          const uint64_t c2 = f2(scale_log2, scale_log2), nm2 = kBias ? f2(add - m_use, add - m_use) : f2(-m_use, -m_use);
           uint64_t rs2[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {  // 32 score columns -> 16 TMEM columns of P
@@ -637,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D, bool QK8, bool ODD, class Bias>
 static int launch_fwd_impl(const FwdLaunch& a, const Bias& bias, cudaStream_t st) {
-  using C = FwdCfg<D>;
+  using C = FwdCfg<D, std::is_same_v<Bias, BiasParams>>;
   static bool attr_set[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
