@@ -140,6 +140,94 @@ __device__ __forceinline__ StepRows step_rows(const BwdItem& it, int G, int j) {
   return r;
 }
 
+// With a bias: the statistics and the bias window of each step, which warps
+// 2-3 (64 threads t) bring into shared memory.
+struct BiasSteps {
+  float lse[2], delta[2], win[4];  // the next step's, in registers
+  bool windowed;
+  BucketRun seen{0, 0, 0};
+
+  __device__ __forceinline__ void load(const BwdParams& p, const BiasParams& bp, const Buckets& bk, const BwdItem& it,
+                                       int G, int j, int t) {
+    const StepRows sr = step_rows(it, G, j);
+    const float* bias_row = bp.bias + (size_t)sr.h * bp.n;
+    const int first = sr.q0 - it.key0 - 127;  // distance of window entry 0
+    const int near = max(first, 0);
+    if (near < seen.lo || near >= seen.hi) bucket_run(seen, bk, bp.n, near);
+    windowed = first + 254 >= seen.hi;
+    const float one = windowed ? 0.f : bias_log2(bias_row, seen.bucket);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = t + 64 * u;
+      const bool valid = r < min(128, sr.q_end - sr.q0);
+      // Negated, as without a bias. A row whose buckets are all masked (LSE =
+      // -inf) gets P = 0, as the rows past the piece do.
+      const float l = valid ? __ldg(p.lse + (size_t)sr.h * p.T + sr.q0 + r) : -INFINITY;
+      lse[u] = l == -INFINITY ? -INFINITY : one - l * kLog2e;
+      delta[u] = valid ? -__ldg(p.delta + (size_t)sr.h * p.T + sr.q0 + r) : 0.f;
+    }
+    if (windowed) {
+      const float inv_scale = 1.f / p.scale;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        win[u] = bias_over_scale(bias_row, bk.of(bp.n, max(first + t + 64 * u, 0)), inv_scale);
+    }
+  }
+  __device__ __forceinline__ void store_lse(float* stat, int* windowed_sh, int t) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) stat[t + 64 * u] = lse[u];
+    if (windowed) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) stat[256 + t + 64 * u] = win[u];
+    }
+    if (t == 0) *reinterpret_cast<volatile int*>(windowed_sh) = windowed;
+  }
+  __device__ __forceinline__ void store_delta(float* stat, int t) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) stat[128 + t + 64 * u] = delta[u];
+  }
+
+};
+
+// With a bias: one compute warp's sums of dS by buckets. Its block of a step
+// is 32 key rows x 64 query columns; a block of one bucket adds to a sum held
+// in registers while the bucket and the head stay, the others are summed by
+// diagonals.
+struct BiasSums {
+  BucketRun run{0, 0, 0};
+  float sum = 0.f;       // this lane's share of the run's
+  float* row = nullptr;  // the head's table row
+
+  __device__ __forceinline__ void flush(int lane) {
+    if (row) add_run(row + run.bucket, sum, lane);
+  }
+  // block: the stored dS (fp16, swizzled); base: distance of its diagonal 0
+  // (column 0, row 31).
+  __device__ __forceinline__ void add(uint32_t block, float* head_row, const Buckets& bk, int n, int base, int lane) {
+    if (base + 94 < 0) return;
+    const int near = max(base, 0);
+    if (row != head_row || near < run.lo || near >= run.hi) {
+      flush(lane);
+      row = head_row;
+      bucket_run(run, bk, n, near);
+    }
+    __syncwarp();  // the warp's rows are stored
+    if (base + 94 < run.hi) {
+      sum += block_sum(block, lane);
+    } else {
+      float d[3];
+      diagonal_sums(block, lane, d);
+#pragma unroll 1
+      for (int w = 0; w < 3; ++w, base += 32) {
+        add_by_bucket(row, bk.of(n, max(base + lane, 0)), d[0], lane);
+        d[0] = d[1];
+        d[1] = d[2];
+      }
+    }
+    __syncwarp();  // and read, before the next step's are
+  }
+};
+
 // TMA bulk reduce-add of a shared-memory tile into global memory.
 __device__ __forceinline__ void tma_reduce_add_3d(const void* tmap, const void* src, int c0, int c1,
                                                   int c2) {
@@ -188,16 +276,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_s_full, bar_dp_full, bar_p_ready, bar_ds_ready, bar_ds_free;
   __shared__ __align__(8) uint64_t bar_dq_full, bar_dq_free, bar_dkdv_full, bar_dkdv_free;
   __shared__ __align__(8) uint64_t bar_stg_full[2], bar_stg_free[2];  // dV / dK staging, per half
-  __shared__ __align__(8) uint64_t bar_stat_full;  // bias: the step's statistics and window
+  __shared__ __align__(8) uint64_t bar_lse_full, bar_delta_full;  // bias: LSE and window, D of the step
   __shared__ WorkRing<4> ring;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ int bias_starts[kBias ? kMaxBuckets : 1];
+  __shared__ std::conditional_t<kBias, Buckets, NoBias> buckets;
+  __shared__ int windowed_sh;  // bias: the step's tile spans several buckets
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if constexpr (kBias) {
-    if (tid < bp.n) bias_starts[tid] = bp.starts[tid];
-  }
+  if constexpr (kBias) buckets.init(bp, tid, kThreads);
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled layouts need 1024-byte alignment
     if (tid == 0) atomicOr(p.err, 2);
     return;
@@ -211,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_q_full[s], kBias ? 1 : 2);
       mbar_init(&bar_q_empty[s], 1);
     }
-    mbar_init(&bar_stat_full, 1);
+    mbar_init(&bar_lse_full, 2);
+    mbar_init(&bar_delta_full, 2);
     mbar_init(&bar_do_full, 1);
     mbar_init(&bar_do_empty, 1);
     mbar_init(&bar_s_full, 1);
@@ -260,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t kv_items = 0, qc = 0, dc = 0;
     uint32_t issued_q[2] = {0, 0};
     bool ok = true;
-    const float inv_scale = 1.f / p.scale;
     uint32_t k = 0;
     for (int w = blockIdx.x; ok;) {
       if (lane == 0) ok = ring.put(k, w, wc);
@@ -312,20 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(smem + C::kQ + s * C::kTile + pn * 16384, &tm_q, &bar_q_full[s], pn * 64, h, q0);
           ++issued_q[s];
         }
-        float st_lse[kBias ? 4 : 1], st_delta[kBias ? 4 : 1];
-        if constexpr (kBias) {
-          // Into registers: the one stage is written when the step before is
-          // done with it. A row whose buckets are all masked (LSE = -inf) gets
-          // P = 0, as the rows past the piece do.
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int r = lane + 32 * u;
-            const bool valid = r < q_rows;
-            const float lse = valid ? __ldg(p.lse + (size_t)h * p.T + q0 + r) : -INFINITY;
-            st_lse[u] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-            st_delta[u] = valid ? -__ldg(p.delta + (size_t)h * p.T + q0 + r) : 0.f;
-          }
-        } else {
+        if constexpr (!kBias) {  // with a bias warps 2-3 write them
           float* st = stat + s * 256;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -349,30 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&bar_do_full, C::kTile);
           for (int pn = 0; pn < C::kPanels; ++pn)
             tma_load_3d(smem + C::kDO + pn * 16384, &tm_do, &bar_do_full, pn * 64, h, q0);
-        }
-        if constexpr (kBias) {
-          // The window: entry y is the bias of query q0 + y - 127 less key
-          // key0, over the scale; element (key row, column) of the tile takes
-          // entry column + 127 - row.
-          const float* bias_row = bp.bias + (size_t)h * bp.n;
-          float win[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            win[u] = bias_over_scale(bias_row, bucket_of(bias_starts, bp.n, max(q0 - it.key0 - 127 + lane + 32 * u, 0)),
-                                     inv_scale);
-          if (dc >= 1) {
-            ok = mbar_wait(&bar_ds_ready, (dc - 1) & 1, wc);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; ++dc; break; }
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            stat[lane + 32 * u] = st_lse[u];
-            stat[128 + lane + 32 * u] = st_delta[u];
-          }
-#pragma unroll
-          for (int u = 0; u < 8; ++u) stat[256 + lane + 32 * u] = win[u];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_stat_full);
         }
         ++dc;
       }
@@ -486,9 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2 || warp == 3) {
     // ------------------------------------------------------------ K/V to fp16
     const int t = tid - 64;
-    uint32_t items = 0;
+    uint32_t items = 0, gstep = 0;
     bool ok = true, ovf = false;
     uint4* kv = reinterpret_cast<uint4*>(smem + C::kK);  // K and V tiles are contiguous
+    BiasSteps bias;
     for (uint32_t k = 0; ok; ++k) {
       int w = 0;
       ok = ring.get(k, w, wc);
@@ -496,23 +547,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) ring.release(k);
       if (w >= n_work) break;
-      if constexpr (kDeviceChecks) {
-        if (decode(p, w).bad) continue;
+      BwdItem it;
+      if constexpr (kDeviceChecks || kBias) {
+        it = decode(p, w);
+        if (it.bad) continue;
       }
-      ok = mbar_wait(&bar_kv_full, items & 1, wc);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      auto convert = [&]() {
+        ok = mbar_wait(&bar_kv_full, items & 1, wc);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; return; }
 #pragma unroll 4
-      for (int i = t; i < 2 * C::kTile / 16; i += 64) {
-        uint4 x = kv[i];
-        x.x = bf16x2_to_f16x2(x.x, ovf);
-        x.y = bf16x2_to_f16x2(x.y, ovf);
-        x.z = bf16x2_to_f16x2(x.z, ovf);
-        x.w = bf16x2_to_f16x2(x.w, ovf);
-        kv[i] = x;
+        for (int i = t; i < 2 * C::kTile / 16; i += 64) {
+          uint4 x = kv[i];
+          x.x = bf16x2_to_f16x2(x.x, ovf);
+          x.y = bf16x2_to_f16x2(x.y, ovf);
+          x.z = bf16x2_to_f16x2(x.z, ovf);
+          x.w = bf16x2_to_f16x2(x.w, ovf);
+          kv[i] = x;
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bar_kv_conv);
+        ++items;
+      };
+      if constexpr (!kBias) {
+        convert();
+        if (!ok) break;
+      } else {
+        // With a bias these warps also follow the unit's steps: LSE, D and the
+        // bias window of a step go into shared memory as soon as the compute
+        // warps are done with those of the step before.
+        const int nsteps = G * it.nq;
+        for (int j = -1; j < nsteps; ++j) {
+          const bool more = j + 1 < nsteps;
+          if (more) bias.load(p, bp, buckets, it, G, j + 1, t);
+          if (j < 0) {
+            convert();
+          } else {
+            ok = mbar_wait(&bar_p_ready, gstep & 1, wc);
+            ok = __all_sync(0xffffffffu, ok);
+          }
+          if (!ok) break;
+          if (more) {
+            bias.store_lse(stat, &windowed_sh, t);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_lse_full);
+          }
+          if (j >= 0) {
+            ok = mbar_wait(&bar_ds_ready, gstep & 1, wc);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            ++gstep;
+          }
+          if (more) {
+            bias.store_delta(stat, t);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_delta_full);
+          }
+        }
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&bar_kv_conv);
-      ++items;
     }
     if (ovf) atomicOr(p.err, 4);
   } else if (warp < 12) {
@@ -537,9 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nsteps = G * it.nq;
       const bool key_valid = kr < it.n;
       const int key = it.key0 + kr;
-      BucketRun run{0, 0, 0};       // the bucket of the tiles far from the diagonal
-      float run_sum = 0.f;          // this lane's dS in that bucket
-      int run_head = 0;
+      BiasSums sums;
       for (int j = 0; j < nsteps; ++j, ++gstep) {
         const uint32_t c = qc + j, s = c & 1;
         const StepRows sr = step_rows(it, G, j);
@@ -549,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (query rows past the piece end have LSE = +inf, hence P = 0).
         const bool unmasked = it.n == 128 && it.key0 + 127 <= q0;
         ok = mbar_wait(&bar_s_full, gstep & 1, wc) &&
-             (kBias ? mbar_wait(&bar_stat_full, gstep & 1, wc) : mbar_wait(&bar_q_full[s], (c >> 1) & 1, wc));
+             (kBias ? mbar_wait(&bar_lse_full, gstep & 1, wc) : mbar_wait(&bar_q_full[s], (c >> 1) & 1, wc));
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         const float4* st4 = reinterpret_cast<const float4*>(stat + (kBias ? 0 : s * 256) + 64 * half);
@@ -560,20 +648,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(s_cols, va);
           tmem_ld32(s_cols + 32, vb);
           tmem_ld_wait();
+          if constexpr (kBias) {
+            // A tile of one bucket has its bias in the LSE; the others add the
+            // window (entry column + 127 - row) to the raw scores.
+            if (*reinterpret_cast<volatile int*>(&windowed_sh)) {
+              const float* w = stat + 256 + 64 * half + 127 - kr;
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                f2_split(f2_add(f2(va[e], va[e + 1]), f2(w[e], w[e + 1])), va[e], va[e + 1]);
+                f2_split(f2_add(f2(vb[e], vb[e + 1]), f2(w[32 + e], w[33 + e])), vb[e], vb[e + 1]);
+              }
+            }
+          }
           const uint64_t c2 = f2(p.scale_log2, p.scale_log2);
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             const float* v = e < 32 ? va + e : vb + (e - 32);
             const float4 l4 = st4[e >> 2];  // -LSE log2 e of the four query columns
-            float v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
-            if constexpr (kBias) {  // every tile takes its window: no second path to fetch
-              const float* w = stat + 256 + 64 * half + 127 - kr + e;
-              f2_split(f2_add(f2(v0, v1), f2(w[0], w[1])), v0, v1);
-              f2_split(f2_add(f2(v2, v3), f2(w[2], w[3])), v2, v3);
-            }
             float p0, p1, p2, p3;
-            f2_split(f2_fma(f2(v0, v1), c2, f2(l4.x, l4.y)), p0, p1);
-            f2_split(f2_fma(f2(v2, v3), c2, f2(l4.z, l4.w)), p2, p3);
+            f2_split(f2_fma(f2(v[0], v[1]), c2, f2(l4.x, l4.y)), p0, p1);
+            f2_split(f2_fma(f2(v[2], v[3]), c2, f2(l4.z, l4.w)), p2, p3);
             p0 = ex2(p0);
             p1 = ex2(p1);
             p2 = ex2(p2);
@@ -599,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bar_p_ready);
         ok = mbar_wait(&bar_dp_full, gstep & 1, wc);
         if (ok && gstep > 0) ok = mbar_wait(&bar_ds_free, (gstep - 1) & 1, wc);
+        if constexpr (kBias) ok = ok && mbar_wait(&bar_delta_full, gstep & 1, wc);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         // dS = P (dP - D) in packed fp16: (dP - D) and the product are each
@@ -632,35 +727,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&bar_ds_ready);
-        // The bias's gradient: sums of the dS just stored (fp16, the operands of
-        // the dK and dQ products), read back and added in fp32 after the MMA
-        // thread has been let go on. The distance of the warp's element (row
-        // r, column e) is base + 31 + e - r.
-        if constexpr (kBias) {
-          const int base = q0 + 64 * half - it.key0 - 32 * (warp & 3) - 31, near = max(base, 0);
-          if (base + 94 >= 0) {
-            float* row = bp.dbias + (size_t)sr.h * bp.n;
-            if (run_head != sr.h || near < run.lo || near >= run.hi) {
-              add_run(bp.dbias + (size_t)run_head * bp.n + run.bucket, run_sum, lane);
-              run_head = sr.h;
-              bucket_run(run, bias_starts, bp.n, near);
-            }
-            if (base + 94 < run.hi) {
-              run_sum += row_sum(ds_panel, kr);
-            } else {
-              __syncwarp();  // the warp's rows are stored
-              float sum[3];
-              diagonal_sums(ds_panel, 32 * (warp & 3), lane, sum);
-              __syncwarp();  // and read by all lanes
-#pragma unroll
-              for (int w = 0; w < 3; ++w)
-                add_by_bucket(row, bucket_of(bias_starts, bp.n, max(base + lane + 32 * w, 0)), sum[w], lane);
-            }
-          }
-        }
+        // The bias's gradient: the dS just stored (fp16, the operands of the
+        // dK and dQ products) read back and added in fp32, once the MMA thread
+        // has been let go on.
+        if constexpr (kBias)
+          sums.add(ds_panel + 4096 * (warp & 3), bp.dbias + (size_t)sr.h * bp.n, buckets, bp.n,
+                   q0 + 64 * half - it.key0 - 32 * (warp & 3) - 31, lane);
       }
       if (!ok) break;
-      if constexpr (kBias) add_run(bp.dbias + (size_t)run_head * bp.n + run.bucket, run_sum, lane);
+      if constexpr (kBias) sums.flush(lane);
       qc += nsteps;
       // dV (columns-0 group) or dK (columns-64 group) of this key tile ->
       // global rows: 32-column chunks staged in this group's half of the dS

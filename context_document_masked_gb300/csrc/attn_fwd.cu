@@ -212,14 +212,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ WorkRing<4> ring;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ int bias_starts[kBias ? kMaxBuckets : 1];
+  __shared__ std::conditional_t<kBias, Buckets, NoBias> buckets;
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
-  if constexpr (kBias) {
-    if (tid < bp.n) bias_starts[tid] = bp.starts[tid];
-  }
+  if constexpr (kBias) buckets.init(bp, tid, kThreads);
 
   if (tid == 0) {
     mbar_init(&bar_q_full, 1);
@@ -457,11 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int far = q_warp + 31 - key, near = max(q_warp - key - 127, 0);
             if (far >= 0) {
               if (near < run.lo || near >= run.hi) {
-                bucket_run(run, bias_starts, bp.n, near);
+                bucket_run(run, buckets, bp.n, near);
                 run_bias = bias_log2(bias_row, run.bucket);
               }
               windowed = far >= run.hi;
-              if (windowed) fill_window(window, bias_starts, bp.n, bias_row, far, inv_scale, lane);
+              if (windowed) fill_window(window, buckets, bp.n, bias_row, far, inv_scale, lane);
             }
           }
           ok = mbar_wait_inline(&bar_s_full[i], s_cnt & 1, wc);

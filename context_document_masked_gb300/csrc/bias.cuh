@@ -27,14 +27,31 @@ namespace dev {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMaskBelow = -1e30f;  // a bias at or below this masks its bucket
 
-// Last bucket whose first distance is <= dist (dist >= 0, starts[0] = 0).
-__device__ __forceinline__ int bucket_of(const int* starts, int n, int dist) {
-  int b = 0;
+// The buckets in shared memory: their first distances, and the bucket of each
+// distance below kNear (near the diagonal every element needs its own).
+constexpr int kNear = 128;
+struct Buckets {
+  int starts[kMaxBuckets];
+  uint8_t near[kNear];
+
+  __device__ __forceinline__ void init(const BiasParams& bp, int tid, int threads) {
+    for (int i = tid; i < bp.n; i += threads) starts[i] = bp.starts[i];
+    __syncthreads();
+    for (int i = tid; i < kNear; i += threads) near[i] = (uint8_t)search(bp.n, i);
+  }
+  // Last bucket whose first distance is <= dist (dist >= 0, starts[0] = 0).
+  __device__ __forceinline__ int search(int n, int dist) const {
+    int b = 0;
 #pragma unroll
-  for (int step = kMaxBuckets / 2; step; step >>= 1)
-    if (b + step < n && starts[b + step] <= dist) b += step;
-  return b;
-}
+    for (int step = kMaxBuckets / 2; step; step >>= 1)
+      if (b + step < n && starts[b + step] <= dist) b += step;
+    return b;
+  }
+  __device__ __forceinline__ int of(int n, int dist) const {
+    if (dist < kNear) return near[dist];
+    return dist >= starts[n - 1] ? n - 1 : search(n, dist);
+  }
+};
 
 // The bias of a bucket in units of log 2.
 __device__ __forceinline__ float bias_log2(const float* row, int bucket) {
@@ -46,10 +63,10 @@ __device__ __forceinline__ float bias_log2(const float* row, int bucket) {
 struct BucketRun {
   int lo, hi, bucket;
 };
-__device__ __forceinline__ void bucket_run(BucketRun& r, const int* starts, int n, int dist) {
-  r.bucket = bucket_of(starts, n, dist);
-  r.lo = starts[r.bucket];
-  r.hi = r.bucket + 1 < n ? starts[r.bucket + 1] : INT32_MAX;
+__device__ __forceinline__ void bucket_run(BucketRun& r, const Buckets& bk, int n, int dist) {
+  r.bucket = bk.of(n, dist);
+  r.lo = bk.starts[r.bucket];
+  r.hi = r.bucket + 1 < n ? bk.starts[r.bucket + 1] : INT32_MAX;
 }
 
 // The same over the softmax scale, to be added to raw scores.
@@ -66,12 +83,12 @@ __device__ __forceinline__ float bias_over_scale(const float* row, int bucket, f
 // banks.
 constexpr int kWindowCopy = 168;
 constexpr int kWindowFloats = 4 * kWindowCopy;
-__device__ __forceinline__ void fill_window(float* win, const int* starts, int n, const float* row, int far,
+__device__ __forceinline__ void fill_window(float* win, const Buckets& bk, int n, const float* row, int far,
                                             float inv_scale, int lane) {
   __syncwarp();  // every row of the tile before has been read
 #pragma unroll 1
   for (int y = lane; y < 160; y += 32) {
-    const float b = bias_over_scale(row, bucket_of(starts, n, max(far - y, 0)), inv_scale);
+    const float b = bias_over_scale(row, bk.of(n, max(far - y, 0)), inv_scale);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (y >= k) win[k * kWindowCopy + y - k] = b;
@@ -99,7 +116,7 @@ __device__ __forceinline__ void add_run(float* at, float& v, int lane) {
 // Adds each lane's v to row[bucket], the buckets not falling with the lane:
 // one atomic for every bucket of the warp.
 __device__ __forceinline__ void add_by_bucket(float* row, int bucket, float v, int lane) {
-#pragma unroll
+#pragma unroll 1
   for (int m = 1; m < 32; m <<= 1) {  // inclusive sums inside a run of equal buckets
     const float up = __shfl_up_sync(0xffffffffu, v, m);
     const int b = __shfl_up_sync(0xffffffffu, bucket, m);
@@ -109,34 +126,37 @@ __device__ __forceinline__ void add_by_bucket(float* row, int bucket, float v, i
   if ((lane == 31 || next != bucket) && v != 0.f) atomicAdd(row + bucket, v);
 }
 
-// Sum over a warp's 32 x 64 tile of dS (fp16, one half of the swizzled panel,
-// first row `row0`) of every diagonal: this lane's entries lane, lane + 32 and
-// lane + 64 of the window, entry y the elements with column - row = y - 31.
-__device__ __forceinline__ void diagonal_sums(uint32_t panel, int row0, int lane, float (&sum)[3]) {
+// Sums along the diagonals of 32 rows x 64 columns of dS (fp16, rows of 128
+// bytes in the 128-byte swizzle): this lane's diagonals lane, lane + 32 and
+// lane + 64, diagonal y the elements with column - row = y - 31. The lanes of
+// a warp read neighbouring columns of one row at a time.
+__device__ __forceinline__ void diagonal_sums(uint32_t block, int lane, float (&sum)[3]) {
   sum[0] = sum[1] = sum[2] = 0.f;
 #pragma unroll 4
   for (int r = 0; r < 32; ++r) {
-    const uint32_t at = panel + (row0 + r) * 128, x = (row0 + r) & 7;
-    const uint32_t c1 = lane + 1 + r, c2 = (lane + 33 + r) & 63;  // entry lane + 32; lane or lane + 64
+    const uint32_t c1 = lane + 1 + r, c2 = (lane + 33 + r) & 63;  // diagonal lane + 32; lane or lane + 64
+    const uint32_t row = block + r * 128, swizzle = (r & 7) << 4;
     uint16_t a, b;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(at + (((c1 >> 3) ^ x) << 4) + (c1 & 7) * 2) : "memory");
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(at + (((c2 >> 3) ^ x) << 4) + (c2 & 7) * 2) : "memory");
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(row + ((2 * c1) ^ swizzle)) : "memory");
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(row + ((2 * c2) ^ swizzle)) : "memory");
     sum[1] += __half2float(__ushort_as_half(a));
     const float v = __half2float(__ushort_as_half(b));
-    sum[0] += lane + r >= 31 ? v : 0.f;
-    sum[2] += lane + r >= 31 ? 0.f : v;
+    if (lane + r >= 31)
+      sum[0] += v;
+    else
+      sum[2] += v;
   }
 }
 
-// Sum of one row of it.
-__device__ __forceinline__ float row_sum(uint32_t panel, int row) {
+// Sum of this lane's share of such a block.
+__device__ __forceinline__ float block_sum(uint32_t block, int lane) {
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
   for (int c = 0; c < 8; ++c) {
     uint32_t v[4];
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(panel + sw128_offset(row, c))
+                 : "r"(block + 512 * c + 16 * lane)
                  : "memory");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
