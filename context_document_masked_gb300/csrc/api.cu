@@ -273,11 +273,12 @@ int fcp_plan_upload(const fcp_plan_t* plan, void* dev_buf, int64_t bytes, void* 
 // copies of V ([T][Hkv][d]) and of the received V rows ([R][Hkv][d], R = all
 // shards' remote rows of the plan), the forward's P*V operands; e4m3 copies
 // of Q, K and the received K rows; the tickets (zero between calls) and
-// partial sums of the norm weights' gradients.
+// partial sums of the norm weights' gradients; the biased backward's sums of dS
+// by distance (zero between calls).
 constexpr int64_t kWorkCounterOff = 64;
 
 struct WsLayout {
-  int64_t delta, q16, do16, v16, vb16, q8, k8, kb8, tickets, partial, total;
+  int64_t delta, q16, do16, v16, vb16, q8, k8, kb8, tickets, partial, by_distance, total;
 };
 
 // Header words of the e4m3 Q K^T forward: amax bits of Q and K, then their
@@ -306,7 +307,8 @@ static WsLayout ws_layout(const fcp_dims& d, int64_t remote_rows) {
   w.tickets = w.kb8 + ws_align(R * hkv * dd);
   constexpr int64_t groups = (fcp::kNormRopeMaxCtas + fcp::kNormRopeGroup - 1) / fcp::kNormRopeGroup;
   w.partial = w.tickets + ws_align((1 + groups) * 4);
-  w.total = w.partial + ws_align((fcp::kNormRopeMaxCtas + groups) * 2 * dd * 4);
+  w.by_distance = w.partial + ws_align((fcp::kNormRopeMaxCtas + groups) * 2 * dd * 4);
+  w.total = w.by_distance + ws_align(hq * fcp::kNearDistances * 4);
   return w;
 }
 
@@ -347,10 +349,11 @@ static int check_bias(const fcp_rel_bias* b) {
   return FCP_OK;
 }
 
-static void set_bias(fcp::BiasParams* p, const fcp_rel_bias* b, float* dbias) {
+static void set_bias(fcp::BiasParams* p, const fcp_rel_bias* b, float* dbias, float* by_distance) {
   static_assert(FCP_MAX_BUCKETS == fcp::kMaxBuckets, "bucket count");
   p->bias = b->bias;
   p->dbias = dbias;
+  p->by_distance = by_distance;
   p->n = b->n_buckets;
   std::copy(b->starts, b->starts + b->n_buckets, p->starts);
 }
@@ -459,7 +462,7 @@ static int attn_fwd_impl(const void* q, const void* k, const void* v, const void
   fp.wait_ns = g_wait_ns;
   a.d = dims.d;
   a.num_sms = num_sms();
-  if ((a.has_bias = bias != nullptr)) set_bias(&a.bias, bias, nullptr);
+  if ((a.has_bias = bias != nullptr)) set_bias(&a.bias, bias, nullptr, nullptr);
   return fcp::launch_attn_fwd(a, cs);
 }
 
@@ -639,7 +642,7 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
   bp.wait_ns = g_wait_ns;
   a.d = dims.d;
   a.num_sms = num_sms();
-  if ((a.has_bias = bias != nullptr)) set_bias(&a.bias, bias, dbias);
+  if ((a.has_bias = bias != nullptr)) set_bias(&a.bias, bias, dbias, reinterpret_cast<float*>(wsb + wl.by_distance));
   return fcp::launch_attn_bwd(a, s);
 }
 

@@ -144,7 +144,8 @@ __device__ __forceinline__ StepRows step_rows(const BwdItem& it, int G, int j) {
 // 2-3 (64 threads t) bring into shared memory.
 struct BiasSteps {
   float lse[2], delta[2], win[4];  // the next step's, in registers
-  bool windowed;
+  bool windowed;                   // its tile holds several buckets
+  float* one_bucket = nullptr;     // else its bucket's place in dbias
   BucketRun seen{0, 0, 0};
 
   __device__ __forceinline__ void load(const BwdParams& p, const BiasParams& bp, const Buckets& bk, const BwdItem& it,
@@ -155,6 +156,7 @@ struct BiasSteps {
     const int near = max(first, 0);
     if (near < seen.lo || near >= seen.hi) bucket_run(seen, bk, bp.n, near);
     windowed = first + 254 >= seen.hi;
+    one_bucket = windowed ? nullptr : bp.dbias + (size_t)sr.h * bp.n + seen.bucket;
     const float one = windowed ? 0.f : bias_log2(bias_row, seen.bucket);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -189,44 +191,50 @@ struct BiasSteps {
 
 };
 
-// With a bias: one compute warp's sums of dS by buckets. Its block of a step
-// is 32 key rows x 64 query columns; a block of one bucket adds to a sum held
-// in registers while the bucket and the head stay, the others are summed by
-// diagonals.
-struct BiasSums {
-  BucketRun run{0, 0, 0};
-  float sum = 0.f;       // this lane's share of the run's
-  float* row = nullptr;  // the head's table row
+// With a bias: dS summed by buckets (fp32 sums of the stored fp16 values). A
+// tile of one bucket, as most far from the diagonal are, is summed whole by
+// warps 2-3, who keep the sum while the bucket and the head stay. In the others
+// each compute warp takes its own block, 32 key rows x 64 query columns:
+// near the diagonal, at distances below kNearDistances, the block's diagonals
+// are added to a table by distance (a lane's sums to neighbouring words), which
+// a kernel after this one sums by buckets; farther off they are added by
+// buckets at once.
+struct TileSums {
+  float sum = 0.f;
+  float* at = nullptr;  // the bucket's place in dbias
 
-  __device__ __forceinline__ void flush(int lane) {
-    if (row) add_run(row + run.bucket, sum, lane);
-  }
-  // block: the stored dS (fp16, swizzled); base: distance of its diagonal 0
-  // (column 0, row 31).
-  __device__ __forceinline__ void add(uint32_t block, float* head_row, const Buckets& bk, int n, int base, int lane) {
-    if (base + 94 < 0) return;
-    const int near = max(base, 0);
-    if (row != head_row || near < run.lo || near >= run.hi) {
+  __device__ __forceinline__ void add(uint32_t panel, float* to, int lane) {
+    if (to != at) {
       flush(lane);
-      row = head_row;
-      bucket_run(run, bk, n, near);
+      at = to;
     }
-    __syncwarp();  // the warp's rows are stored
-    if (base + 94 < run.hi) {
-      sum += block_sum(block, lane);
-    } else {
-      float d[3];
-      diagonal_sums(block, lane, d);
-#pragma unroll 1
-      for (int w = 0; w < 3; ++w, base += 32) {
-        add_by_bucket(row, bk.of(n, max(base + lane, 0)), d[0], lane);
-        d[0] = d[1];
-        d[1] = d[2];
-      }
-    }
-    __syncwarp();  // and read, before the next step's are
+    sum += panel_sum(panel, lane);
+  }
+  __device__ __forceinline__ void flush(int lane) {
+    if (at) add_run(at, sum, lane);
   }
 };
+// block: the stored dS; base: distance of its diagonal 0 (column 0, row 31).
+// Out of line, for its registers are the ones that the P and dS loops lack.
+static __device__ __noinline__ void add_block(uint32_t block, int h, const Buckets& bk, const BiasParams& bp, int base,
+                                              int lane) {
+  if (base + 94 < 0) return;
+  __syncwarp();  // the warp's rows are stored
+  float d[3];
+  diagonal_sums(block, lane, d);
+#pragma unroll 1
+  for (int w = 0; w < 3; ++w, base += 32) {
+    const int dist = base + lane;
+    if (base + 31 < kNearDistances) {
+      if (dist >= 0) red_add(bp.by_distance + (size_t)h * kNearDistances + dist, d[0]);
+    } else {
+      add_by_bucket(bp.dbias + (size_t)h * bp.n, bk.of(bp.n, dist), d[0], lane);
+    }
+    d[0] = d[1];
+    d[1] = d[2];
+  }
+  __syncwarp();  // and read, before the next step's are
+}
 
 // TMA bulk reduce-add of a shared-memory tile into global memory.
 __device__ __forceinline__ void tma_reduce_add_3d(const void* tmap, const void* src, int c0, int c1,
@@ -306,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar_dp_full, 1);
     mbar_init(&bar_p_ready, 256);
     mbar_init(&bar_ds_ready, 256);
-    mbar_init(&bar_ds_free, 1);
+    mbar_init(&bar_ds_free, kBias ? 3 : 1);
     mbar_init(&bar_dq_full, 1);
     mbar_init(&bar_dq_free, 128);
     mbar_init(&bar_dkdv_full, 1);
@@ -540,6 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, ovf = false;
     uint4* kv = reinterpret_cast<uint4*>(smem + C::kK);  // K and V tiles are contiguous
     BiasSteps bias;
+    TileSums sums;
+    const uint32_t ds_panel = smem_u32(smem + C::kDS) + (warp - 2) * 16384;
     for (uint32_t k = 0; ok; ++k) {
       int w = 0;
       ok = ring.get(k, w, wc);
@@ -574,10 +584,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // With a bias these warps also follow the unit's steps: LSE, D and the
         // bias window of a step go into shared memory as soon as the compute
-        // warps are done with those of the step before.
+        // warps are done with those of the step before, and the dS tile of a
+        // step of one bucket is summed beside its dK and dQ products, half of
+        // the columns by each warp.
         const int nsteps = G * it.nq;
         for (int j = -1; j < nsteps; ++j) {
           const bool more = j + 1 < nsteps;
+          float* one_bucket = bias.one_bucket;  // of step j
           if (more) bias.load(p, bp, buckets, it, G, j + 1, t);
           if (j < 0) {
             convert();
@@ -601,9 +614,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_delta_full);
           }
+          if (j >= 0) {
+            if (one_bucket) sums.add(ds_panel, one_bucket, lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_ds_free);
+          }
         }
       }
     }
+    if constexpr (kBias) sums.flush(lane);
     if (ovf) atomicOr(p.err, 4);
   } else if (warp < 12) {
     // ------------------------------------------------------------ P and dS
@@ -627,11 +646,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nsteps = G * it.nq;
       const bool key_valid = kr < it.n;
       const int key = it.key0 + kr;
-      BiasSums sums;
       for (int j = 0; j < nsteps; ++j, ++gstep) {
         const uint32_t c = qc + j, s = c & 1;
-        const StepRows sr = step_rows(it, G, j);
-        const int q0 = sr.q0;
+        const int q0 = step_rows(it, G, j).q0;
         const int lim = key - q0 - 64 * half;  // local columns below lim cannot see this key
         // Whole tile below the diagonal with 128 keys: no element needs a mask
         // (query rows past the piece end have LSE = +inf, hence P = 0).
@@ -641,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         const float4* st4 = reinterpret_cast<const float4*>(stat + (kBias ? 0 : s * 256) + 64 * half);
+        bool windowed = false;  // bias: the tile holds several buckets
         uint32_t pk[32];
         {
           // Both 32-column halves of this group's S^T in flight together.
@@ -651,7 +669,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kBias) {
             // A tile of one bucket has its bias in the LSE; the others add the
             // window (entry column + 127 - row) to the raw scores.
-            if (*reinterpret_cast<volatile int*>(&windowed_sh)) {
+            windowed = *reinterpret_cast<volatile int*>(&windowed_sh) != 0;
+            if (windowed) {
               const float* w = stat + 256 + 64 * half + 127 - kr;
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
@@ -727,15 +746,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(&bar_ds_ready);
-        // The bias's gradient: the dS just stored (fp16, the operands of the
-        // dK and dQ products) read back and added in fp32, once the MMA thread
-        // has been let go on.
-        if constexpr (kBias)
-          sums.add(ds_panel + 4096 * (warp & 3), bp.dbias + (size_t)sr.h * bp.n, buckets, bp.n,
-                   q0 + 64 * half - it.key0 - 32 * (warp & 3) - 31, lane);
+        if constexpr (kBias) {
+          if (windowed)
+            add_block(ds_panel + 4096 * (warp & 3), step_rows(it, G, j).h, buckets, bp,
+                      q0 + 64 * half - it.key0 - 32 * (warp & 3) - 31, lane);
+        }
       }
       if (!ok) break;
-      if constexpr (kBias) sums.flush(lane);
       qc += nsteps;
       // dV (columns-0 group) or dK (columns-64 group) of this key tile ->
       // global rows: 32-column chunks staged in this group's half of the dS
@@ -743,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // layout of a [128 rows][32 fp32] TMA box) and reduce-added by one
       // thread with TMA. Rows of keys past the tile hold zeros.
       ok = mbar_wait(&bar_dkdv_full, items & 1, wc);
+      if constexpr (kBias) ok = ok && mbar_wait(&bar_ds_free, (gstep - 1) & 1, wc);  // the last dS is summed too
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc_fence_after();
       const uint32_t src_col = lane_base + (half == 0 ? C::kColDV : C::kColDK);
@@ -880,6 +898,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
+// dbias += the near distances' sums, which are set back to zero. A block a
+// head, a thread a distance, then a thread a bucket.
+static __global__ void __launch_bounds__(kNearDistances) near_sums_kernel(const __grid_constant__ BiasParams bp) {
+  __shared__ float by[kNearDistances];
+  const int h = blockIdx.x, t = threadIdx.x;
+  float* at = bp.by_distance + (size_t)h * kNearDistances + t;
+  by[t] = *at;
+  *at = 0.f;
+  __syncthreads();
+  if (t < bp.n) {
+    const int end = t + 1 < bp.n ? min(bp.starts[t + 1], kNearDistances) : kNearDistances;
+    float v = 0.f;
+    for (int x = bp.starts[t]; x < end; ++x) v += by[x];
+    bp.dbias[(size_t)h * bp.n + t] += v;
+  }
+}
+
 template <int D, class Bias>
 static int launch_bwd_impl(const BwdLaunch& a, const Bias& bias, cudaStream_t st) {
   using C = BwdCfg<D>;
@@ -901,6 +936,7 @@ static int launch_bwd_impl(const BwdLaunch& a, const Bias& bias, cudaStream_t st
   p.order_block = grid;
   attn_bwd_kernel<D, Bias><<<grid, kThreads, C::kSmem, st>>>(a.tm_q, a.tm_do, a.tm_k, a.tm_v, a.tm_kb,
                                                       a.tm_vb, a.tm_dq, a.tm_dk, a.tm_dv, p, bias);
+  if constexpr (std::is_same_v<Bias, BiasParams>) near_sums_kernel<<<p.hq, kNearDistances, 0, st>>>(bias);
   return cudaGetLastError() == cudaSuccess ? FCP_OK : FCP_ERR_CUDA;
 }
 

@@ -100,6 +100,12 @@ __device__ __forceinline__ const float4* window_row(const float* win, int lane) 
   return reinterpret_cast<const float4*>(win + k * kWindowCopy + first - k);
 }
 
+// (An atomicAdd through a pointer of unknown space brings code for shared
+// memory with it.)
+__device__ __forceinline__ void red_add(float* at, float v) {
+  asm volatile("red.global.add.f32 [%0], %1;" ::"l"(__cvta_generic_to_global(at)), "f"(v) : "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
@@ -108,8 +114,9 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Adds the warp's sum of v to *at and sets v back to zero.
 __device__ __forceinline__ void add_run(float* at, float& v, int lane) {
+  if (!__any_sync(0xffffffffu, v != 0.f)) return;
   const float sum = warp_sum(v);
-  if (lane == 0 && sum != 0.f) atomicAdd(at, sum);
+  if (lane == 0 && sum != 0.f) red_add(at, sum);
   v = 0.f;
 }
 
@@ -123,48 +130,78 @@ __device__ __forceinline__ void add_by_bucket(float* row, int bucket, float v, i
     if (lane >= m && b == bucket) v += up;
   }
   const int next = __shfl_down_sync(0xffffffffu, bucket, 1);
-  if ((lane == 31 || next != bucket) && v != 0.f) atomicAdd(row + bucket, v);
+  if ((lane == 31 || next != bucket) && v != 0.f) red_add(row + bucket, v);
 }
 
-// Sums along the diagonals of 32 rows x 64 columns of dS (fp16, rows of 128
-// bytes in the 128-byte swizzle): this lane's diagonals lane, lane + 32 and
-// lane + 64, diagonal y the elements with column - row = y - 31. The lanes of
-// a warp read neighbouring columns of one row at a time.
-__device__ __forceinline__ void diagonal_sums(uint32_t block, int lane, float (&sum)[3]) {
-  sum[0] = sum[1] = sum[2] = 0.f;
-#pragma unroll 4
-  for (int r = 0; r < 32; ++r) {
-    const uint32_t c1 = lane + 1 + r, c2 = (lane + 33 + r) & 63;  // diagonal lane + 32; lane or lane + 64
-    const uint32_t row = block + r * 128, swizzle = (r & 7) << 4;
-    uint16_t a, b;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(row + ((2 * c1) ^ swizzle)) : "memory");
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(row + ((2 * c2) ^ swizzle)) : "memory");
-    sum[1] += __half2float(__ushort_as_half(a));
-    const float v = __half2float(__ushort_as_half(b));
-    if (lane + r >= 31)
-      sum[0] += v;
-    else
-      sum[2] += v;
-  }
+// Blocks of dS: 32 rows (keys) x 64 columns (queries), fp16,
+// rows of 128 bytes in the 128-byte swizzle. Diagonal y holds the elements
+// with column - row = y - 31.
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+// sum += one of a pair of fp16 values (one instruction: the fp32 add takes the
+// 16-bit operand).
+__device__ __forceinline__ void add_lo(float& sum, uint32_t pair) {
+  asm("add.f32.f16 %0, %1, %0;" : "+f"(sum) : "h"((uint16_t)pair));
+}
+__device__ __forceinline__ void add_hi(float& sum, uint32_t pair) {
+  asm("add.f32.f16 %0, %1, %0;" : "+f"(sum) : "h"((uint16_t)(pair >> 16)));
 }
 
-// Sum of this lane's share of such a block.
-__device__ __forceinline__ float block_sum(uint32_t block, int lane) {
+// Sum of a 128 x 64 panel of dS, in shares of the lanes. A short loop: what it
+// fetches counts for more than its operations.
+__device__ __forceinline__ float panel_sum(uint32_t panel, int lane) {
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < 32; ++c) {
     uint32_t v[4];
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                 : "r"(block + 512 * c + 16 * lane)
-                 : "memory");
+    ld_shared_v4(panel + 512 * c + 16 * lane, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-      sum[i] += f.x + f.y;
+      add_lo(sum[i], v[i]);
+      add_hi(sum[i], v[i]);
     }
   }
   return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+}
+
+// Sums along the diagonals: this lane's lane, lane + 32 and lane + 64. Every
+// lane reads its row and hands each pair of columns to the lane that keeps its
+// first element's diagonal; the second element's is the next one, kept apart
+// (b) until the end.
+__device__ __forceinline__ void diagonal_sums(uint32_t block, int lane, float (&sum)[3]) {
+  float a_lo = 0.f, a_hi = 0.f, b_lo = 0.f, b_hi = 0.f, b_last = 0.f;
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll 2
+    for (int c8 = 0; c8 < 4; ++c8) {
+      uint32_t v[4];
+      ld_shared_v4(block + sw128_offset(lane, 4 * half + c8), v);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int c = 8 * c8 + 2 * m;
+        const uint32_t got = __shfl_sync(0xffffffffu, v[m], c + 31 - lane);
+        if (lane >= c) {
+          add_lo(a_lo, got);
+          add_hi(b_lo, got);
+        } else {
+          add_lo(a_hi, got);
+          add_hi(b_hi, got);
+        }
+      }
+    }
+    // The low entries are complete; the high ones are the next half's low ones.
+    sum[0] = sum[1];
+    sum[1] = a_lo + __shfl_sync(0xffffffffu, lane == 31 ? b_last : b_lo, lane + 31);
+    b_last = b_lo;
+    a_lo = a_hi;
+    b_lo = b_hi;
+    a_hi = b_hi = 0.f;
+  }
+  sum[2] = a_lo + __shfl_sync(0xffffffffu, lane == 31 ? b_last : b_lo, lane + 31);
 }
 
 }  // namespace dev
