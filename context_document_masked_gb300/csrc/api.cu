@@ -308,7 +308,7 @@ static WsLayout ws_layout(const fcp_dims& d, int64_t remote_rows) {
   constexpr int64_t groups = (fcp::kNormRopeMaxCtas + fcp::kNormRopeGroup - 1) / fcp::kNormRopeGroup;
   w.partial = w.tickets + ws_align((1 + groups) * 4);
   w.by_distance = w.partial + ws_align((fcp::kNormRopeMaxCtas + groups) * 2 * dd * 4);
-  w.total = w.by_distance + ws_align(hq * fcp::kNearDistances * 4);
+  w.total = w.by_distance + ws_align(hq * fcp::kTableDistances * 4);
   return w;
 }
 

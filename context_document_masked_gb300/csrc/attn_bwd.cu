@@ -194,11 +194,10 @@ struct BiasSteps {
 // With a bias: dS summed by buckets (fp32 sums of the stored fp16 values). A
 // tile of one bucket, as most far from the diagonal are, is summed whole by
 // warps 2-3, who keep the sum while the bucket and the head stay. In the others
-// each compute warp takes its own block, 32 key rows x 64 query columns:
-// near the diagonal, at distances below kNearDistances, the block's diagonals
-// are added to a table by distance (a lane's sums to neighbouring words), which
-// a kernel after this one sums by buckets; farther off they are added by
-// buckets at once.
+// each compute warp takes its own block, 32 key rows x 64 query columns, and
+// adds its diagonals to a table by distance (a lane's sums to neighbouring
+// words), which a kernel after this one sums by buckets. Distances that the
+// table does not hold are added by buckets at once.
 struct TileSums {
   float sum = 0.f;
   float* at = nullptr;  // the bucket's place in dbias
@@ -225,8 +224,8 @@ static __device__ __noinline__ void add_block(uint32_t block, int h, const Bucke
 #pragma unroll 1
   for (int w = 0; w < 3; ++w, base += 32) {
     const int dist = base + lane;
-    if (base + 31 < kNearDistances) {
-      if (dist >= 0) red_add(bp.by_distance + (size_t)h * kNearDistances + dist, d[0]);
+    if (base + 31 < kTableDistances) {
+      if (dist >= 0) red_add(bp.by_distance + (size_t)h * kTableDistances + dist, d[0]);
     } else {
       add_by_bucket(bp.dbias + (size_t)h * bp.n, bk.of(bp.n, dist), d[0], lane);
     }
@@ -898,20 +897,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-// dbias += the near distances' sums, which are set back to zero. A block a
-// head, a thread a distance, then a thread a bucket.
-static __global__ void __launch_bounds__(kNearDistances) near_sums_kernel(const __grid_constant__ BiasParams bp) {
-  __shared__ float by[kNearDistances];
-  const int h = blockIdx.x, t = threadIdx.x;
-  float* at = bp.by_distance + (size_t)h * kNearDistances + t;
-  by[t] = *at;
-  *at = 0.f;
+// dbias += the table's sums by distance, which are set back to zero: one block
+// a head, a warp a bucket. Blocks of dS reach 255 distances past the last
+// bucket's first.
+constexpr int kTableThreads = 512;
+static __global__ void __launch_bounds__(kTableThreads) table_sums_kernel(const __grid_constant__ BiasParams bp) {
+  __shared__ float by[kTableDistances];
+  const int used = min(min(bp.starts[bp.n - 1], kTableDistances) + 256, kTableDistances);
+  float* table = bp.by_distance + (size_t)blockIdx.x * kTableDistances;
+  for (int x = threadIdx.x; x < used; x += kTableThreads) {
+    by[x] = table[x];
+    table[x] = 0.f;
+  }
   __syncthreads();
-  if (t < bp.n) {
-    const int end = t + 1 < bp.n ? min(bp.starts[t + 1], kNearDistances) : kNearDistances;
+  const int lane = threadIdx.x & 31;
+  for (int b = threadIdx.x >> 5; b < bp.n; b += kTableThreads / 32) {
+    const int end = b + 1 < bp.n ? min(bp.starts[b + 1], used) : used;
     float v = 0.f;
-    for (int x = bp.starts[t]; x < end; ++x) v += by[x];
-    bp.dbias[(size_t)h * bp.n + t] += v;
+    for (int x = bp.starts[b] + lane; x < end; x += 32) v += by[x];
+    v = warp_sum(v);
+    if (lane == 0) bp.dbias[(size_t)blockIdx.x * bp.n + b] += v;
   }
 }
 
@@ -936,7 +941,7 @@ static int launch_bwd_impl(const BwdLaunch& a, const Bias& bias, cudaStream_t st
   p.order_block = grid;
   attn_bwd_kernel<D, Bias><<<grid, kThreads, C::kSmem, st>>>(a.tm_q, a.tm_do, a.tm_k, a.tm_v, a.tm_kb,
                                                       a.tm_vb, a.tm_dq, a.tm_dk, a.tm_dv, p, bias);
-  if constexpr (std::is_same_v<Bias, BiasParams>) near_sums_kernel<<<p.hq, kNearDistances, 0, st>>>(bias);
+  if constexpr (std::is_same_v<Bias, BiasParams>) table_sums_kernel<<<p.hq, kTableThreads, 0, st>>>(bias);
   return cudaGetLastError() == cudaSuccess ? FCP_OK : FCP_ERR_CUDA;
 }
 

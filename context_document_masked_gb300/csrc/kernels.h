@@ -52,11 +52,11 @@ struct FwdParams {
 // holds the distances from starts[u] to starts[u + 1] - 1 (the last one all
 // from starts[u] on).
 constexpr int kMaxBuckets = 128;
-constexpr int kNearDistances = 256;
+constexpr int kTableDistances = 8192;
 struct BiasParams {
   const float* bias;       // [hq][n]
   float* dbias;            // backward: [hq][n], accumulated
-  float* by_distance;      // backward: [hq][kNearDistances] sums of dS, zero at launch and after it
+  float* by_distance;      // backward: [hq][kTableDistances] sums of dS, zero at launch and after it
   int32_t n;
   int32_t starts[kMaxBuckets];
 };
