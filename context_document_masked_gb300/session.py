@@ -14,6 +14,8 @@ from . import fcp
 def _on_stream(stream):
     """The stream of a call (a torch stream, a raw handle or None: the current
     one) as a context: what torch does for the call runs in its order."""
+    if stream is None:
+        return fcp._HERE_CTX
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream)
@@ -123,13 +125,19 @@ class CPAttention:
         with _on_stream(stream):
             if dq is None:
                 dq = torch.empty(self.T, self.hq, self.d, dtype=torch.float32, device=self.device)
-            new = [torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device) if x is None else x
-                   for x in (dk, dv)]
-            new.append(torch.zeros_like(bias) if dbias is None else dbias)
-            for given, x in zip((dk, dv, dbias), new):
-                if given is not None and zero_grads:
-                    x.zero_()
-            dk, dv, dbias = new
+            if dk is None and dv is None and dbias is None:  # one fill for the three
+                n = self.T * self.hkv * self.d
+                new = torch.zeros(2 * n + bias.numel(), dtype=torch.float32, device=self.device)
+                dk, dv = new[:2 * n].view(2, self.T, self.hkv, self.d)
+                dbias = new[2 * n:].view(bias.shape)
+            else:
+                given = [x for x in (dk, dv, dbias) if x is not None]
+                dk, dv = (torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device) if x is None else x
+                          for x in (dk, dv))
+                dbias = torch.zeros_like(bias) if dbias is None else dbias
+                if zero_grads:
+                    for x in given:
+                        x.zero_()
         fcp.attn_bwd_bias(q, k, v, self.kbuf, self.vbuf, bias, starts, out, lse, dout, self.dplan, shard, dq, dk, dv, dbias,
                           self.ws, scale=self.scale, stream=stream)
         return dq, dk, dv, dbias
@@ -180,10 +188,10 @@ class CPAttention:
             dq_in = rows(self.hq) if dq_in is None else dq_in
             dk_in = rows(self.hkv) if dk_in is None else dk_in
             dv_in = rows(self.hkv) if dv_in is None and dv is not None else dv_in
-            if dwq is None and wq is not None:
-                dwq = torch.zeros(self.d, dtype=torch.float32, device=self.device)
-            if dwk is None and wk is not None:
-                dwk = torch.zeros(self.d, dtype=torch.float32, device=self.device)
+            if (dwq is None and wq is not None) or (dwk is None and wk is not None):
+                new = torch.zeros(2, self.d, dtype=torch.float32, device=self.device)
+                dwq = new[0] if dwq is None and wq is not None else dwq
+                dwk = new[1] if dwk is None and wk is not None else dwk
         fcp.qk_norm_rope_bwd(dq, dk, dv, q_in, k_in, self.dplan, shard, dq_in, dk_in, dv_in, dwq, dwk, self.ws, wq=wq,
                              wk=wk, inv_freq=inv_freq, norm=norm, eps=eps, interleaved=interleaved, stream=stream)
         return dq_in, dk_in, dv_in, dwq, dwk
