@@ -14,63 +14,96 @@
 //   dx = r (g - x r^2 mean(g x)),  dw = sum over tokens and heads of z x r.
 //
 // Angles. p inv_freq / (2 pi) is taken modulo 1 exactly in integers: each
-// frequency becomes a 64-bit fixed-point fraction of a turn once per warp,
+// frequency becomes a 64-bit fixed-point fraction of a turn once per CTA (by
+// every warp, the few fp64 units made it half of a small call's time),
 // and the fraction after p positions is the low 64 bits of an integer
 // product, so a position of 10^6 is turned as exactly as position 1 (a
 // product in fp32 would be off by up to 0.03 rad there).
 //
-// Layout. D / 16 lanes hold one head, 16 values each as two 16-byte chunks
+// Layout. D / 8 lanes hold one head, eight values each as two chunks of four
 // chosen so that both values of every pair are in one lane, in either pair
-// order; a warp holds 4 heads (d = 128) or 8 (d = 64) at a time and walks the
-// heads of one token, whose angles it computes once: lane i those of pairs
-// 2i and 2i + 1, handed round by shuffles.
+// order; a warp holds 2 heads (d = 128) or 4 (d = 64) at a time, a pass, and
+// walks the heads of one token, whose angles it computes once: lane i those of
+// pairs 2i and 2i + 1, handed round by shuffles.
 //
-// Bound: device memory, one read of each input and one write of each output.
+// Bound: device memory, one read of each input and one write of each output,
+// and its latency: four passes are loaded before the first is worked on, and
+// the arithmetic runs on pairs of values (f32x2) to keep the registers that
+// this takes. 65536 tokens of 64 + 8 + 8 heads of 128: 419 us, 6.40 TB/s (0.96
+// of the copy rate measured on this part); gradient of 32768 tokens of 32 + 8
+// + 8: 261 us, 5.91 TB/s (0.88). Slower: sixteen values a lane (gradient 287
+// us, two passes do not fit), asynchronous copies into shared memory (485 and
+// 370 us, for their instructions), units looked up ahead by the CTA (the same).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "sm103.cuh"
 
 namespace fcp {
+
+using namespace dev;
 
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kE = 8;  // values of a head in a lane
+// Passes over the heads in flight, and CTAs an SM, for the registers that both
+// take (a few spilled ones cost the gradient a quarter of its speed).
+constexpr int kFwdPasses = 4, kFwdCtas = 4, kBwdPasses = 4, kBwdCtas = 2;
 
-__device__ __forceinline__ float lo16(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float hi16(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
+// Bf16 pairs as fp32 pairs, and back.
+__device__ __forceinline__ uint64_t unpack2(uint32_t v) {
+  return f2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
-__device__ __forceinline__ void unpack8(const uint4& v, float* x) {
-  x[0] = lo16(v.x), x[1] = hi16(v.x), x[2] = lo16(v.y), x[3] = hi16(v.y);
-  x[4] = lo16(v.z), x[5] = hi16(v.z), x[6] = lo16(v.w), x[7] = hi16(v.w);
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+  float lo, hi;
+  f2_split(x, lo, hi);
+  return pack_bf16(lo, hi);
 }
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
-
-// Where a lane's two chunks lie inside a head. Lanes below n_rot hold chunk l
-// of the first half of the rotated dimensions and chunk l of the second half
-// (the pairs (i, i + rot / 2) and the pairs (2i, 2i + 1) are then both inside
-// a lane); the others two neighbouring chunks of the rest.
+__device__ __forceinline__ float f2_sum(uint64_t a, uint64_t b) {
+  float lo, hi;
+  f2_split(f2_add(a, b), lo, hi);
+  return lo + hi;
+}
+// Where a lane's two chunks of kE / 2 values lie inside a head. The lanes of
+// the first rot_dim values hold chunk l of the first half of the rotated
+// dimensions and chunk l of the second half (the pairs (i, i + rot / 2) and the
+// pairs (2i, 2i + 1) are then both inside a lane); the others two neighbouring
+// chunks of the rest.
 struct Lane {
   int l, head, off_a, off_b;
   bool turns;
 };
 template <int D>
 __device__ __forceinline__ Lane lane_of(int lane, int rot_dim) {
-  constexpr int kPerHead = D / 16;
-  const int n_rot = rot_dim / 16;
   Lane x;
-  x.l = lane % kPerHead;
-  x.head = lane / kPerHead;
-  x.turns = x.l < n_rot;
-  x.off_a = x.turns ? 8 * x.l : 16 * x.l;
-  x.off_b = x.turns ? rot_dim / 2 + 8 * x.l : 16 * x.l + 8;
+  x.l = lane % (D / kE);
+  x.head = lane / (D / kE);
+  x.turns = kE * x.l < rot_dim;
+  x.off_a = x.turns ? kE / 2 * x.l : kE * x.l;
+  x.off_b = x.turns ? (rot_dim + kE * x.l) / 2 : kE * x.l + kE / 2;
   return x;
+}
+
+// A lane's pairs (chunk a's, then chunk b's): bf16 as stored, and fp32.
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16* at, const Lane& ln, uint32_t (&v)[kE / 2]) {
+  const uint2 a = *reinterpret_cast<const uint2*>(at + ln.off_a), b = *reinterpret_cast<const uint2*>(at + ln.off_b);
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* at, const Lane& ln, const uint64_t (&x)[kE / 2]) {
+  *reinterpret_cast<uint2*>(at + ln.off_a) = make_uint2(pack2(x[0]), pack2(x[1]));
+  *reinterpret_cast<uint2*>(at + ln.off_b) = make_uint2(pack2(x[2]), pack2(x[3]));
+}
+__device__ __forceinline__ void load_f32(const float* at, const Lane& ln, uint64_t (&x)[kE / 2]) {
+  const float4 a = *reinterpret_cast<const float4*>(at + ln.off_a), b = *reinterpret_cast<const float4*>(at + ln.off_b);
+  x[0] = f2(a.x, a.y), x[1] = f2(a.z, a.w), x[2] = f2(b.x, b.y), x[3] = f2(b.z, b.w);
 }
 
 // inv_freq (radians a position) as a fraction of a turn, in units of 2^-64.
@@ -79,19 +112,19 @@ __device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
   return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
 }
 
-// Cosines and sines of this lane's eight pairs at position `pos`; f0 and f1
-// are the frequencies of pairs 2 * lane and 2 * lane + 1.
+// Cosines and sines of this lane's pairs at position `pos`; f0 and f1 are the
+// frequencies of pairs 2 * lane and 2 * lane + 1.
 template <bool INTER>
-__device__ __forceinline__ void row_angles(uint32_t pos, uint64_t f0, uint64_t f1, const Lane& ln, int n_rot,
-                                           float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ void row_angles(uint32_t pos, uint64_t f0, uint64_t f1, const Lane& ln, int rot_dim,
+                                           float (&c)[kE / 2], float (&s)[kE / 2]) {
   const float h0 = (float)(int32_t)((f0 * pos) >> 32) * 0x1p-31f;  // half turns, in [-1, 1]
   const float h1 = (float)(int32_t)((f1 * pos) >> 32) * 0x1p-31f;
   float c0, s0, c1, s1;
   sincospif(h0, &s0, &c0);
   sincospif(h1, &s1, &c1);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int src = INTER ? (u < 2 ? 2 * ln.l + u : 2 * n_rot + 2 * ln.l + u - 2) : 4 * ln.l + u;
+  for (int u = 0; u < kE / 4; ++u) {
+    const int src = !INTER ? kE / 4 * ln.l + u : u < kE / 8 ? kE / 8 * ln.l + u : rot_dim / 8 + kE / 8 * ln.l + u - kE / 8;
     const float ca = __shfl_sync(0xffffffffu, c0, src), cb = __shfl_sync(0xffffffffu, c1, src);
     const float sa = __shfl_sync(0xffffffffu, s0, src), sb = __shfl_sync(0xffffffffu, s1, src);
     c[2 * u] = ln.turns ? ca : 1.f;
@@ -101,23 +134,35 @@ __device__ __forceinline__ void row_angles(uint32_t pos, uint64_t f0, uint64_t f
   }
 }
 
-// The sixteen values x[0..7] (chunk a), x[8..15] (chunk b) turned in place:
-// forwards for kSign = 1, backwards for -1.
+// The kE values of chunk a (the first kE / 4 pairs of registers) and chunk b
+// turned in place: forwards for kSign = 1, backwards for -1.
 template <bool INTER, int kSign>
-__device__ __forceinline__ void turn16(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+__device__ __forceinline__ void turn(uint64_t (&x)[kE / 2], const float (&c)[kE / 2], const float (&s)[kE / 2]) {
+  if constexpr (INTER) {  // pairs (2i, 2i + 1)
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int i = INTER ? 2 * e : e, k = INTER ? 2 * e + 1 : 8 + e;
-    const float a = x[i], b = x[k], sn = kSign * s[e];
-    x[i] = a * c[e] - b * sn;
-    x[k] = a * sn + b * c[e];
+    for (int e = 0; e < kE / 2; ++e) {
+      float a, b;
+      f2_split(x[e], a, b);
+      const float sn = kSign * s[e];
+      x[e] = f2(a * c[e] - b * sn, a * sn + b * c[e]);
+    }
+  } else {  // value i of chunk a with value i of chunk b
+#pragma unroll
+    for (int i = 0; i < kE / 4; ++i) {
+      const uint64_t c2 = f2(c[2 * i], c[2 * i + 1]), s2 = f2(s[2 * i], s[2 * i + 1]);
+      const uint64_t n2 = f2(-s[2 * i], -s[2 * i + 1]);
+      const uint64_t a = x[i], b = x[kE / 4 + i];
+      x[i] = f2_fma(b, kSign > 0 ? n2 : s2, f2_mul(a, c2));
+      x[kE / 4 + i] = f2_fma(a, kSign > 0 ? s2 : n2, f2_mul(b, c2));
+    }
   }
 }
 
-template <int D>
+// Sum over the N lanes of a head.
+template <int N>
 __device__ __forceinline__ float head_sum(float v) {
 #pragma unroll
-  for (int m = 1; m < D / 16; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  for (int m = 1; m < N; m <<= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
 }
 
@@ -151,62 +196,61 @@ __device__ __forceinline__ Rows unit_rows(const NormRopeParams& p, int u) {
 // ---------------------------------------------------------------- forward
 template <int D, bool INTER>
 __device__ __forceinline__ void heads_forward(const __nv_bfloat16* in, __nv_bfloat16* out, int n_heads, const float* w,
-                                              const Lane& ln, const float (&c)[8], const float (&s)[8],
+                                              const Lane& ln, const float (&c)[kE / 2], const float (&s)[kE / 2],
                                               const NormRopeParams& p) {
-  constexpr int kHeads = 512 / D;  // heads a warp holds at a time
-  float wl[16];
+  constexpr int kHeads = 32 * kE / D;  // heads a warp holds at a time
+  for (int h0 = 0; h0 < n_heads; h0 += kFwdPasses * kHeads) {
+    uint32_t v[kFwdPasses][kE / 2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) wl[e] = w[ln.off_a + e], wl[8 + e] = w[ln.off_b + e];
-  for (int h0 = 0; h0 < n_heads; h0 += 2 * kHeads) {
-    uint4 a[2], b[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kFwdPasses; ++u) {
       const int h = h0 + u * kHeads + ln.head;
-      a[u] = b[u] = make_uint4(0, 0, 0, 0);
-      if (h < n_heads) {
-        a[u] = *reinterpret_cast<const uint4*>(in + (size_t)h * D + ln.off_a);
-        b[u] = *reinterpret_cast<const uint4*>(in + (size_t)h * D + ln.off_b);
-      }
+#pragma unroll
+      for (int i = 0; i < kE / 2; ++i) v[u][i] = 0;
+      if (h < n_heads) load_bf16(in + (size_t)h * D, ln, v[u]);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kFwdPasses; ++u) {
+      if (u > 0 && h0 + u * kHeads >= n_heads) break;
       const int h = h0 + u * kHeads + ln.head;
-      float x[16];
-      unpack8(a[u], x);
-      unpack8(b[u], x + 8);
+      uint64_t x[kE / 2];
+#pragma unroll
+      for (int i = 0; i < kE / 2; ++i) x[i] = unpack2(v[u][i]);
       if (p.norm) {
-        float ss = 0.f;
+        uint64_t sa = 0, sb = 0, wl[kE / 2];
+        load_f32(w, ln, wl);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-        const float r = rsqrtf(head_sum<D>(ss) * (1.f / D) + p.eps);
+        for (int i = 0; i < kE / 4; ++i) {
+          sa = f2_fma(x[i], x[i], sa);
+          sb = f2_fma(x[kE / 4 + i], x[kE / 4 + i], sb);
+        }
+        const float r = rsqrtf(head_sum<D / kE>(f2_sum(sa, sb)) * (1.f / D) + p.eps);
+        const uint64_t r2 = f2(r, r);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = x[e] * r * wl[e];
+        for (int i = 0; i < kE / 2; ++i) x[i] = f2_mul(f2_mul(x[i], r2), wl[i]);
       }
-      turn16<INTER, 1>(x, c, s);
-      if (h < n_heads) {
-        *reinterpret_cast<uint4*>(out + (size_t)h * D + ln.off_a) = pack8(x);
-        *reinterpret_cast<uint4*>(out + (size_t)h * D + ln.off_b) = pack8(x + 8);
-      }
+      turn<INTER, 1>(x, c, s);
+      if (h < n_heads) store_bf16(out + (size_t)h * D, ln, x);
     }
   }
 }
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParams p) {
-  __shared__ float w[2][D];
+__global__ void __launch_bounds__(kThreads, kFwdCtas) norm_rope_kernel(const NormRopeParams p) {
+  __shared__ __align__(16) float w[2][D];
+  __shared__ uint64_t turns[D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) w[i / D][i % D] = load_w(i < D ? p.wq : p.wk, p.w_f32, i % D);
+  if (threadIdx.x < D / 2)
+    turns[threadIdx.x] = 2 * threadIdx.x < p.rot_dim ? turn_fraction(__ldg(p.inv_freq + threadIdx.x)) : 0;
   __syncthreads();
   const Lane ln = lane_of<D>(lane, p.rot_dim);
-  const int n_rot = p.rot_dim / 16, n_pairs = p.rot_dim / 2;
-  const uint64_t f0 = 2 * lane < n_pairs ? turn_fraction(__ldg(p.inv_freq + 2 * lane)) : 0;
-  const uint64_t f1 = 2 * lane < n_pairs ? turn_fraction(__ldg(p.inv_freq + 2 * lane + 1)) : 0;
+  const uint64_t f0 = 2 * lane < D / 2 ? turns[2 * lane] : 0, f1 = 2 * lane < D / 2 ? turns[2 * lane + 1] : 0;
   for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
     const Rows rows = unit_rows(p, u);
     for (int i = warp; i < rows.n; i += kWarps) {
       const size_t t = rows.first + i;
-      float c[8], s[8];
-      row_angles<INTER>(rows.pos + i, f0, f1, ln, n_rot, c, s);
+      float c[kE / 2], s[kE / 2];
+      row_angles<INTER>(rows.pos + i, f0, f1, ln, p.rot_dim, c, s);
       heads_forward<D, INTER>(p.q_in + t * p.q_in_stride, p.q + t * p.hq * D, p.hq, w[0], ln, c, s, p);
       heads_forward<D, INTER>(p.k_in + t * p.k_in_stride, p.k + t * p.hkv * D, p.hkv, w[1], ln, c, s, p);
       if (p.v) {
@@ -219,54 +263,54 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeParam
 }
 
 // --------------------------------------------------------------- backward
-// One token's heads: dx written, z x r added to acc[16] (this lane's dims).
+// One token's heads: dx written, z x r added to acc (this lane's dims).
 template <int D, bool INTER>
 __device__ __forceinline__ void heads_backward(const float* dy, const __nv_bfloat16* in, __nv_bfloat16* dx, int n_heads,
-                                               const float* w, float (&acc)[16], const Lane& ln, const float (&c)[8],
-                                               const float (&s)[8], const NormRopeParams& p) {
-  constexpr int kHeads = 512 / D;
-  for (int h0 = 0; h0 < n_heads; h0 += kHeads) {
-    const int h = h0 + ln.head;
-    float z[16], x[16];
+                                               const float* w, uint64_t (&acc)[kE / 2], const Lane& ln,
+                                               const float (&c)[kE / 2], const float (&s)[kE / 2],
+                                               const NormRopeParams& p) {
+  constexpr int kHeads = 32 * kE / D;
+  for (int h0 = 0; h0 < n_heads; h0 += kBwdPasses * kHeads) {
+    uint64_t zz[kBwdPasses][kE / 2];
+    uint32_t v[kBwdPasses][kE / 2];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) z[e] = x[e] = 0.f;
-    if (h < n_heads) {
-      const float4* ga = reinterpret_cast<const float4*>(dy + (size_t)h * D + ln.off_a);
-      const float4* gb = reinterpret_cast<const float4*>(dy + (size_t)h * D + ln.off_b);
+    for (int u = 0; u < kBwdPasses; ++u) {
+      const int h = h0 + u * kHeads + ln.head;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 va = ga[i], vb = gb[i];
-        z[4 * i] = va.x, z[4 * i + 1] = va.y, z[4 * i + 2] = va.z, z[4 * i + 3] = va.w;
-        z[8 + 4 * i] = vb.x, z[9 + 4 * i] = vb.y, z[10 + 4 * i] = vb.z, z[11 + 4 * i] = vb.w;
+      for (int i = 0; i < kE / 2; ++i) zz[u][i] = v[u][i] = 0;
+      if (h < n_heads) {
+        load_f32(dy + (size_t)h * D, ln, zz[u]);
+        if (p.norm) load_bf16(in + (size_t)h * D, ln, v[u]);
       }
+    }
+#pragma unroll
+    for (int u = 0; u < kBwdPasses; ++u) {
+      if (u > 0 && h0 + u * kHeads >= n_heads) break;
+      const int h = h0 + u * kHeads + ln.head;
+      uint64_t(&z)[kE / 2] = zz[u];
+      turn<INTER, -1>(z, c, s);
       if (p.norm) {
-        unpack8(*reinterpret_cast<const uint4*>(in + (size_t)h * D + ln.off_a), x);
-        unpack8(*reinterpret_cast<const uint4*>(in + (size_t)h * D + ln.off_b), x + 8);
-      }
-    }
-    turn16<INTER, -1>(z, c, s);
-    if (p.norm) {
-      float ss = 0.f, gx = 0.f;
+        uint64_t x[kE / 2], wl[kE / 2];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float g = z[e] * w[(e < 8 ? ln.off_a : ln.off_b - 8) + e];
-        ss = fmaf(x[e], x[e], ss);
-        gx = fmaf(g, x[e], gx);
-      }
-      ss = head_sum<D>(ss);
-      gx = head_sum<D>(gx);
-      const float r = rsqrtf(ss * (1.f / D) + p.eps);
-      const float m = r * r * (gx * (1.f / D));
+        for (int i = 0; i < kE / 2; ++i) x[i] = unpack2(v[u][i]);
+        load_f32(w, ln, wl);
+        uint64_t sq = 0, gx2 = 0;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float g = z[e] * w[(e < 8 ? ln.off_a : ln.off_b - 8) + e];
-        acc[e] = fmaf(z[e], x[e] * r, acc[e]);
-        z[e] = r * (g - x[e] * m);
+        for (int i = 0; i < kE / 2; ++i) {
+          sq = f2_fma(x[i], x[i], sq);
+          gx2 = f2_fma(f2_mul(z[i], wl[i]), x[i], gx2);
+        }
+        const float ss = head_sum<D / kE>(f2_sum(sq, 0)), gx = head_sum<D / kE>(f2_sum(gx2, 0));
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        const float m = -r * (r * r * (gx * (1.f / D)));
+        const uint64_t r2 = f2(r, r), m2 = f2(m, m);
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) {
+          acc[i] = f2_fma(f2_mul(z[i], x[i]), r2, acc[i]);
+          z[i] = f2_fma(x[i], m2, f2_mul(f2_mul(z[i], wl[i]), r2));
+        }
       }
-    }
-    if (h < n_heads) {
-      *reinterpret_cast<uint4*>(dx + (size_t)h * D + ln.off_a) = pack8(z);
-      *reinterpret_cast<uint4*>(dx + (size_t)h * D + ln.off_b) = pack8(z + 8);
+      if (h < n_heads) store_bf16(dx + (size_t)h * D, ln, z);
     }
   }
 }
@@ -290,49 +334,38 @@ __device__ __forceinline__ void sum_rows(const float* rows, int n, float* out_q,
 }
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRopeParams p) {
-  __shared__ float w[2][D];
-  // Each lane's sixteen sums for the key weights, then (after the last row)
-  // the warps' sums of both weights.
-  __shared__ float4 acc_k[kWarps][4][32];
+__global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rope_bwd_kernel(const NormRopeParams p) {
+  __shared__ __align__(16) float w[2][D];
+  __shared__ uint64_t turns[D / 2];
+  // The warps' sums of both weights' gradients, after the last row.
+  __shared__ float sums[kWarps][2][D];
   __shared__ int ticket;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) w[i / D][i % D] = load_w(i < D ? p.wq : p.wk, p.w_f32, i % D);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) acc_k[warp][e][lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (threadIdx.x < D / 2)
+    turns[threadIdx.x] = 2 * threadIdx.x < p.rot_dim ? turn_fraction(__ldg(p.inv_freq + threadIdx.x)) : 0;
   __syncthreads();
   const Lane ln = lane_of<D>(lane, p.rot_dim);
-  const int n_rot = p.rot_dim / 16, n_pairs = p.rot_dim / 2;
-  const uint64_t f0 = 2 * lane < n_pairs ? turn_fraction(__ldg(p.inv_freq + 2 * lane)) : 0;
-  const uint64_t f1 = 2 * lane < n_pairs ? turn_fraction(__ldg(p.inv_freq + 2 * lane + 1)) : 0;
-  float acc[16];
+  uint64_t aq[kE / 2], ak[kE / 2];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  for (int e = 0; e < kE / 2; ++e) aq[e] = ak[e] = 0;
+  const uint64_t f0 = 2 * lane < D / 2 ? turns[2 * lane] : 0, f1 = 2 * lane < D / 2 ? turns[2 * lane + 1] : 0;
   for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
     const Rows rows = unit_rows(p, u);
     for (int i = warp; i < rows.n; i += kWarps) {
       const size_t t = rows.first + i;
-      float c[8], s[8];
-      row_angles<INTER>(rows.pos + i, f0, f1, ln, n_rot, c, s);
+      float c[kE / 2], s[kE / 2];
+      row_angles<INTER>(rows.pos + i, f0, f1, ln, p.rot_dim, c, s);
       heads_backward<D, INTER>(p.dq + t * p.hq * D, p.q_in + t * p.q_in_stride, p.dq_in + t * p.dq_in_stride, p.hq, w[0],
-                               acc, ln, c, s, p);
-      float ak[16];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 v = acc_k[warp][e][lane];
-        ak[4 * e] = v.x, ak[4 * e + 1] = v.y, ak[4 * e + 2] = v.z, ak[4 * e + 3] = v.w;
-      }
+                               aq, ln, c, s, p);
       heads_backward<D, INTER>(p.dk + t * p.hkv * D, p.k_in + t * p.k_in_stride, p.dk_in + t * p.dk_in_stride, p.hkv,
                                w[1], ak, ln, c, s, p);
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        acc_k[warp][e][lane] = make_float4(ak[4 * e], ak[4 * e + 1], ak[4 * e + 2], ak[4 * e + 3]);
       if (p.dv) {
         const float4* src = reinterpret_cast<const float4*>(p.dv + t * p.hkv * D);
         uint4* dst = reinterpret_cast<uint4*>(p.dv_in + t * p.dv_in_stride);
         for (int e = lane; e < p.hkv * D / 8; e += 32) {
           const float4 a = src[2 * e], b = src[2 * e + 1];
-          dst[e] = make_uint4(pack2(a.x, a.y), pack2(a.z, a.w), pack2(b.x, b.y), pack2(b.z, b.w));
+          dst[e] = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
         }
       }
     }
@@ -342,27 +375,22 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRo
   // Weight gradients, in a fixed order (the result does not depend on which
   // CTA finishes when): lanes of a warp, warps of the CTA, CTAs of a group of
   // kNormRopeGroup by the last of them to finish, groups by the last group.
-  float ak[16];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float4 v = acc_k[warp][e][lane];
-    ak[4 * e] = v.x, ak[4 * e + 1] = v.y, ak[4 * e + 2] = v.z, ak[4 * e + 3] = v.w;
-  }
+  for (int e = 0; e < kE / 2; ++e) {
+    const int dim = 2 * e < kE / 2 ? ln.off_a + 2 * e : ln.off_b + 2 * e - kE / 2;
 #pragma unroll
-  for (int e = 0; e < 16; ++e)
+    for (int qk = 0; qk < 2; ++qk) {
+      float lo, hi;
+      f2_split(qk ? ak[e] : aq[e], lo, hi);
 #pragma unroll
-    for (int m = D / 16; m < 32; m <<= 1) {
-      acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], m);
-      ak[e] += __shfl_xor_sync(0xffffffffu, ak[e], m);
-    }
-  __syncthreads();
-  float* sums = reinterpret_cast<float*>(acc_k);  // [kWarps][2][D]
-  if (lane < D / 16) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const int dim = e < 8 ? ln.off_a + e : ln.off_b + e - 8;
-      sums[(warp * 2 + 0) * D + dim] = acc[e];
-      sums[(warp * 2 + 1) * D + dim] = ak[e];
+      for (int m = D / kE; m < 32; m <<= 1) {
+        lo += __shfl_xor_sync(0xffffffffu, lo, m);
+        hi += __shfl_xor_sync(0xffffffffu, hi, m);
+      }
+      if (lane < D / kE) {
+        sums[warp][qk][dim] = lo;
+        sums[warp][qk][dim + 1] = hi;
+      }
     }
   }
   __syncthreads();
@@ -370,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const NormRo
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) v += sums[k * 2 * D + i];
+    for (int k = 0; k < kWarps; ++k) v += sums[k][i / D][i % D];
     __stcg(part + i, v);
   }
   const int group = blockIdx.x / kNormRopeGroup, n_groups = ((int)gridDim.x + kNormRopeGroup - 1) / kNormRopeGroup;
@@ -417,7 +445,7 @@ int launch_norm_rope(const NormRopeLaunch& a, cudaStream_t st) {
   const int64_t units = (int64_t)a.n_tiles * p.chunks;
   if (units > INT32_MAX) return FCP_ERR_UNSUPPORTED;
   p.n_units = (int)units;
-  const int most = a.num_sms * (a.backward ? 2 : 4);
+  const int most = a.num_sms * (a.backward ? kBwdCtas : kFwdCtas);
   int64_t grid = units < most ? units : most;
   if (a.backward && grid > kNormRopeMaxCtas) grid = kNormRopeMaxCtas;
   auto go = [&](auto kernel) {
