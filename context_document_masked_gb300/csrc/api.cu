@@ -272,13 +272,14 @@ int fcp_plan_upload(const fcp_plan_t* plan, void* dev_buf, int64_t bytes, void* 
 // (fp32 [Hq][T]); fp16 copies of Q and dO ([T][Hq][d] each, backward); fp16
 // copies of V ([T][Hkv][d]) and of the received V rows ([R][Hkv][d], R = all
 // shards' remote rows of the plan), the forward's P*V operands; e4m3 copies
-// of Q, K and the received K rows; the tickets (zero between calls) and
-// partial sums of the norm weights' gradients; the biased backward's sums of dS
-// by distance (zero between calls).
+// of Q, K and the received K rows; partial sums of the norm weights' gradients;
+// the biased backward's sums of dS by distance. Only the header holds what a
+// call leaves for the next one (the zeros of its counters): the rest moves with
+// the sizes, and one workspace may serve several.
 constexpr int64_t kWorkCounterOff = 64;
 
 struct WsLayout {
-  int64_t delta, q16, do16, v16, vb16, q8, k8, kb8, tickets, partial, by_distance, total;
+  int64_t delta, q16, do16, v16, vb16, q8, k8, kb8, partial, by_distance, total;
 };
 
 // Header words of the e4m3 Q K^T forward: amax bits of Q and K, then their
@@ -288,6 +289,9 @@ constexpr int64_t kQkScaleOff = 136;
 // Diagnostic counter of the forward: online-softmax rescales of O after a
 // query tile's first key tile (one count per warp and event).
 constexpr int64_t kRescaleCountOff = 192;
+// Tickets of the norm weights' gradients (zero between calls).
+constexpr int64_t kTicketsOff = 68;
+static_assert(kTicketsOff + (1 + fcp::kNormRopeGroups) * 4 <= kQkAmaxOff, "tickets inside the header");
 
 static int64_t ws_align(int64_t x) { return (x + 255) / 256 * 256; }
 
@@ -304,10 +308,8 @@ static WsLayout ws_layout(const fcp_dims& d, int64_t remote_rows) {
   w.q8 = w.vb16 + ws_align(R * hkv * dd * 2);
   w.k8 = w.q8 + ws_align(T * hq * dd);
   w.kb8 = w.k8 + ws_align(T * hkv * dd);
-  w.tickets = w.kb8 + ws_align(R * hkv * dd);
-  constexpr int64_t groups = (fcp::kNormRopeMaxCtas + fcp::kNormRopeGroup - 1) / fcp::kNormRopeGroup;
-  w.partial = w.tickets + ws_align((1 + groups) * 4);
-  w.by_distance = w.partial + ws_align((fcp::kNormRopeMaxCtas + groups) * 2 * dd * 4);
+  w.partial = w.kb8 + ws_align(R * hkv * dd);
+  w.by_distance = w.partial + ws_align((fcp::kNormRopeMaxCtas + fcp::kNormRopeGroups) * 2 * dd * 4);
   w.total = w.by_distance + ws_align(hq * fcp::kTableDistances * 4);
   return w;
 }
@@ -354,6 +356,8 @@ static void set_bias(fcp::BiasParams* p, const fcp_rel_bias* b, float* dbias, fl
   p->bias = b->bias;
   p->dbias = dbias;
   p->by_distance = by_distance;
+  // Tiles of several buckets reach 254 distances past the last one's first.
+  p->n_distances = std::min(std::min(b->starts[b->n_buckets - 1], fcp::kTableDistances) + 256, fcp::kTableDistances);
   p->n = b->n_buckets;
   std::copy(b->starts, b->starts + b->n_buckets, p->starts);
 }
@@ -827,7 +831,7 @@ int fcp_qk_norm_rope_bwd(const float* dq, const float* dk, const float* dv, cons
   a.p.dwk = dwk;
   char* wsb = static_cast<char*>(ws);
   a.p.partial = reinterpret_cast<float*>(wsb + wl.partial);
-  a.p.tickets = reinterpret_cast<int*>(wsb + wl.tickets);
+  a.p.tickets = reinterpret_cast<int*>(wsb + kTicketsOff);
   a.p.err = static_cast<int*>(ws);
   return fcp::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
 }

@@ -224,8 +224,8 @@ static __device__ __noinline__ void add_block(uint32_t block, int h, const Bucke
 #pragma unroll 1
   for (int w = 0; w < 3; ++w, base += 32) {
     const int dist = base + lane;
-    if (base + 31 < kTableDistances) {
-      if (dist >= 0) red_add(bp.by_distance + (size_t)h * kTableDistances + dist, d[0]);
+    if (base + 31 < bp.n_distances) {
+      if (dist >= 0) red_add(bp.by_distance + (size_t)h * bp.n_distances + dist, d[0]);
     } else {
       add_by_bucket(bp.dbias + (size_t)h * bp.n, bk.of(bp.n, dist), d[0], lane);
     }
@@ -897,24 +897,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-// dbias += the table's sums by distance, which are set back to zero: one block
-// a head, a warp a bucket. Blocks of dS reach 255 distances past the last
-// bucket's first.
+// dbias += the table's sums by distance: one block a head, a warp a bucket.
 constexpr int kTableThreads = 512;
 static __global__ void __launch_bounds__(kTableThreads) table_sums_kernel(const __grid_constant__ BiasParams bp) {
-  __shared__ float by[kTableDistances];
-  const int used = min(min(bp.starts[bp.n - 1], kTableDistances) + 256, kTableDistances);
-  float* table = bp.by_distance + (size_t)blockIdx.x * kTableDistances;
-  for (int x = threadIdx.x; x < used; x += kTableThreads) {
-    by[x] = table[x];
-    table[x] = 0.f;
-  }
-  __syncthreads();
+  const float* table = bp.by_distance + (size_t)blockIdx.x * bp.n_distances;
   const int lane = threadIdx.x & 31;
   for (int b = threadIdx.x >> 5; b < bp.n; b += kTableThreads / 32) {
-    const int end = b + 1 < bp.n ? min(bp.starts[b + 1], used) : used;
+    const int end = b + 1 < bp.n ? min(bp.starts[b + 1], bp.n_distances) : bp.n_distances;
     float v = 0.f;
-    for (int x = bp.starts[b] + lane; x < end; x += 32) v += by[x];
+#pragma unroll 4
+    for (int x = bp.starts[b] + lane; x < end; x += 32) v += __ldcg(table + x);
     v = warp_sum(v);
     if (lane == 0) bp.dbias[(size_t)blockIdx.x * bp.n + b] += v;
   }
@@ -939,6 +931,10 @@ static int launch_bwd_impl(const BwdLaunch& a, const Bias& bias, cudaStream_t st
   // together stream the same query rows (Q, dO, dQ) of that head group.
   BwdParams p = a.p;
   p.order_block = grid;
+  if constexpr (std::is_same_v<Bias, BiasParams>) {
+    if (cudaMemsetAsync(bias.by_distance, 0, sizeof(float) * p.hq * bias.n_distances, st) != cudaSuccess)
+      return FCP_ERR_CUDA;
+  }
   attn_bwd_kernel<D, Bias><<<grid, kThreads, C::kSmem, st>>>(a.tm_q, a.tm_do, a.tm_k, a.tm_v, a.tm_kb,
                                                       a.tm_vb, a.tm_dq, a.tm_dk, a.tm_dv, p, bias);
   if constexpr (std::is_same_v<Bias, BiasParams>) table_sums_kernel<<<p.hq, kTableThreads, 0, st>>>(bias);

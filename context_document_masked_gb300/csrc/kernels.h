@@ -52,11 +52,12 @@ struct FwdParams {
 // holds the distances from starts[u] to starts[u + 1] - 1 (the last one all
 // from starts[u] on).
 constexpr int kMaxBuckets = 128;
-constexpr int kTableDistances = 8192;
+constexpr int kTableDistances = 8192;  // at most
 struct BiasParams {
   const float* bias;       // [hq][n]
   float* dbias;            // backward: [hq][n], accumulated
-  float* by_distance;      // backward: [hq][kTableDistances] sums of dS, zero at launch and after it
+  float* by_distance;      // backward: [hq][n_distances] sums of dS (set to zero by the launch)
+  int32_t n_distances;
   int32_t n;
   int32_t starts[kMaxBuckets];
 };
@@ -153,9 +154,11 @@ int launch_merge(const float* o_parts, const float* lse_parts, int32_t B, int64_
 
 // Head norm and rotation, and their gradient (norm_rope.cu). At most
 // kNormRopeMaxCtas CTAs write partial sums of the weight gradients, summed in
-// groups of kNormRopeGroup.
-constexpr int kNormRopeMaxCtas = 512;
-constexpr int kNormRopeGroup = 16;
+// groups of kNormRopeGroup (the tickets of 14 groups and one for the groups
+// fit the workspace header).
+constexpr int kNormRopeGroup = 32;
+constexpr int kNormRopeGroups = 14;
+constexpr int kNormRopeMaxCtas = kNormRopeGroup * kNormRopeGroups;
 
 struct NormRopeParams {
   const int32_t* pieces;   // plan piece table
@@ -187,7 +190,7 @@ struct NormRopeParams {
   float* dwq;              // [d], accumulated, or null
   float* dwk;
   float* partial;          // [kNormRopeMaxCtas + their groups][2][d]
-  int* tickets;            // 1 + number of groups, zero at launch and at its end
+  int* tickets;            // 1 + kNormRopeGroups, zero at launch and at its end
   int* err;                // error word (checked build) or null
 };
 

@@ -427,8 +427,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rope_bwd_kernel(const
   __threadfence();
   if (threadIdx.x == 0) p.tickets[0] = 0;
   float* all = p.partial + (size_t)kNormRopeMaxCtas * 2 * D;
-  for (int g = 0; g < n_groups; g += kNormRopeGroup)
-    sum_rows<D>(all + (size_t)g * 2 * D, min(kNormRopeGroup, n_groups - g), p.dwq, p.dwk, true);
+  sum_rows<D>(all, n_groups, p.dwq, p.dwk, true);
 }
 
 }  // namespace

@@ -249,12 +249,15 @@ def test_captured_with_new_biases_and_on_another_stream(cuda):
     assert s.device_status() == 0
 
 
-def test_one_long_document(cuda):
-    """16,385 tokens on four shards against a plain form in 64 bits on the GPU."""
+@pytest.mark.parametrize("which", ["usual", "narrow far off"])
+def test_one_long_document(cuda, which):
+    """16,385 tokens on four shards against a plain form in 64 bits on the GPU;
+    buckets by logarithms up to 8192, and narrow ones past that."""
     from context_document_masked_gb300 import fcp
     T, hq, hkv, d = 16385, 2, 1, 64
-    starts = fcp.rel_buckets(64, 8192)
-    x = make([T], hq, hkv, d, 64, seed=7)
+    far = [0, 1, 100, 5000, 8180, 8200, 9000, 9003, 9004, 9040, 9041, 12000, 16300]
+    starts = fcp.rel_buckets(64, 8192) if which == "usual" else np.array(far)
+    x = make([T], hq, hkv, d, len(starts), seed=7)
     s = session([T], 4, hq, hkv, d)
     xc = [t.cuda() for t in x]
     got = step(s, xc, starts)
@@ -281,11 +284,45 @@ def test_one_long_document(cuda):
         edv = edv + (H + 2 * es + T * 2 * U) * (p.T @ do[:, h].abs()) + T * 2.0 ** -24 * do.abs().max()
         dk[:, 0] += ds.T @ q[:, h] / 8
         dv[:, 0] += p.T @ do[:, h]
-        by = torch.zeros(64, dtype=torch.float64, device="cuda").index_add_(0, bucket.flatten(), ds.flatten())
+        by = torch.zeros(len(starts), dtype=torch.float64, device="cuda").index_add_(0, bucket.flatten(), ds.flatten())
         lim = torch.zeros_like(by).index_add_(0, bucket.flatten(), eds.flatten())
         assert ((got[5][h] - by).abs() <= lim).all()
         del p, x_, ds, eds, ex
     assert ((got[3][:, 0] - dk[:, 0]).abs() <= edk).all() and ((got[4][:, 0] - dv[:, 0]).abs() <= edv).all()
+
+
+def test_one_workspace_for_other_plans_and_sizes(cuda):
+    """A session re-planned (its workspace's regions move) and one workspace used
+    for two shapes in turn: nothing that one call leaves reaches the next."""
+    from context_document_masked_gb300 import fcp
+    hq, hkv, d, starts = 4, 2, 64, [0, 1, 3, 50]
+    s = session([500, 12], 2, hq, hkv, d, "hybrid")
+    for seed, docs in ((1, [500, 12]), (2, [1] * 100 + [412]), (3, [256, 256]), (4, [512])):
+        if seed > 1:
+            s.set_plan(docs)
+        x = make(docs, hq, hkv, d, 4, seed=seed)
+        want = reference(*x, starts, docs)
+        for name, t in zip(("out", "lse", "dq", "dk", "dv", "dbias"), step(s, [t.cuda() for t in x], starts)):
+            within(t, want, name)
+    small, big = ([300, 84], 2, 1, 64), ([700, 68], 6, 3, 128)
+    ss = [session(docs, 1, *shape) for docs, *shape in (small, big)]
+    ss[0].ws = ss[1].ws
+    rows = []
+    for k in range(4):
+        (docs, *shape), s = (small, big)[k % 2], ss[k % 2]
+        x = make(docs, *shape, 4, seed=10 + k)
+        want = reference(*x, starts, docs)
+        xc = [t.cuda() for t in x]
+        for name, t in zip(("out", "lse", "dq", "dk", "dv", "dbias"), step(s, xc, starts)):
+            within(t, want, name)
+        w = torch.ones(shape[2], device="cuda")
+        g = torch.Generator("cuda").manual_seed(5 + k % 2)
+        grads = [torch.randn(sum(docs), h, shape[2], device="cuda", generator=g) for h in (shape[0], shape[1])]
+        qk = [torch.randn(sum(docs), h, shape[2], device="cuda", generator=g).to(torch.bfloat16) for h in (shape[0], shape[1])]
+        rows.append(s.qk_norm_rope_backward(*grads, None, *qk, wq=w, wk=w))
+    for a, b in ((0, 2), (1, 3)):
+        for m, n in zip(rows[a], rows[b]):
+            assert m is None and n is None or torch.equal(m, n)
 
 
 def test_norm_rope_then_biased_attention(cuda):
