@@ -689,7 +689,7 @@ static bool spans_meet(const RowSpan& a, const RowSpan& b, int64_t rows) {
 static int check_norm_rope(const fcp_norm_rope* nr, const void* wq, const void* wk, const float* inv_freq,
                            const fcp_dims& dims) {
   if (!nr || (nr->norm != 0 && nr->norm != 1) || (nr->interleaved != 0 && nr->interleaved != 1) ||
-      (nr->w_dtype != FCP_OUT_BF16 && nr->w_dtype != FCP_OUT_F32))
+      (nr->w_dtype != FCP_OUT_BF16 && nr->w_dtype != FCP_OUT_F32) || (nr->add_dw != 0 && nr->add_dw != 1))
     return FCP_ERR_INVALID_ARG;
   if (nr->norm && !(nr->eps >= 0.f && nr->eps <= 3.4e38f)) return FCP_ERR_INVALID_ARG;
   if (!nr->norm && (wq || wk)) return FCP_ERR_INVALID_ARG;
@@ -730,6 +730,7 @@ static fcp::NormRopeLaunch norm_rope_launch(const fcp_norm_rope* nr, const void*
   a.p.eps = nr->eps;
   a.p.rot_dim = nr->rot_dim;
   a.p.w_f32 = nr->w_dtype == FCP_OUT_F32;
+  a.p.add_dw = nr->add_dw;
   a.p.inv_freq = inv_freq;
   a.p.wq = wq;
   a.p.wk = wk;

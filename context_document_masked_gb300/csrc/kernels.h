@@ -187,7 +187,8 @@ struct NormRopeParams {
   __nv_bfloat16* dk_in;
   __nv_bfloat16* dv_in;
   int64_t dq_in_stride, dk_in_stride, dv_in_stride;
-  float* dwq;              // [d], accumulated, or null
+  int32_t add_dw;          // 1: dwq and dwk are added to
+  float* dwq;              // [d] or null
   float* dwk;
   float* partial;          // [kNormRopeMaxCtas + their groups][2][d]
   int* tickets;            // 1 + kNormRopeGroups, zero at launch and at its end

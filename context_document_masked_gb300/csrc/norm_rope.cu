@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rope_bwd_kernel(const
   if (threadIdx.x == 0) p.tickets[1 + group] = 0;
   const float* rows = p.partial + (size_t)group * kNormRopeGroup * 2 * D;
   if (n_groups == 1) {
-    sum_rows<D>(rows, in_group, p.dwq, p.dwk, true);
+    sum_rows<D>(rows, in_group, p.dwq, p.dwk, p.add_dw != 0);
     return;
   }
   float* gpart = p.partial + (size_t)(kNormRopeMaxCtas + group) * 2 * D;
@@ -427,14 +427,19 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rope_bwd_kernel(const
   __threadfence();
   if (threadIdx.x == 0) p.tickets[0] = 0;
   float* all = p.partial + (size_t)kNormRopeMaxCtas * 2 * D;
-  sum_rows<D>(all, n_groups, p.dwq, p.dwk, true);
+  sum_rows<D>(all, n_groups, p.dwq, p.dwk, p.add_dw != 0);
 }
 
 }  // namespace
 
 int launch_norm_rope(const NormRopeLaunch& a, cudaStream_t st) {
   NormRopeParams p = a.p;
-  if (a.n_tiles == 0) return FCP_OK;
+  if (a.n_tiles == 0) {  // a shard without tokens
+    for (float* dw : {p.dwq, p.dwk})
+      if (a.backward && !p.add_dw && dw && cudaMemsetAsync(dw, 0, sizeof(float) * a.d, st) != cudaSuccess)
+        return FCP_ERR_CUDA;
+    return FCP_OK;
+  }
   // Rows a CTA takes at a time: 8, one a warp, as a small sequence has to
   // spread over all SMs; whole tiles where tiles are short (documents of a
   // few tokens), whose units would otherwise mostly be empty.

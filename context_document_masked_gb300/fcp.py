@@ -10,6 +10,7 @@ import ctypes as C
 import os
 
 import numpy as np
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # FCP_DEVICE_CHECKS=1 selects the checked build (device-side bounds checks on
@@ -32,6 +33,9 @@ EXPORTED = (
     "fcp_qk_norm_rope_bwd", "fcp_rel_buckets", "fcp_attn_fwd_bias", "fcp_attn_bwd_bias",
 )
 MAX_BUCKETS = 128
+
+
+_BF16, _F32, _BF16_F32 = (torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32)
 
 
 class FcpError(RuntimeError):
@@ -79,7 +83,7 @@ class Dims(C.Structure):
 
 class NormRope(C.Structure):
     _fields_ = [("norm", C.c_int32), ("eps", C.c_float), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
-                ("w_dtype", C.c_int32)]
+                ("w_dtype", C.c_int32), ("add_dw", C.c_int32)]
 
 
 class RelBias(C.Structure):
@@ -233,7 +237,6 @@ class Plan:
         """Copy the work tables into `buf` (an int32 device tensor of >= device_bytes()
         bytes) on `stream`, staged through pinned host memory so that the host does
         not wait for the stream's earlier work."""
-        import torch
         n = self.device_bytes() // 4
         dp = self.bind(buf)
         host = torch.empty(n, dtype=torch.int32, pin_memory=True)
@@ -273,7 +276,6 @@ def _stream(stream):
     if stream is None:
         # torch.cuda.current_stream().cuda_stream, without making a Stream object
         # (8 us of a call's 45 on this host).
-        import torch
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
@@ -286,7 +288,6 @@ def _t(t, name, dtypes=None, shape=None):
     """Checks a tensor before its raw pointer goes to the library, which cannot
     see dtypes, strides or devices: a contiguous CUDA tensor of one of
     `dtypes`, of `shape` (None entries free). Raises ValueError."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if not t.is_cuda:
@@ -308,11 +309,10 @@ def _t(t, name, dtypes=None, shape=None):
 
 def _qkv(q, k, v):
     """Q [T][hq][d] and K, V [T][hkv][d], bf16; returns (T, hq, hkv, d)."""
-    import torch
-    _t(q, "q", (torch.bfloat16,), (None, None, None))
+    _t(q, "q", _BF16, (None, None, None))
     T, hq, d = q.shape
-    _t(k, "k", (torch.bfloat16,), (T, None, d))
-    _t(v, "v", (torch.bfloat16,), tuple(k.shape))
+    _t(k, "k", _BF16, (T, None, d))
+    _t(v, "v", _BF16, tuple(k.shape))
     return T, hq, k.shape[1], d
 
 
@@ -320,18 +320,16 @@ def _kbuf(kbuf, vbuf, dplan, shard, hkv, d):
     """The received-key buffers hold at least the rows the plan sends to
     `shard` (all shards' for -1): the library writes and reads them by the
     plan, not by their size."""
-    import torch
     rows = max(1, dplan.remote_rows(shard))
     for t, n in ((kbuf, "kbuf"), (vbuf, "vbuf")):
-        _t(t, n, (torch.bfloat16,), (None, hkv, d))
+        _t(t, n, _BF16, (None, hkv, d))
         if t.shape[0] < rows:
             raise ValueError(f"{n}: {t.shape[0]} rows, the plan receives {rows}")
 
 
 def _out_lse(out, lse, T, hq, d):
-    import torch
-    _t(out, "out", (torch.bfloat16, torch.float32), (T, hq, d))
-    _t(lse, "lse", (torch.float32,), (hq, T))
+    _t(out, "out", _BF16_F32, (T, hq, d))
+    _t(lse, "lse", _F32, (hq, T))
 
 
 def dims(T: int, hq: int, hkv: int, d: int, scale: float = 0.0) -> Dims:
@@ -343,9 +341,8 @@ def workspace_bytes(dm: Dims, plan: "Plan | None" = None) -> int:
 
 
 def gather_kv(k, v, dplan: DevicePlan, shard: int, kbuf, vbuf, stream=None):
-    import torch
-    _t(k, "k", (torch.bfloat16,), (None, None, None))
-    _t(v, "v", (torch.bfloat16,), tuple(k.shape))
+    _t(k, "k", _BF16, (None, None, None))
+    _t(v, "v", _BF16, tuple(k.shape))
     _kbuf(kbuf, vbuf, dplan, shard, k.shape[1], k.shape[2])
     _check(_lib.fcp_gather_kv(_ptr(k), _ptr(v), C.byref(dplan.c), shard, k.shape[1], k.shape[2],
                               _ptr(kbuf), _ptr(vbuf), _stream(stream)), "fcp_gather_kv")
@@ -353,7 +350,6 @@ def gather_kv(k, v, dplan: DevicePlan, shard: int, kbuf, vbuf, stream=None):
 
 def attn_fwd(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, lse, ws, kv_lo: int = 0,
              kv_hi: int | None = None, scale: float = 0.0, stream=None):
-    import torch
     T, hq, hkv, d = _qkv(q, k, v)
     _kbuf(kbuf, vbuf, dplan, shard, hkv, d)
     _out_lse(out, lse, T, hq, d)
@@ -369,7 +365,6 @@ def attn_fwd(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, lse, ws, k
 def attn_fwd_qk8(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, lse, ws, kv_lo: int = 0,
                  kv_hi: int | None = None, scale: float = 0.0, stream=None):
     """fcp_attn_fwd_qk8: the forward with Q K^T on e4m3 copies of Q and K."""
-    import torch
     T, hq, hkv, d = _qkv(q, k, v)
     _kbuf(kbuf, vbuf, dplan, shard, hkv, d)
     _out_lse(out, lse, T, hq, d)
@@ -384,10 +379,9 @@ def attn_fwd_qk8(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, lse, w
 
 def quant_e4m3(x, out, scale_out, scratch, stream=None):
     """fcp_quant_e4m3: out (uint8, x.numel() bytes) = e4m3(x * 2^k); scale_out[0] = 2^k."""
-    import torch
-    _t(x, "x", (torch.bfloat16,))
+    _t(x, "x", _BF16)
     _t(out, "out", (torch.uint8,))
-    _t(scale_out, "scale_out", (torch.float32,))
+    _t(scale_out, "scale_out", _F32)
     _t(scratch, "scratch", (torch.int32,))
     if out.numel() < x.numel() or scale_out.numel() < 1 or scratch.numel() < 1:
         raise ValueError("quant_e4m3: out holds x.numel() bytes, scale_out and scratch one element each")
@@ -400,7 +394,6 @@ def attn_fwd_ring(q, k, v, dplan: DevicePlan, shard: int, ring_step: int, out, l
     """fcp_attn_fwd_ring: every needed key read from its owner's rows of K/V,
     owners in ring order; ring_step -1 = all owners in one pass, s >= 0 = the
     partial result of ring step s."""
-    import torch
     T, hq, hkv, d = _qkv(q, k, v)
     _out_lse(out, lse, T, hq, d)
     _t(ws, "ws")
@@ -416,7 +409,6 @@ def attn_fwd_noalloc(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, ls
                      kv_hi: int | None = None, scale: float = 0.0, stream=None):
     """fcp_attn_fwd_noalloc: the forward with the library's static scratch
     instead of a caller workspace (for callers that cannot allocate)."""
-    import torch
     T, hq, hkv, d = _qkv(q, k, v)
     _kbuf(kbuf, vbuf, dplan, shard, hkv, d)
     _out_lse(out, lse, T, hq, d)
@@ -430,21 +422,19 @@ def attn_fwd_noalloc(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, ls
 
 def round_bf16(x, out, stream=None):
     """fcp_round_bf16: out (bf16, same element count) = x (fp32) rounded to nearest even."""
-    import torch
-    _t(x, "x", (torch.float32,))
-    _t(out, "out", (torch.bfloat16,))
+    _t(x, "x", _F32)
+    _t(out, "out", _BF16)
     if x.numel() != out.numel():
         raise ValueError("round_bf16: x and out differ in element count")
     _check(_lib.fcp_round_bf16(_ptr(x), x.numel(), _ptr(out), _stream(stream)), "fcp_round_bf16")
 
 
 def _merge_args(o_parts, lse_parts, out, lse_out):
-    import torch
-    _t(o_parts, "o_parts", (torch.float32,), (None, None, None, None))
+    _t(o_parts, "o_parts", _F32, (None, None, None, None))
     B, rows, hq, d = o_parts.shape
-    _t(lse_parts, "lse_parts", (torch.float32,), (B, hq, rows))
-    _t(out, "out", (torch.bfloat16,), (rows, hq, d))
-    _t(lse_out, "lse_out", (torch.float32,), (hq, rows))
+    _t(lse_parts, "lse_parts", _F32, (B, hq, rows))
+    _t(out, "out", _BF16, (rows, hq, d))
+    _t(lse_out, "lse_out", _F32, (hq, rows))
     return B, rows, hq, d
 
 
@@ -470,14 +460,13 @@ def merge_ring(dplan: DevicePlan, o_parts, lse_parts, part_step, out, lse_out, s
 
 def attn_bwd(q, k, v, kbuf, vbuf, out, lse, dout, dplan: DevicePlan, shard: int, dq, dk, dv, ws,
              scale: float = 0.0, stream=None):
-    import torch
     T, hq, hkv, d = _qkv(q, k, v)
     _kbuf(kbuf, vbuf, dplan, shard, hkv, d)
     _out_lse(out, lse, T, hq, d)
-    _t(dout, "dout", (torch.bfloat16,), (T, hq, d))
-    _t(dq, "dq", (torch.float32,), (T, hq, d))
-    _t(dk, "dk", (torch.float32,), (T, hkv, d))
-    _t(dv, "dv", (torch.float32,), (T, hkv, d))
+    _t(dout, "dout", _BF16, (T, hq, d))
+    _t(dq, "dq", _F32, (T, hq, d))
+    _t(dk, "dk", _F32, (T, hkv, d))
+    _t(dv, "dv", _F32, (T, hkv, d))
     _t(ws, "ws")
     dm = Dims(T, hq, hkv, d, scale)
     out_dtype = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
@@ -500,7 +489,6 @@ def rel_buckets(n_buckets: int, max_distance: int) -> np.ndarray:
 
 def _rel_bias(bias, starts, hq):
     """The C struct, and the host array it points to (kept for the call)."""
-    import torch
     s = starts.tolist() if hasattr(starts, "tolist") else list(starts)
     try:
         a = (C.c_int32 * len(s))(*s)
@@ -508,7 +496,7 @@ def _rel_bias(bias, starts, hq):
         raise ValueError("starts: one whole number a bucket") from None
     if not s or min(s) < 0 or max(s) >= 1 << 31:
         raise ValueError("starts: distances of 0 to 2^31 - 1, one a bucket")
-    _t(bias, "bias", (torch.float32,), (hq, len(s)))
+    _t(bias, "bias", _F32, (hq, len(s)))
     return RelBias(_ptr(bias), a, len(s)), a
 
 
@@ -517,14 +505,13 @@ def attn_fwd_bias(q, k, v, kbuf, vbuf, bias, starts, dplan: DevicePlan, shard: i
     """fcp_attn_fwd_bias: attn_fwd with bias[h, bucket(i - j)] (fp32 [hq][n])
     added to the scores; starts (host, n whole numbers) are the buckets' first
     distances."""
-    import torch
     T, hq, hkv, d = _qkv(q, k, v)
     _kbuf(kbuf, vbuf, dplan, shard, hkv, d)
     _out_lse(out, lse, T, hq, d)
     _t(ws, "ws")
     rb, keep = _rel_bias(bias, starts, hq)
     out_dtype = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
-    with _on(q, k, v, kbuf, vbuf, bias, out, lse, ws):
+    with _on(q, k, v, kbuf, vbuf, bias, out, lse, ws, dplan.buf):
         _check(_lib.fcp_attn_fwd_bias(_ptr(q), _ptr(k), _ptr(v), _ptr(kbuf), _ptr(vbuf), C.byref(rb), C.byref(dplan.c),
                                       shard, kv_lo, T if kv_hi is None else kv_hi, Dims(T, hq, hkv, d, scale), out_dtype,
                                       _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
@@ -535,19 +522,18 @@ def attn_bwd_bias(q, k, v, kbuf, vbuf, bias, starts, out, lse, dout, dplan: Devi
                   scale: float = 0.0, stream=None):
     """fcp_attn_bwd_bias: attn_bwd of attn_fwd_bias; dbias (fp32 [hq][n]) is
     accumulated like dk and dv."""
-    import torch
     T, hq, hkv, d = _qkv(q, k, v)
     _kbuf(kbuf, vbuf, dplan, shard, hkv, d)
     _out_lse(out, lse, T, hq, d)
-    _t(dout, "dout", (torch.bfloat16,), (T, hq, d))
-    _t(dq, "dq", (torch.float32,), (T, hq, d))
-    _t(dk, "dk", (torch.float32,), (T, hkv, d))
-    _t(dv, "dv", (torch.float32,), (T, hkv, d))
+    _t(dout, "dout", _BF16, (T, hq, d))
+    _t(dq, "dq", _F32, (T, hq, d))
+    _t(dk, "dk", _F32, (T, hkv, d))
+    _t(dv, "dv", _F32, (T, hkv, d))
     _t(ws, "ws")
     rb, keep = _rel_bias(bias, starts, hq)
-    _t(dbias, "dbias", (torch.float32,), tuple(bias.shape))
+    _t(dbias, "dbias", _F32, tuple(bias.shape))
     out_dtype = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
-    with _on(q, k, v, kbuf, vbuf, bias, out, lse, dout, dq, dk, dv, dbias, ws):
+    with _on(q, k, v, kbuf, vbuf, bias, out, lse, dout, dq, dk, dv, dbias, ws, dplan.buf):
         _check(_lib.fcp_attn_bwd_bias(_ptr(q), _ptr(k), _ptr(v), _ptr(kbuf), _ptr(vbuf), C.byref(rb), _ptr(out),
                                       out_dtype, _ptr(lse), _ptr(dout), C.byref(dplan.c), shard,
                                       Dims(T, hq, hkv, d, scale), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dbias), _ptr(ws),
@@ -573,7 +559,6 @@ _HERE_CTX = _Here()
 def _on(first, *tensors):
     """Makes the tensors' device the current one for a call (the library
     launches on the current device); all tensors on that device."""
-    import torch
     i = first.get_device()
     for t in tensors:
         if t is not None and t.get_device() != i:
@@ -584,7 +569,6 @@ def _on(first, *tensors):
 def _rows(t, name, T, heads, d):
     """A bf16 [T][heads][d] tensor whose rows of heads * d values are contiguous
     and `stride` elements apart (a slice of a fused projection): the stride."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if not t.is_cuda:
@@ -604,19 +588,19 @@ def _rows(t, name, T, heads, d):
     return stride
 
 
-def _norm_rope_opts(wq, wk, inv_freq, d, norm, eps, interleaved):
-    import torch
+def _norm_rope_opts(wq, wk, inv_freq, d, norm, eps, interleaved, add_dw=0):
     for t, n in ((wq, "wq"), (wk, "wk")):
         if t is not None:
-            _t(t, n, (torch.bfloat16, torch.float32), (d,))
+            _t(t, n, _BF16_F32, (d,))
     if wq is not None and wk is not None and wq.dtype != wk.dtype:
         raise ValueError(f"wq and wk: dtypes {wq.dtype} and {wk.dtype}, expected one for both")
     w = wq if wq is not None else wk
     rot = 0
     if inv_freq is not None:
-        _t(inv_freq, "inv_freq", (torch.float32,), (None,))
+        _t(inv_freq, "inv_freq", _F32, (None,))
         rot = 2 * inv_freq.numel()
-    return NormRope(int(norm), eps, rot, int(interleaved), OUT_BF16 if w is not None and w.dtype == torch.bfloat16 else OUT_F32)
+    w_dtype = OUT_BF16 if w is not None and w.dtype == torch.bfloat16 else OUT_F32
+    return NormRope(int(norm), eps, rot, int(interleaved), w_dtype, int(add_dw))
 
 
 def qk_norm_rope(q_in, k_in, v_in, dplan: DevicePlan, shard: int, q, k, v, wq=None, wk=None, inv_freq=None,
@@ -625,34 +609,34 @@ def qk_norm_rope(q_in, k_in, v_in, dplan: DevicePlan, shard: int, q, k, v, wq=No
     normed and turned by their document positions, and v_in's rows; the inputs
     may be slices of a fused projection. inv_freq (fp32, rot_dim / 2 values)
     None: no rotation. v_in and v may be None."""
-    import torch
-    _t(q, "q", (torch.bfloat16,), (None, None, None))
+    _t(q, "q", _BF16, (None, None, None))
     T, hq, d = q.shape
-    _t(k, "k", (torch.bfloat16,), (T, None, d))
+    _t(k, "k", _BF16, (T, None, d))
     hkv = k.shape[1]
     sq, sk = _rows(q_in, "q_in", T, hq, d), _rows(k_in, "k_in", T, hkv, d)
     if (v_in is None) != (v is None):
         raise ValueError("v_in and v: both or neither")
     sv = 0
     if v is not None:
-        _t(v, "v", (torch.bfloat16,), (T, hkv, d))
+        _t(v, "v", _BF16, (T, hkv, d))
         sv = _rows(v_in, "v_in", T, hkv, d)
     nr = _norm_rope_opts(wq, wk, inv_freq, d, norm, eps, interleaved)
-    with _on(q, k, v, q_in, k_in, v_in, wq, wk, inv_freq):
+    with _on(q, k, v, q_in, k_in, v_in, wq, wk, inv_freq, dplan.buf):
         _check(_lib.fcp_qk_norm_rope(_ptr(q_in), sq, _ptr(k_in), sk, _ptr(v_in), sv, _ptr(wq), _ptr(wk), _ptr(inv_freq),
                                      C.byref(nr), C.byref(dplan.c), shard, Dims(T, hq, hkv, d, 0.0), _ptr(q), _ptr(k),
                                      _ptr(v), _stream(stream)), "fcp_qk_norm_rope")
 
 
 def qk_norm_rope_bwd(dq, dk, dv, q_in, k_in, dplan: DevicePlan, shard: int, dq_in, dk_in, dv_in, dwq, dwk, ws, wq=None,
-                     wk=None, inv_freq=None, norm: bool = True, eps: float = 1e-6, interleaved: bool = False, stream=None):
+                     wk=None, inv_freq=None, norm: bool = True, eps: float = 1e-6, interleaved: bool = False,
+                     add_dw: bool = False, stream=None):
     """fcp_qk_norm_rope_bwd: from the attention's fp32 dq, dk, dv the bf16
     gradients of qk_norm_rope's inputs (dq_in, dk_in, dv_in may be slices of one
-    fused gradient); dwq and dwk (fp32 [d]) are accumulated."""
-    import torch
-    _t(dq, "dq", (torch.float32,), (None, None, None))
+    fused gradient); dwq and dwk (fp32 [d]) are written, or with add_dw added
+    to."""
+    _t(dq, "dq", _F32, (None, None, None))
     T, hq, d = dq.shape
-    _t(dk, "dk", (torch.float32,), (T, None, d))
+    _t(dk, "dk", _F32, (T, None, d))
     hkv = dk.shape[1]
     sq = sk = sdv = 0
     if norm:
@@ -663,14 +647,14 @@ def qk_norm_rope_bwd(dq, dk, dv, q_in, k_in, dplan: DevicePlan, shard: int, dq_i
     if (dv_in is None) != (dv is None):
         raise ValueError("dv and dv_in: both or neither")
     if dv is not None:
-        _t(dv, "dv", (torch.float32,), (T, hkv, d))
+        _t(dv, "dv", _F32, (T, hkv, d))
         sdv = _rows(dv_in, "dv_in", T, hkv, d)
     for t, n in ((dwq, "dwq"), (dwk, "dwk")):
         if t is not None:
-            _t(t, n, (torch.float32,), (d,))
+            _t(t, n, _F32, (d,))
     _t(ws, "ws")
-    nr = _norm_rope_opts(wq, wk, inv_freq, d, norm, eps, interleaved)
-    with _on(dq, dk, dv, q_in, k_in, dq_in, dk_in, dv_in, dwq, dwk, ws, wq, wk, inv_freq):
+    nr = _norm_rope_opts(wq, wk, inv_freq, d, norm, eps, interleaved, add_dw)
+    with _on(dq, dk, dv, q_in, k_in, dq_in, dk_in, dv_in, dwq, dwk, ws, wq, wk, inv_freq, dplan.buf):
         _check(_lib.fcp_qk_norm_rope_bwd(_ptr(dq), _ptr(dk), _ptr(dv), _ptr(q_in), sq, _ptr(k_in), sk, _ptr(wq),
                                          _ptr(wk), _ptr(inv_freq), C.byref(nr), C.byref(dplan.c), shard,
                                          Dims(T, hq, hkv, d, 0.0), _ptr(dq_in), sdq, _ptr(dk_in), sdk, _ptr(dv_in), sdv,

@@ -188,12 +188,15 @@ class CPAttention:
             dq_in = rows(self.hq) if dq_in is None else dq_in
             dk_in = rows(self.hkv) if dk_in is None else dk_in
             dv_in = rows(self.hkv) if dv_in is None and dv is not None else dv_in
-            if (dwq is None and wq is not None) or (dwk is None and wk is not None):
-                new = torch.zeros(2, self.d, dtype=torch.float32, device=self.device)
-                dwq = new[0] if dwq is None and wq is not None else dwq
-                dwk = new[1] if dwk is None and wk is not None else dwk
+            add = dwq is not None or dwk is not None  # to the given ones: new ones start at zero
+            make = torch.zeros if add else torch.empty
+            if dwq is None and wq is not None:
+                dwq = make(self.d, dtype=torch.float32, device=self.device)
+            if dwk is None and wk is not None:
+                dwk = make(self.d, dtype=torch.float32, device=self.device)
         fcp.qk_norm_rope_bwd(dq, dk, dv, q_in, k_in, self.dplan, shard, dq_in, dk_in, dv_in, dwq, dwk, self.ws, wq=wq,
-                             wk=wk, inv_freq=inv_freq, norm=norm, eps=eps, interleaved=interleaved, stream=stream)
+                             wk=wk, inv_freq=inv_freq, norm=norm, eps=eps, interleaved=interleaved, add_dw=add,
+                             stream=stream)
         return dq_in, dk_in, dv_in, dwq, dwk
 
     def device_status(self) -> int:

@@ -222,8 +222,9 @@ typedef struct {
  * Q and dO ([T][Hq][d] each, the backward's tensor-core operands) and of V and
  * the plan's received V rows (the forward's P*V operands), and the partial
  * sums of the norm weights' gradients (fcp_qk_norm_rope_bwd). The caller
- * zero-fills a new workspace once before its first call: the error word must
- * start at zero (fcp_get_device_status clears it after reporting an error),
+ * zero-fills a new workspace once before its first call: the error word and
+ * the counters beside it in the first 256 bytes must start at zero
+ * (fcp_get_device_status clears the word after reporting an error),
  * and a one-shard backward reads the fp16 Q and dO rows of whole 128-row
  * tiles, rows of other shards included, which must hold finite values (their
  * probabilities are zero, but 0 * NaN is not); each call writes the rows of
@@ -414,9 +415,9 @@ int fcp_rel_buckets(int32_t n_buckets, int32_t max_distance, int32_t* starts);
  * Distances are of documents' tokens, so the result does not depend on the
  * plan. Arguments, layouts, key blocks, workspace and results as
  * fcp_attn_fwd (its partials merge with fcp_merge); `starts` is read during
- * the call, `bias` when the kernel runs. Biases are finite with |b| < 1e30, or
- * at or below -1e30 (the lowest fp32 value and -inf included): such a one
- * masks its bucket. A row with nothing left gets O = 0 and LSE = -inf.
+ * the call, `bias` when the kernel runs. Biases are finite with |b| < 1e30
+ * and b / scale finite, or at or below -1e30 (the lowest fp32 value and -inf
+ * included): such a one masks its bucket. A row with nothing left gets O = 0 and LSE = -inf.
  * Values of q, k, v that no query may see are computed with all the same and
  * have to be finite.
  */
@@ -446,15 +447,16 @@ typedef struct {
   int32_t rot_dim;      /* leading dimensions of a head that turn: 0, 16, 32, ... up to d     */
   int32_t interleaved;  /* pairs of dimensions: 0 (i, i + rot_dim/2), 1 (2i, 2i + 1)          */
   int32_t w_dtype;      /* type of wq and wk: FCP_OUT_BF16 or FCP_OUT_F32                     */
+  int32_t add_dw;       /* gradient: 1 adds to dwq and dwk, 0 writes them                     */
 } fcp_norm_rope;
 
 /*
  * fcp_qk_norm_rope -- norm and rotation of the query and key heads before the
- * attention, at the positions of a packed sequence ([CPGuide] "RoPE and
- * position_ids follow the sharding": a shard's tokens keep their own
- * positions; here a token's position is its index inside its document, taken
- * from the plan). For every token t of the shard (of all shards for shard ==
- * -1) and every head x of its query and key rows:
+ * attention, at the positions of a packed sequence ([CPGuide] asks of RoPE and
+ * the position ids that they follow the sharding: a shard's tokens keep their
+ * own positions. Here a token's position is its index inside its document,
+ * taken from the plan). For every token t of the shard (of all shards for
+ * shard == -1) and every head x of its query and key rows:
  *   n = x / sqrt(mean(x^2) + eps) * w           (norm = 1; else n = x)
  *   y = n with pair i of its first rot_dim dimensions turned by the angle
  *       (t - start of t's document) * inv_freq[i].
@@ -491,8 +493,9 @@ int fcp_qk_norm_rope(const void* q_in, int64_t q_stride, const void* k_in, int64
  *   dq_in, dk_in, dv_in  bf16 rows with their own strides (elements), as
  *             q_in; written only at the shard's rows. dq_in may be q_in itself
  *             (same stride), dk_in k_in; no other overlap.
- *   dwq, dwk  fp32 [d], ACCUMULATED (+=), or NULL. Summed in a fixed order:
- *             equal inputs give equal bits.
+ *   dwq, dwk  fp32 [d] or NULL, written (add_dw = 0) or accumulated (add_dw =
+ *             1, for one shard after another). Summed in a fixed order: equal
+ *             inputs give equal bits.
  *   ws        workspace of fcp_workspace_bytes(dims, plan) bytes.
  * Errors as fcp_qk_norm_rope; FCP_ERR_CAPACITY if the workspace is too small.
  */

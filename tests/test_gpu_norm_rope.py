@@ -172,6 +172,26 @@ def test_shards_make_up_the_whole(cuda, policy):
         assert float((a - b).abs().max()) <= 320 * U * sum(docs) * n * 4
 
 
+def test_a_shard_without_tokens(cuda):
+    """Its weight gradients are zeros where they are written, and nothing else is."""
+    from context_document_masked_gb300 import fcp
+    docs, hq, hkv, d = [1], 2, 1, 64
+    qkv, w, f, (dq, dk, _) = make(docs, hq, hkv, d, d, seed=2)
+    s = session(docs, 2, hq, hkv, d)
+    empty = [j for j in range(2) if s.plan.shard(j)["tokens"] == 0][0]
+    x = qkv.cuda()
+    out = [torch.full((1, h, d), 3.0, dtype=torch.bfloat16, device="cuda") for h in (hq, hkv)]
+    gw = [torch.full((d,), 3.0, device="cuda") for _ in range(2)]
+    args = (dq.cuda(), dk.cuda(), None, *slices(x, hq, hkv)[:2], s.dplan, empty, *out, None, *gw, s.ws)
+    kw = dict(wq=w[0].cuda(), wk=w[1].cuda(), inv_freq=f.cuda())
+    fcp.qk_norm_rope_bwd(*args, **kw, add_dw=True)
+    assert all((t == 3).all() for t in out + gw)
+    fcp.qk_norm_rope_bwd(*args, **kw)
+    assert all((t == 3).all() for t in out) and all((t == 0).all() for t in gw)
+    s.qk_norm_rope(*slices(x, hq, hkv)[:2], **kw, shard=empty, q=out[0], k=out[1])
+    assert all((t == 3).all() for t in out)
+
+
 def test_in_place_and_equal_bits_twice(cuda):
     docs, hq, hkv, d = [500, 12], 4, 2, 128
     qkv, w, f, (dq, dk, dv) = make(docs, hq, hkv, d, d, seed=9)
@@ -185,6 +205,9 @@ def test_in_place_and_equal_bits_twice(cuda):
     for m, n in zip(a, own):
         assert torch.equal(m, n)
     first = s.qk_norm_rope_backward(*g, *slices(x, hq, hkv)[:2], **kw)
+    added = torch.full_like(first[3], 2.0)
+    both = s.qk_norm_rope_backward(*g, *slices(x, hq, hkv)[:2], **kw, dwq=added)
+    assert both[3] is added and torch.equal(added, first[3] + 2.0) and torch.equal(both[4], first[4])
     again = s.qk_norm_rope_backward(*g, *slices(x, hq, hkv)[:2], **kw)
     for m, n in zip(first, again):
         assert torch.equal(m, n)

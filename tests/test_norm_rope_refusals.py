@@ -58,6 +58,7 @@ def options(lib):
         "inf eps": (dict(nr=N(1, float("inf"), D, 0, 1)), inv), "rot over d": (dict(nr=N(1, 1e-6, D + 16, 0, 1)), inv),
         "rot negative": (dict(nr=N(1, 1e-6, -16, 0, 1)), inv), "rot 8": (dict(nr=N(1, 1e-6, 8, 0, 1)), uns),
         "pair order": (dict(nr=N(1, 1e-6, D, 2, 1)), inv), "weight type": (dict(nr=N(1, 1e-6, D, 0, 2)), inv),
+        "add_dw 2": (dict(nr=N(1, 1e-6, D, 0, 1, 2)), inv),
         "no frequencies": (dict(f=None), inv), "misaligned frequencies": (dict(f=at(9, 2)), inv),
         "misaligned weights": (dict(wq=at(9, 2)), inv), "shard": (dict(shard=2), inv),
         "d 96": (dict(dims=lib.dims(2048, HQ, HKV, 96)), uns), "groups": (dict(dims=lib.dims(2048, 5, 2, D)), uns),
@@ -68,7 +69,7 @@ def options(lib):
 
 
 @pytest.mark.parametrize("what", sorted(["no options", "norm 2", "negative eps", "nan eps", "inf eps", "rot over d",
-                                         "rot negative", "rot 8", "pair order", "weight type", "no frequencies",
+                                         "rot negative", "rot 8", "pair order", "weight type", "add_dw 2", "no frequencies",
                                          "misaligned frequencies", "misaligned weights", "shard", "d 96", "groups", "tokens",
                                          "no q_in", "q_in misaligned", "short stride", "odd stride"]))
 def test_options_and_inputs(lib, bound, what):
