@@ -37,6 +37,18 @@
 // group that O_i may be rescaled.
 // The two heads ping-pong: while one softmax group works on its S, the
 // tensor core runs the other head's P*V and next S.
+//
+// With a bias (a separate instantiation: the one without is as it was), s_ij
+// gains b[h][bucket(i - j)]. A warp's tile, 32 rows x 128 keys, holds 159
+// distances. If one bucket has them all, its bias goes into the maximum and
+// into the constant that the exponentials subtract anyway, and costs nothing;
+// otherwise each warp puts the biases by distance into its window in shared
+// memory before it waits for S, and each row adds its 128 entries to S. Rows
+// whose buckets are all masked have no finite score: O = 0, LSE = -inf.
+// 32K workload (32/8 heads, d = 128, 32 buckets): 1.57 ms against 1.48 without;
+// one document of 16K, where more tiles hold several buckets: 1.03 against
+// 0.80. Folding columns of one bucket inside such a tile: 1.69 ms for 1.57, for
+// the spills that it brings at 168 registers a thread.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

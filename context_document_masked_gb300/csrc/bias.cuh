@@ -12,7 +12,9 @@
 // operations: shuffles from a window kept in registers (five instructions an
 // element, 10 KB of code) left the warps waiting for instructions and took
 // 2.05 ms against the plain forward's 1.48 ms on the 32K workload, and 1.6 ms
-// against 0.8 ms on one document of 16K.
+// against 0.8 ms on one document of 16K (16 query and 2 KV heads of 128, 32
+// buckets). Through shared memory: 1.57 and 1.03 ms; the eight warps read
+// a tile's windows in 1,024 cycles, half as many as its products take.
 #pragma once
 
 #include <cstdint>
@@ -80,15 +82,23 @@ __device__ __forceinline__ float bias_over_scale(const float* row, int bucket, f
 // c + 31 - lane. A row's 128 entries are read as 32 float4: four copies of the
 // window, copy k shifted by k entries, give every row an aligned start, and
 // copies 168 floats apart put the eight rows of a quarter-warp into different
-// banks.
+// banks. Distances fall from one entry to a lane's next, 32 below it, and far
+// from the diagonal the bucket is most often the same: it is kept and only
+// looked up again when it is not (16K as above: 1.09 ms with a search for every
+// entry. All entries' loads before the first store: 1.02, but 1.61 for 1.57 on
+// the 32K workload).
 constexpr int kWindowCopy = 168;
 constexpr int kWindowFloats = 4 * kWindowCopy;
 __device__ __forceinline__ void fill_window(float* win, const Buckets& bk, int n, const float* row, int far,
                                             float inv_scale, int lane) {
   __syncwarp();  // every row of the tile before has been read
+  int bucket = n - 1;
 #pragma unroll 1
   for (int y = lane; y < 160; y += 32) {
-    const float b = bias_over_scale(row, bk.of(n, max(far - y, 0)), inv_scale);
+    const int dist = max(far - y, 0);
+    if (dist < kNear) bucket = bk.near[dist];
+    else if (bk.starts[bucket] > dist) bucket = bk.search(n, dist);
+    const float b = bias_over_scale(row, bucket, inv_scale);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (y >= k) win[k * kWindowCopy + y - k] = b;
