@@ -301,7 +301,8 @@ __device__ __forceinline__ void heads_backward(const float* dy, const __nv_bfloa
           gx2 = f2_fma(f2_mul(z[i], wl[i]), x[i], gx2);
         }
         const float ss = head_sum<D / kE>(f2_sum(sq, 0)), gx = head_sum<D / kE>(f2_sum(gx2, 0));
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
+        // No head past the last one: with eps = 0 its 0 x inf would reach acc.
+        const float r = h < n_heads ? rsqrtf(ss * (1.f / D) + p.eps) : 0.f;
         const float m = -r * (r * r * (gx * (1.f / D)));
         const uint64_t r2 = f2(r, r), m2 = f2(m, m);
 #pragma unroll

@@ -118,6 +118,20 @@ def test_forward_and_gradient(cuda, case):
     assert s.device_status() == 0
 
 
+def test_no_eps_and_lanes_without_a_head(cuda):
+    """eps = 0 with head counts that leave lanes without a head: the gradients
+    of the weights are those of the heads alone."""
+    docs, hq, hkv, d = [33], 6, 3, 64
+    qkv, w, f, (dq, dk, _) = make(docs, hq, hkv, d, d, seed=12)
+    s = session(docs, 1, hq, hkv, d)
+    x = qkv.cuda()
+    gq, gk, _, gwq, gwk = s.qk_norm_rope_backward(dq.cuda(), dk.cuda(), None, *slices(x, hq, hkv)[:2], wq=w[0].cuda(),
+                                                  wk=w[1].cuda(), inv_freq=f.cuda(), eps=0.0)
+    xq, xk, _ = slices(qkv, hq, hkv)
+    check_backward(gq, gwq, xq, dq, docs, w[0], f, True, 0.0, False)
+    check_backward(gk, gwk, xk, dk, docs, w[1], f, True, 0.0, False)
+
+
 def test_far_positions(cuda):
     """Rows at the end of a document of 300,000 tokens, every 10,007th before:
     the angle there is 300,000 inv_freq, and must be as exact as at row 1."""
