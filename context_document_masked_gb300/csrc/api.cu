@@ -339,6 +339,12 @@ int fcp_gather_kv(const void* k, const void* v, const fcp_dev_plan* plan, int32_
                             static_cast<cudaStream_t>(stream));
 }
 
+// Whether two arrays of n floats share a byte.
+static bool ranges_meet(const float* a, const float* b, int64_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b), len = 4 * (uintptr_t)n;
+  return x < y + len && y < x + len;
+}
+
 // The table's pointer and the bucket starts (host): the first distance of the
 // first bucket is 0 and none is below the one before.
 static int check_bias(const fcp_rel_bias* b) {
@@ -665,6 +671,8 @@ int fcp_attn_bwd_bias(const void* q, const void* k, const void* v, const void* k
   const int st = check_bias(bias);
   if (st) return st;
   if (!dbias || (reinterpret_cast<uintptr_t>(dbias) & 3)) return FCP_ERR_INVALID_ARG;
+  // Added to while the biases are read.
+  if (dims.hq > 0 && ranges_meet(bias->bias, dbias, (int64_t)dims.hq * bias->n_buckets)) return FCP_ERR_INVALID_ARG;
   return attn_bwd_impl(q, k, v, kbuf, vbuf, out, out_dtype, lse, dout, plan, shard, dims, dq, dk, dv, ws, ws_bytes, stream,
                        bias, dbias);
 }
@@ -795,6 +803,7 @@ int fcp_qk_norm_rope_bwd(const float* dq, const float* dk, const float* dv, cons
   if (!dv != !dv_in || (dv && !strided_ok(dv_in, dv_stride, dims.hkv, dims))) return FCP_ERR_INVALID_ARG;
   if (!nr->norm && (dwq || dwk)) return FCP_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(dwq) & 3) || (reinterpret_cast<uintptr_t>(dwk) & 3)) return FCP_ERR_INVALID_ARG;
+  if (dwq && dwk && ranges_meet(dwq, dwk, dims.d)) return FCP_ERR_INVALID_ARG;
   if (!ws || !aligned16(ws)) return FCP_ERR_INVALID_ARG;
   const WsLayout wl = ws_layout(dims, plan->host->total_remote);
   if (ws_bytes < wl.total) return FCP_ERR_CAPACITY;

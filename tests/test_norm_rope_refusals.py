@@ -98,6 +98,7 @@ def test_overlaps(lib, bound):
     assert bwd(lib, dp, T, dq_in=at(1), so=HQ * D) == inv                         # over dq
     assert bwd(lib, dp, T, dk_in=at(6, HQ * D * 2 - 16)) == inv                   # slices of one row that share values
     assert bwd(lib, dp, T, dq_in=at(4, 16)) == inv
+    assert bwd(lib, dp, T, dwk=at(7)) == inv and bwd(lib, dp, T, dwk=at(7, D * 4 - 4)) == inv   # one gradient over the other
     assert bwd(lib, dp, T, dv=None) == inv and bwd(lib, dp, T, dv_in=None) == inv
 
 

@@ -11,7 +11,7 @@ import synth
 
 torch = pytest.importorskip("torch")
 
-FAKE = C.c_void_p(1 << 24)
+FAKE, FAKE_GRAD = C.c_void_p(1 << 24), C.c_void_p(1 << 25)
 
 
 @pytest.fixture()
@@ -28,7 +28,7 @@ def rel(lib, starts, bias=FAKE, n=None):
     return lib.RelBias(bias, a if starts else None, len(starts) if n is None else n)
 
 
-def calls(lib, dp, dm, rb, dbias=FAKE, ws_bytes=1 << 40):
+def calls(lib, dp, dm, rb, dbias=FAKE_GRAD, ws_bytes=1 << 40):
     r = C.byref(rb) if rb is not None else None
     return (lib.raw_call("fcp_attn_fwd_bias", FAKE, FAKE, FAKE, FAKE, FAKE, r, C.byref(dp), -1, 0, dm.T, dm, 0, FAKE, FAKE,
                          FAKE, ws_bytes, None),
@@ -46,6 +46,10 @@ def test_bias_table_and_starts(lib, bound):
     good = rel(lib, [0, 0, 7])
     assert calls(lib, dp, dm, good, dbias=None)[1] == inv
     assert calls(lib, dp, dm, good, dbias=C.c_void_p((1 << 24) + 1))[1] == inv
+    for off in (0, -44, 44):  # the gradient inside the table of 4 x 3
+        assert calls(lib, dp, dm, good, dbias=C.c_void_p((1 << 24) + off))[1] == inv
+    for off in (-48, 48):
+        assert calls(lib, dp, dm, good, dbias=C.c_void_p((1 << 24) + off), ws_bytes=1024)[1] == lib.ERR_CAPACITY
     assert calls(lib, dp, dm, good, ws_bytes=1024) == (lib.ERR_CAPACITY, lib.ERR_CAPACITY)
     assert calls(lib, dp, lib.dims(dm.T, 4, 2, 96), good) == (uns, uns)
     assert calls(lib, dp, lib.dims(dm.T, 4, 3, 64), good) == (uns, uns)
