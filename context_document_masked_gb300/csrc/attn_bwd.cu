@@ -49,7 +49,7 @@
 // of one bucket (TileSums). The compute warps are the critical path, so they
 // have only the window's adds and, in tiles of several buckets, the sums along
 // the diagonals (add_block). One document of 16K (16 query and 2 KV heads of
-// 128, 32 buckets): 3.57 ms against 2.64 without; the 32K workload 5.31
+// 128, 64 buckets): 3.57 ms against 2.64 without; the 32K workload 5.31
 // against 4.63. Slower: the sums in the compute warps (4.09 and 6.94), by
 // matrix instructions (no faster, for their set-up), in a table for each CTA.
 #include <cuda.h>

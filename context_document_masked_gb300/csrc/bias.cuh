@@ -12,7 +12,7 @@
 // operations: shuffles from a window kept in registers (five instructions an
 // element, 10 KB of code) left the warps waiting for instructions and took
 // 2.05 ms against the plain forward's 1.48 ms on the 32K workload, and 1.6 ms
-// against 0.8 ms on one document of 16K (16 query and 2 KV heads of 128, 32
+// against 0.8 ms on one document of 16K (16 query and 2 KV heads of 128, 64
 // buckets). Through shared memory: 1.57 and 1.03 ms; the eight warps read
 // a tile's windows in 1,024 cycles, half as many as its products take.
 #pragma once
@@ -27,7 +27,9 @@ namespace fcp {
 namespace dev {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMaskBelow = -1e30f;  // a bias at or below this masks its bucket
+// A bias at or below this masks its bucket. Scores near it are 2^-4 apart in
+// fp32: a row with no bucket above it would have no softmax to speak of.
+constexpr float kMaskBelow = -1e6f;
 
 // The buckets in shared memory: their first distances, and the bucket of each
 // distance below kNear (near the diagonal every element needs its own).

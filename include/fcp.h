@@ -415,9 +415,10 @@ int fcp_rel_buckets(int32_t n_buckets, int32_t max_distance, int32_t* starts);
  * Distances are of documents' tokens, so the result does not depend on the
  * plan. Arguments, layouts, key blocks, workspace and results as
  * fcp_attn_fwd (its partials merge with fcp_merge); `starts` is read during
- * the call, `bias` when the kernel runs. Biases are finite with |b| < 1e30
- * and b / scale finite, or at or below -1e30 (the lowest fp32 value and -inf
- * included): such a one masks its bucket. A row with nothing left gets O = 0 and LSE = -inf.
+ * the call, `bias` when the kernel runs. A bias at or below -1e6 (-1e9, the
+ * lowest fp32 value and -inf among them) masks its bucket; the others are below
+ * 1e6. A row with nothing left gets O = 0 and LSE = -inf. (Scores are fp32: the
+ * probabilities are good to about 2^-23 of the largest |s_ij| of a row.)
  * Values of q, k, v that no query may see are computed with all the same and
  * have to be finite.
  */
@@ -431,7 +432,7 @@ int fcp_attn_fwd_bias(const void* q, const void* k, const void* v, const void* k
  * Arguments and results as fcp_attn_bwd, and
  *   dbias  fp32 [hq][n_buckets], ACCUMULATED (+=): dbias[h][u] = sum of dS_ij
  *          over the pairs whose distance is in bucket u (0 for a masked one);
- *          zero it before the first shard. Its terms are the fp16 dS that the
+ *          zero it before the first shard; it may not overlap the biases. Its terms are the fp16 dS that the
  *          dQ and dK products take, added in fp32; like dq, dk and dv it is
  *          added up by atomics, whose order can change its last bits.
  */
@@ -494,8 +495,8 @@ int fcp_qk_norm_rope(const void* q_in, int64_t q_stride, const void* k_in, int64
  *             q_in; written only at the shard's rows. dq_in may be q_in itself
  *             (same stride), dk_in k_in; no other overlap.
  *   dwq, dwk  fp32 [d] or NULL, written (add_dw = 0) or accumulated (add_dw =
- *             1, for one shard after another). Summed in a fixed order: equal
- *             inputs give equal bits.
+ *             1, for one shard after another); not the same array. Summed in
+ *             a fixed order: equal inputs give equal bits.
  *   ws        workspace of fcp_workspace_bytes(dims, plan) bytes.
  * Errors as fcp_qk_norm_rope; FCP_ERR_CAPACITY if the workspace is too small.
  */

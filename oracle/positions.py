@@ -82,10 +82,10 @@ def _scores(q, k, b, starts, scale):
 
 def bias_attention(q, k, v, bias, starts, cu, scale=None, key_block=None):
     """(O, LSE) of document-masked attention with bias[h, bucket(i - j)] added to
-    the scores; a bias of -1e30 or less masks its bucket. Rows with no key left
+    the scores; a bias of -1e6 or less masks its bucket. Rows with no key left
     get O = 0, LSE = -inf. key_block (lo, hi) restricts the keys."""
     q, k, v, bias = to_f64(q), to_f64(k), to_f64(v), to_f64(bias)
-    bias = np.where(bias <= -1e30, -np.inf, bias)
+    bias = np.where(bias <= -1e6, -np.inf, bias)
     T, hq, d = q.shape
     G = hq // k.shape[1]
     scale = default_scale(d) if scale is None else scale
@@ -110,7 +110,7 @@ def bias_attention_bwd(q, k, v, bias, starts, do, cu, scale=None):
     """(dQ, dK, dV, dbias) of bias_attention for an upstream dO."""
     o, lse = bias_attention(q, k, v, bias, starts, cu, scale)
     q, k, v, bias, do = to_f64(q), to_f64(k), to_f64(v), to_f64(bias), to_f64(do)
-    bias = np.where(bias <= -1e30, -np.inf, bias)
+    bias = np.where(bias <= -1e6, -np.inf, bias)
     T, hq, d = q.shape
     G = hq // k.shape[1]
     scale = default_scale(d) if scale is None else scale
