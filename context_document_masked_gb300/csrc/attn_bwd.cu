@@ -49,9 +49,12 @@
 // of one bucket (TileSums). The compute warps are the critical path, so they
 // have only the window's adds and, in tiles of several buckets, the sums along
 // the diagonals (add_block). One document of 16K (16 query and 2 KV heads of
-// 128, 64 buckets): 3.57 ms against 2.64 without; the 32K workload 5.31
-// against 4.63. Slower: the sums in the compute warps (4.09 and 6.94), by
-// matrix instructions (no faster, for their set-up), in a table for each CTA.
+// 128, 64 buckets): 3.43 ms against 2.64 without; the 32K workload 5.25
+// against 4.63. Most of the difference is instructions fetched, not executed
+// (stalls for them 2.4 an issue, 0.35 without a bias): both kinds of sums are
+// 0.5 and 0.2 ms of it, a loop or a call in BiasSteps::load added 0.4 to 0.8.
+// Slower: the sums in the compute warps (4.09 and 6.94), by matrix instructions
+// (no faster, for their set-up), in a table for each CTA.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -155,52 +158,65 @@ __device__ __forceinline__ StepRows step_rows(const BwdItem& it, int G, int j) {
 // With a bias: the statistics and the bias window of each step, which warps
 // 2-3 (64 threads t) bring into shared memory.
 struct BiasSteps {
-  float lse[2], delta[2], win[4];  // the next step's, in registers
+  // The next step's, as they lie in memory: nothing waits for them until they
+  // are stored.
+  float lse[2], delta[2], one, win[4];
+  int sr_h, idx;
   bool windowed;                   // its tile holds several buckets
   float* one_bucket = nullptr;     // else its bucket's place in dbias
   BucketRun seen{0, 0, 0};
 
   __device__ __forceinline__ void load(const BwdParams& p, const BiasParams& bp, const Buckets& bk, const BwdItem& it,
                                        int G, int j, int t) {
-    const StepRows sr = step_rows(it, G, j);
+    if (j == 0) {  // step_rows(it, G, j), one step after another
+      sr_h = it.g * G;
+      idx = 0;
+    } else if (++idx == it.nq) {
+      ++sr_h;
+      idx = 0;
+    }
+    StepRows sr;
+    sr.h = sr_h;
+    sr.q0 = idx < it.na ? it.qa0 + 128 * idx : it.qb0 + 128 * (idx - it.na);
+    sr.q_end = idx < it.na ? it.qa_end : it.qb_end;
     const float* bias_row = bp.bias + (size_t)sr.h * bp.n;
     const int first = sr.q0 - it.key0 - 127;  // distance of window entry 0
     const int near = max(first, 0);
     if (near < seen.lo || near >= seen.hi) bucket_run(seen, bk, bp.n, near);
     windowed = first + 254 >= seen.hi;
     one_bucket = windowed ? nullptr : bp.dbias + (size_t)sr.h * bp.n + seen.bucket;
-    const float one = windowed ? 0.f : bias_log2(bias_row, seen.bucket);
+    one = windowed ? 0.f : __ldg(bias_row + seen.bucket);
+    const size_t row = (size_t)sr.h * p.T + sr.q0 + t;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int r = t + 64 * u;
-      const bool valid = r < min(128, sr.q_end - sr.q0);
-      // Negated, as without a bias. A row whose buckets are all masked (LSE =
-      // -inf) gets P = 0, as the rows past the piece do.
-      const float l = valid ? __ldg(p.lse + (size_t)sr.h * p.T + sr.q0 + r) : -INFINITY;
-      lse[u] = l == -INFINITY ? -INFINITY : one - l * kLog2e;
-      delta[u] = valid ? -__ldg(p.delta + (size_t)sr.h * p.T + sr.q0 + r) : 0.f;
+      const bool valid = t + 64 * u < sr.q_end - sr.q0;
+      lse[u] = valid ? __ldg(p.lse + row + 64 * u) : -INFINITY;
+      delta[u] = valid ? __ldg(p.delta + row + 64 * u) : 0.f;
     }
     if (windowed) {
-      const float inv_scale = 1.f / p.scale;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        win[u] = bias_over_scale(bias_row, bk.of(bp.n, max(first + t + 64 * u, 0)), inv_scale);
+      for (int u = 0; u < 4; ++u) {
+        const int dist = max(first + t + 64 * u, 0);
+        win[u] = __ldg(bias_row + (dist < seen.hi && dist >= kNear ? seen.bucket : bk.of(bp.n, dist)));
+      }
     }
   }
-  __device__ __forceinline__ void store_lse(float* stat, int* windowed_sh, int t) const {
+  __device__ __forceinline__ void store_lse(float* stat, int* windowed_sh, float inv_scale, int t) const {
+    const float add = one <= kMaskBelow ? -INFINITY : one * kLog2e;
+    // Negated, as without a bias. A row whose buckets are all masked (LSE =
+    // -inf) gets P = 0, as the rows past the piece do.
 #pragma unroll
-    for (int u = 0; u < 2; ++u) stat[t + 64 * u] = lse[u];
+    for (int u = 0; u < 2; ++u) stat[t + 64 * u] = lse[u] == -INFINITY ? -INFINITY : add - lse[u] * kLog2e;
     if (windowed) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) stat[256 + t + 64 * u] = win[u];
+      for (int u = 0; u < 4; ++u) stat[256 + t + 64 * u] = win[u] <= kMaskBelow ? -INFINITY : win[u] * inv_scale;
     }
     if (t == 0) *reinterpret_cast<volatile int*>(windowed_sh) = windowed;
   }
   __device__ __forceinline__ void store_delta(float* stat, int t) const {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) stat[128 + t + 64 * u] = delta[u];
+    for (int u = 0; u < 2; ++u) stat[128 + t + 64 * u] = -delta[u];
   }
-
 };
 
 // With a bias: dS summed by buckets (fp32 sums of the stored fp16 values). A
@@ -296,7 +312,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_s_full, bar_dp_full, bar_p_ready, bar_ds_ready, bar_ds_free;
   __shared__ __align__(8) uint64_t bar_dq_full, bar_dq_free, bar_dkdv_full, bar_dkdv_free;
   __shared__ __align__(8) uint64_t bar_stg_full[2], bar_stg_free[2];  // dV / dK staging, per half
-  __shared__ __align__(8) uint64_t bar_lse_full, bar_delta_full;  // bias: LSE and window, D of the step
   __shared__ WorkRing<4> ring;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
@@ -318,12 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar_q_full[s], kBias ? 1 : 2);
       mbar_init(&bar_q_empty[s], 1);
     }
-    mbar_init(&bar_lse_full, 2);
-    mbar_init(&bar_delta_full, 2);
     mbar_init(&bar_do_full, 1);
     mbar_init(&bar_do_empty, 1);
-    mbar_init(&bar_s_full, 1);
-    mbar_init(&bar_dp_full, 1);
+    mbar_init(&bar_s_full, kBias ? 3 : 1);   // with a bias LSE and the window, and D, by warps 2-3
+    mbar_init(&bar_dp_full, kBias ? 3 : 1);
     mbar_init(&bar_p_ready, 256);
     mbar_init(&bar_ds_ready, 256);
     mbar_init(&bar_ds_free, kBias ? 3 : 1);
@@ -596,9 +609,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // With a bias these warps also follow the unit's steps: LSE, D and the
         // bias window of a step go into shared memory as soon as the compute
-        // warps are done with those of the step before, and the dS tile of a
-        // step of one bucket is summed beside its dK and dQ products, half of
-        // the columns by each warp.
+        // warps are done with those of the step before (they arrive at the
+        // barriers of S and of dP, so the compute warps wait no more often),
+        // and the dS tile of a step of one bucket is summed beside its dK and
+        // dQ products, half of the columns by each warp.
         const int nsteps = G * it.nq;
         for (int j = -1; j < nsteps; ++j) {
           const bool more = j + 1 < nsteps;
@@ -612,9 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           if (more) {
-            bias.store_lse(stat, &windowed_sh, t);
+            bias.store_lse(stat, &windowed_sh, 1.f / p.scale, t);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_lse_full);
+            if (lane == 0) mbar_arrive(&bar_s_full);
           }
           if (j >= 0) {
             ok = mbar_wait(&bar_ds_ready, gstep & 1, wc);
@@ -624,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) {
             bias.store_delta(stat, t);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_delta_full);
+            if (lane == 0) mbar_arrive(&bar_dp_full);
           }
           if (j >= 0) {
             if (one_bucket) sums.add(ds_panel, one_bucket, lane);
@@ -666,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (query rows past the piece end have LSE = +inf, hence P = 0).
         const bool unmasked = it.n == 128 && it.key0 + 127 <= q0;
         ok = mbar_wait(&bar_s_full, gstep & 1, wc) &&
-             (kBias ? mbar_wait(&bar_lse_full, gstep & 1, wc) : mbar_wait(&bar_q_full[s], (c >> 1) & 1, wc));
+             (kBias || mbar_wait(&bar_q_full[s], (c >> 1) & 1, wc));
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         const float4* st4 = reinterpret_cast<const float4*>(stat + (kBias ? 0 : s * 256) + 64 * half);
@@ -724,7 +738,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bar_p_ready);
         ok = mbar_wait(&bar_dp_full, gstep & 1, wc);
         if (ok && gstep > 0) ok = mbar_wait(&bar_ds_free, (gstep - 1) & 1, wc);
-        if constexpr (kBias) ok = ok && mbar_wait(&bar_delta_full, gstep & 1, wc);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
         // dS = P (dP - D) in packed fp16: (dP - D) and the product are each

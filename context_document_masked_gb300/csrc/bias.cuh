@@ -188,7 +188,7 @@ __device__ __forceinline__ void diagonal_sums(uint32_t block, int lane, float (&
   float a_lo = 0.f, a_hi = 0.f, b_lo = 0.f, b_hi = 0.f, b_last = 0.f;
 #pragma unroll 1
   for (int half = 0; half < 2; ++half) {
-#pragma unroll 2
+#pragma unroll 1
     for (int c8 = 0; c8 < 4; ++c8) {
       uint32_t v[4];
       ld_shared_v4(block + sw128_offset(lane, 4 * half + c8), v);
