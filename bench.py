@@ -61,8 +61,8 @@ BWD_TRAFFIC_SOURCES = [
     ("context_document_masked_gb300/csrc/tables.cpp", None, None),
 ]
 BWD_TRAFFIC = {   # workload -> {"sha256": ..., "bytes": ...}
-    5: {"sha256": "47684d10ec18d7e05001afc1a3f0340eb85072d6a0f94c694dbc61e20f14d638",
-        "bytes": (17.46 + 17.42 + 239.75 + 144.04) * 1e9},   # preprocess + main kernel
+    5: {"sha256": "1e783b49d793b4b90fcbfee5463709a1805087d20e2ff9669b91947a5a5da9b8",
+        "bytes": (17.46 + 17.42 + 239.92 + 144.11) * 1e9},   # preprocess + main kernel
 }
 
 
