@@ -347,7 +347,8 @@ static bool ranges_meet(const float* a, const float* b, int64_t n) {
 
 // The table's pointer and the bucket starts (host): the first distance of the
 // first bucket is 0 and none is below the one before.
-static int check_bias(const fcp_rel_bias* b) {
+static int check_bias(const fcp_rel_bias* b, const fcp_dims& dims) {
+  if (softmax_scale(dims) < 1e-30f) return FCP_ERR_UNSUPPORTED;  // the kernels add biases over the scale
   if (!b || !b->bias || !b->starts || (reinterpret_cast<uintptr_t>(b->bias) & 3)) return FCP_ERR_INVALID_ARG;
   if (b->n_buckets < 1) return FCP_ERR_INVALID_ARG;
   if (b->n_buckets > FCP_MAX_BUCKETS) return FCP_ERR_UNSUPPORTED;
@@ -495,7 +496,7 @@ int fcp_attn_fwd_bias(const void* q, const void* k, const void* v, const void* k
                       const fcp_rel_bias* bias, const fcp_dev_plan* plan, int32_t shard, int32_t kv_lo, int32_t kv_hi,
                       fcp_dims dims, int32_t out_dtype, void* out, float* lse, void* ws, int64_t ws_bytes,
                       void* stream) {
-  const int st = check_bias(bias);
+  const int st = check_bias(bias, dims);
   if (st) return st;
   return attn_fwd_impl(q, k, v, kbuf, vbuf, plan, shard, kv_lo, kv_hi, dims, out_dtype, out, lse, ws, ws_bytes, stream,
                        -2, false, bias);
@@ -668,7 +669,7 @@ int fcp_attn_bwd_bias(const void* q, const void* k, const void* v, const void* k
                       const fcp_rel_bias* bias, const void* out, int32_t out_dtype, const float* lse, const void* dout,
                       const fcp_dev_plan* plan, int32_t shard, fcp_dims dims, float* dq, float* dk, float* dv,
                       float* dbias, void* ws, int64_t ws_bytes, void* stream) {
-  const int st = check_bias(bias);
+  const int st = check_bias(bias, dims);
   if (st) return st;
   if (!dbias || (reinterpret_cast<uintptr_t>(dbias) & 3)) return FCP_ERR_INVALID_ARG;
   // Added to while the biases are read.

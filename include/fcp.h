@@ -420,7 +420,9 @@ int fcp_rel_buckets(int32_t n_buckets, int32_t max_distance, int32_t* starts);
  * 1e6. A row with nothing left gets O = 0 and LSE = -inf. (Scores are fp32: the
  * probabilities are good to about 2^-23 of the largest |s_ij| of a row.)
  * Values of q, k, v that no query may see are computed with all the same and
- * have to be finite.
+ * have to be finite. Errors as fcp_attn_fwd, FCP_ERR_INVALID_ARG for the
+ * biases and their starts, FCP_ERR_UNSUPPORTED for more than FCP_MAX_BUCKETS
+ * buckets or a scale below 1e-30.
  */
 int fcp_attn_fwd_bias(const void* q, const void* k, const void* v, const void* kbuf, const void* vbuf,
                       const fcp_rel_bias* bias, const fcp_dev_plan* plan, int32_t shard, int32_t kv_lo, int32_t kv_hi,

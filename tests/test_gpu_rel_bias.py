@@ -43,12 +43,12 @@ def make(docs, hq, hkv, d, n, seed, spread=1.0):
     return q, k, v, do, b
 
 
-def reference(q, k, v, do, b, starts, docs):
+def reference(q, k, v, do, b, starts, docs, scale=None):
     """Results and bounds, document by document and head by head."""
     q, k, v, do, b = (A.to_f64(x) for x in (q, k, v, do, b))
     b = np.where(b <= -1e6, -np.inf, b)
     T, hq, d = q.shape
-    G, scale = hq // k.shape[1], 1 / math.sqrt(d)
+    G, scale = hq // k.shape[1], scale or 1 / math.sqrt(d)
     zero = lambda *s: (np.zeros(s), np.zeros(s))  # noqa: E731
     o, lse, dq, db = zero(T, hq, d), zero(hq, T), zero(T, hq, d), zero(*b.shape)
     dk, dv = zero(*k.shape), zero(*v.shape)
@@ -201,6 +201,54 @@ def test_key_blocks_merge_and_shards(cuda):
     assert torch.equal(o, whole[0]) and torch.equal(l, whole[1]) and s.device_status() == 0
     for name, t in zip(("dq", "dk", "dv", "dbias"), g):
         within(t, want, name)
+
+
+@pytest.mark.parametrize("scale", [0.3, 1e-3])
+def test_other_scales(cuda, scale):
+    """The bias is added after the scale, whatever that is."""
+    from context_document_masked_gb300 import fcp
+    from context_document_masked_gb300.session import CPAttention
+    docs, hq, hkv, d = [333, 1, 178], 4, 2, 64
+    starts = fcp.rel_buckets(16, 100)
+    x = make(docs, hq, hkv, d, 16, seed=9)
+    want = reference(*x, starts, docs, scale=float(np.float32(scale)))
+    s = CPAttention(docs, 2, "perdoc", hq, hkv, d, scale=scale)
+    for name, t in zip(("out", "lse", "dq", "dk", "dv", "dbias"), step(s, [t.cuda() for t in x], starts)):
+        within(t, want, name)
+
+
+def test_a_shard_without_tokens(cuda):
+    """It writes nothing and adds nothing."""
+    docs, hq, hkv, d = [1], 2, 1, 64
+    q, k, v, do, b = (t.cuda() for t in make(docs, hq, hkv, d, 2, seed=5))
+    s = session(docs, 2, hq, hkv, d)
+    empty = [j for j in range(2) if s.plan.shard(j)["tokens"] == 0][0]
+    full = lambda *n: torch.full(n, 3.0, device="cuda")  # noqa: E731
+    out, lse, dq, dk, dv, db = full(1, hq, d), full(hq, 1), full(1, hq, d), full(1, hkv, d), full(1, hkv, d), full(hq, 2)
+    s.forward_bias(q, k, v, b, [0, 1], shard=empty, out=out, lse=lse)
+    s.backward_bias(q, k, v, out, lse, do, b, [0, 1], shard=empty, dq=dq, dk=dk, dv=dv, dbias=db, zero_grads=False)
+    assert all((t == 3).all() for t in (out, lse, dq, dk, dv, db)) and s.device_status() == 0
+
+
+def test_two_sessions_at_once(cuda):
+    """Steps of two sessions on two streams, overlapping."""
+    from context_document_masked_gb300 import fcp
+    shapes = [([900, 100], 4, 2, 128, (32, 128)), ([700, 3, 321], 6, 3, 64, (16, 200))]
+    runs = []
+    for n, (docs, hq, hkv, d, bk) in enumerate(shapes):
+        starts = fcp.rel_buckets(*bk)
+        x = make(docs, hq, hkv, d, len(starts), seed=20 + n)
+        runs.append((session(docs, 2, hq, hkv, d), [t.cuda() for t in x], starts, reference(*x, starts, docs), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s, xc, starts, _w, st in runs:
+            with torch.cuda.stream(st):
+                got.append(step(s, xc, starts))
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        for name, t in zip(("out", "lse", "dq", "dk", "dv", "dbias"), g):
+            within(t, runs[i % 2][3], name)
 
 
 def test_without_a_bias_it_is_the_attention(cuda):

@@ -53,6 +53,7 @@ def test_bias_table_and_starts(lib, bound):
     assert calls(lib, dp, dm, good, ws_bytes=1024) == (lib.ERR_CAPACITY, lib.ERR_CAPACITY)
     assert calls(lib, dp, lib.dims(dm.T, 4, 2, 96), good) == (uns, uns)
     assert calls(lib, dp, lib.dims(dm.T, 4, 3, 64), good) == (uns, uns)
+    assert calls(lib, dp, lib.dims(dm.T, 4, 2, 64, 1e-31), good) == (uns, uns)
     dp.counts[2] += 1
     assert calls(lib, dp, dm, good) == (inv, inv)
 
