@@ -717,14 +717,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             p1 = ex2(p1);
             p2 = ex2(p2);
             p3 = ex2(p3);
-            if (!unmasked) {
-              if (!key_valid || e < lim) p0 = 0.f;
-              if (!key_valid || e + 1 < lim) p1 = 0.f;
-              if (!key_valid || e + 2 < lim) p2 = 0.f;
-              if (!key_valid || e + 3 < lim) p3 = 0.f;
-            }
             pk[e >> 1] = pack_f16(p0, p1);
             pk[(e >> 1) + 1] = pack_f16(p2, p3);
+          }
+          // The mask in its own place, off the way of most tiles: the steps' code
+          // does not fit the instruction cache (masking each value above: the
+          // biased step of one 16K document 3.44 ms for 3.13, without a bias 84 us
+          // for 78 at 4096 tokens of 12 heads of 64 and the same on long ones).
+          if (!unmasked) {
+            const int first = key_valid ? lim : 64;
+#pragma unroll
+            for (int e = 0; e < 64; e += 2)
+              pk[e >> 1] &= (e >= first ? 0xFFFFu : 0u) | (e + 1 >= first ? 0xFFFF0000u : 0u);
           }
         }
         {
