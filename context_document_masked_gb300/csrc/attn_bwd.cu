@@ -49,12 +49,14 @@
 // of one bucket (TileSums). The compute warps are the critical path, so they
 // have only the window's adds and, in tiles of several buckets, the sums along
 // the diagonals (add_block). One document of 16K (16 query and 2 KV heads of
-// 128, 64 buckets): 3.43 ms against 2.64 without; the 32K workload 5.25
-// against 4.63. Most of the difference is instructions fetched, not executed
-// (stalls for them 2.4 an issue, 0.35 without a bias): both kinds of sums are
-// 0.5 and 0.2 ms of it, a loop or a call in BiasSteps::load added 0.4 to 0.8.
-// Slower: the sums in the compute warps (4.09 and 6.94), by matrix instructions
-// (no faster, for their set-up), in a table for each CTA.
+// 128, 64 buckets): 2.90 ms against 2.64 without; the 32K workload 4.73
+// against 4.60; 4096 tokens of 12 heads of 64, most of whose tiles hold several
+// buckets: 103 us against 76. The steps' code of all roles together does not
+// fit the instruction cache, so what a step executes counts by its length (the
+// bias took 4.9 ms on the 32K workload with masks and MMAs written out, and
+// another 0.4 to 0.8 with a loop or a call in BiasSteps::load). Slower: the sums
+// in the compute warps, by matrix instructions (no faster, for their set-up),
+// in a table for each CTA.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -136,24 +138,24 @@ __device__ __forceinline__ BwdItem decode(const BwdParams& p, int w) {
   return it;
 }
 
-// Query tile of step j of a unit: head index within the group j / nq, then
-// the first range's tiles and the second range's.
+// The query tiles of a unit's steps: for every head of the group the first
+// range's tiles, then the second range's.
 struct StepRows {
   int h, q0, q_end;
 };
-__device__ __forceinline__ StepRows step_rows(const BwdItem& it, int G, int j) {
-  StepRows r;
-  const int jh = j / it.nq, jj = j - jh * it.nq;
-  r.h = it.g * G + jh;
-  if (jj < it.na) {
-    r.q0 = it.qa0 + jj * 128;
-    r.q_end = it.qa_end;
-  } else {
-    r.q0 = it.qb0 + (jj - it.na) * 128;
-    r.q_end = it.qb_end;
+struct Steps {
+  int h, idx;
+  __device__ __forceinline__ Steps(const BwdItem& it, int G) : h(it.g * G), idx(0) {}
+  __device__ __forceinline__ StepRows rows(const BwdItem& it) const {
+    return idx < it.na ? StepRows{h, it.qa0 + 128 * idx, it.qa_end} : StepRows{h, it.qb0 + 128 * (idx - it.na), it.qb_end};
   }
-  return r;
-}
+  __device__ __forceinline__ void next(const BwdItem& it) {
+    if (++idx == it.nq) {
+      idx = 0;
+      ++h;
+    }
+  }
+};
 
 // With a bias: the statistics and the bias window of each step, which warps
 // 2-3 (64 threads t) bring into shared memory.
@@ -161,24 +163,13 @@ struct BiasSteps {
   // The next step's, as they lie in memory: nothing waits for them until they
   // are stored.
   float lse[2], delta[2], one, win[4];
-  int sr_h, idx;
   bool windowed;                   // its tile holds several buckets
   float* one_bucket = nullptr;     // else its bucket's place in dbias
   BucketRun seen{0, 0, 0};
 
   __device__ __forceinline__ void load(const BwdParams& p, const BiasParams& bp, const Buckets& bk, const BwdItem& it,
-                                       int G, int j, int t) {
-    if (j == 0) {  // step_rows(it, G, j), one step after another
-      sr_h = it.g * G;
-      idx = 0;
-    } else if (++idx == it.nq) {
-      ++sr_h;
-      idx = 0;
-    }
-    StepRows sr;
-    sr.h = sr_h;
-    sr.q0 = idx < it.na ? it.qa0 + 128 * idx : it.qb0 + 128 * (idx - it.na);
-    sr.q_end = idx < it.na ? it.qa_end : it.qb_end;
+                                       const Steps& steps, int t) {
+    const StepRows sr = steps.rows(it);
     const float* bias_row = bp.bias + (size_t)sr.h * bp.n;
     const int first = sr.q0 - it.key0 - 127;  // distance of window entry 0
     const int near = max(first, 0);
@@ -306,6 +297,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ Bias bp) {
   using C = BwdCfg<D>;
   constexpr bool kBias = std::is_same_v<Bias, BiasParams>;
+  // The bias's code does not leave the room in the instruction cache that all
+  // MMAs of a step written out would take (d = 128, the 32K workload: 4.94 ms
+  // for 4.75, two at a time 4.84; d = 64, 4096 tokens of 12 heads: 106 us for
+  // 102). Without a bias they measured as fast or faster written out.
+  constexpr int kMmaUnroll = kBias ? D / 32 : 8;
+  // For the same reason masks have a place of their own there, off the way of
+  // tiles that need none (one document of 16K 3.44 -> 3.13 ms), and for d = 64
+  // (4096 tokens of 12 heads, without a bias 84 -> 77 us); at d = 128 without a
+  // bias they are as well beside the values (512K workload 1.475 s, apart 1.485).
+  constexpr bool kMaskApart = kBias || D == 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar_kv_full, bar_kv_conv, bar_kv_empty, bar_drain;
   __shared__ __align__(8) uint64_t bar_q_full[2], bar_q_empty[2], bar_do_full, bar_do_empty;
@@ -416,8 +417,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // No L2 prefetches: issued through the tensor-memory accelerator, which
       // also carries this CTA's loads and dQ reduce-adds, they cost more in its
       // queue than they saved.
-      for (int j = 0; j < nsteps; ++j) {
-        const StepRows sr = step_rows(it, G, j);
+      Steps steps(it, G);
+      for (int j = 0; j < nsteps; ++j, steps.next(it)) {
+        const StepRows sr = steps.rows(it);
         const int h = sr.h, q0 = sr.q0;
         const int q_rows = min(128, sr.q_end - q0);
         // Q tile and the rows' LSE / D into Q stage s.
@@ -480,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto qaddr = [&](uint32_t c) { return smem_u32(smem + C::kQ + (c & 1) * C::kTile); };
       auto issue_s = [&](uint32_t c) {
         const uint32_t sQ = qaddr(c);
-#pragma unroll
+#pragma unroll(kMmaUnroll)
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
           mma_bf16_ss(tmem + C::kColS, smem_desc_sw128(sK + off, 0, 1024),
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(&bar_s_full);
       };
       auto issue_dp = [&]() {
-#pragma unroll
+#pragma unroll(kMmaUnroll)
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
           mma_bf16_ss(tmem + C::kColDP, smem_desc_sw128(sV + off, 0, 1024),
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j == 0 && items > 0 && !(ok = mbar_wait(&bar_dkdv_free, (items - 1) & 1, wc))) break;
           tc_fence_after();
           // dV += P^T dO, P^T from TMEM: q columns 0-63 in cols [0,32), 64-127 in [64,96).
-#pragma unroll
+#pragma unroll(kMmaUnroll)
           for (int kk = 0; kk < 8; ++kk)
             mma_f16_ts(tmem + C::kColDV, tmem + C::kColS + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8),
                        smem_desc_sw128(sDO + kk * 2048, 16384, 1024), id_kd, (j > 0 || kk > 0));
@@ -534,12 +536,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!(ok = mbar_wait(&bar_ds_ready, gstep & 1, wc))) break;
           tc_fence_after();
-#pragma unroll
+#pragma unroll(kMmaUnroll)
           for (int kk = 0; kk < 8; ++kk)
             mma_bf16_ss(tmem + C::kColDP, smem_desc_sw128(sDS + kk * 2048, 16384, 1024),
                         smem_desc_sw128(sK + kk * 2048, 16384, 1024), id_dq, kk > 0);
           mma_commit(&bar_dq_full);
-#pragma unroll
+#pragma unroll(kMmaUnroll)
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t aoff = (kk >> 2) * 16384 + (kk & 3) * 32;
             mma_bf16_ss(tmem + C::kColDK, smem_desc_sw128(sDS + aoff, 0, 1024),
@@ -614,10 +616,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and the dS tile of a step of one bucket is summed beside its dK and
         // dQ products, half of the columns by each warp.
         const int nsteps = G * it.nq;
+        Steps steps(it, G);
         for (int j = -1; j < nsteps; ++j) {
           const bool more = j + 1 < nsteps;
           float* one_bucket = bias.one_bucket;  // of step j
-          if (more) bias.load(p, bp, buckets, it, G, j + 1, t);
+          if (more) {
+            bias.load(p, bp, buckets, it, steps, t);
+            steps.next(it);
+          }
           if (j < 0) {
             convert();
           } else {
@@ -672,9 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nsteps = G * it.nq;
       const bool key_valid = kr < it.n;
       const int key = it.key0 + kr;
-      for (int j = 0; j < nsteps; ++j, ++gstep) {
+      Steps steps(it, G);
+      for (int j = 0; j < nsteps; ++j, ++gstep, steps.next(it)) {
         const uint32_t c = qc + j, s = c & 1;
-        const int q0 = step_rows(it, G, j).q0;
+        const int q0 = steps.rows(it).q0;
         const int lim = key - q0 - 64 * half;  // local columns below lim cannot see this key
         // Whole tile below the diagonal with 128 keys: no element needs a mask
         // (query rows past the piece end have LSE = +inf, hence P = 0).
@@ -717,14 +724,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             p1 = ex2(p1);
             p2 = ex2(p2);
             p3 = ex2(p3);
+            if (!kMaskApart && !unmasked) {
+              if (!key_valid || e < lim) p0 = 0.f;
+              if (!key_valid || e + 1 < lim) p1 = 0.f;
+              if (!key_valid || e + 2 < lim) p2 = 0.f;
+              if (!key_valid || e + 3 < lim) p3 = 0.f;
+            }
             pk[e >> 1] = pack_f16(p0, p1);
             pk[(e >> 1) + 1] = pack_f16(p2, p3);
           }
-          // The mask in its own place, off the way of most tiles: the steps' code
-          // does not fit the instruction cache (masking each value above: the
-          // biased step of one 16K document 3.44 ms for 3.13, without a bias 84 us
-          // for 78 at 4096 tokens of 12 heads of 64 and the same on long ones).
-          if (!unmasked) {
+          if (kMaskApart && !unmasked) {
             const int first = key_valid ? lim : 64;
 #pragma unroll
             for (int e = 0; e < 64; e += 2)
@@ -777,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&bar_ds_ready);
         if constexpr (kBias) {
           if (windowed)
-            add_block(ds_panel + 4096 * (warp & 3), step_rows(it, G, j).h, buckets, bp,
+            add_block(ds_panel + 4096 * (warp & 3), steps.h, buckets, bp,
                       q0 + 64 * half - it.key0 - 32 * (warp & 3) - 31, lane);
         }
       }
@@ -864,8 +873,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const BwdItem it = decode(p, w);
       if (it.bad) continue;
       const int nsteps = G * it.nq;
-      for (int j = 0; j < nsteps; ++j, ++gstep) {
-        const StepRows sr = step_rows(it, G, j);
+      Steps steps(it, G);
+      for (int j = 0; j < nsteps; ++j, ++gstep, steps.next(it)) {
+        const StepRows sr = steps.rows(it);
         const int h = sr.h, q0 = sr.q0;
         ok = drain_group_all(mbar_wait(&bar_dq_full, gstep & 1, wc));
         if (!ok) break;
