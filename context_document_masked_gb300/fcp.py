@@ -6,6 +6,7 @@ library and raises if it has not been built: there is no fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import os
 
@@ -489,13 +490,13 @@ def rel_buckets(n_buckets: int, max_distance: int) -> np.ndarray:
 
 def _rel_bias(bias, starts, hq):
     """The C struct, and the host array it points to (kept for the call)."""
-    s = starts.tolist() if hasattr(starts, "tolist") else list(starts)
     try:
-        a = (C.c_int32 * len(s))(*s)
-    except TypeError:
-        raise ValueError("starts: one whole number a bucket") from None
-    if not s or min(s) < 0 or max(s) >= 1 << 31:
-        raise ValueError("starts: distances of 0 to 2^31 - 1, one a bucket")
+        s = array.array("i", starts.tolist() if hasattr(starts, "tolist") else starts)
+    except (TypeError, OverflowError):
+        raise ValueError("starts: whole numbers of 0 to 2^31 - 1, one a bucket") from None
+    if not s or s[0] != 0:
+        raise ValueError("starts: one whole number a bucket, the first 0")
+    a = (C.c_int32 * len(s)).from_buffer(s)
     _t(bias, "bias", _F32, (hq, len(s)))
     return RelBias(_ptr(bias), a, len(s)), a
 
