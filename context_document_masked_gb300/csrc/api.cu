@@ -369,6 +369,43 @@ static void set_bias(fcp::BiasParams* p, const fcp_rel_bias* b, float* dbias, fl
   std::copy(b->starts, b->starts + b->n_buckets, p->starts);
 }
 
+// How the biased backward cuts a KV head's query heads into units of their own
+// (dK and dV are added up over the units). One unit for all of them reads K and
+// V once, but where a long document's first key tiles are a large share of the
+// work the other CTAs wait for them. Estimated as the longer of the longest unit
+// and the mean a CTA, a unit's beginning and end counted as three steps. 7001
+// tokens in documents of up to 4096, groups of three heads: 215 us in one unit,
+// 178 in two, 123 in three; one document of 16K, groups of eight: 2.95 ms, four
+// heads a unit 2.84, two 2.89; the 32K workload, which has units enough: 4.80 ms,
+// two heads a unit 5.10.
+static void cut_groups(fcp::BiasParams* b, const Plan* p, int32_t shard, int32_t n_items, const fcp_dims& dims, int sms) {
+  const int G = dims.hq / dims.hkv;
+  b->parts = 1;
+  b->part_heads = G;
+  if (G == 1 || (int64_t)n_items * dims.hkv >= 8 * (int64_t)sms) return;  // units enough to even out
+  constexpr double kEnds = 3;
+  const int32_t t0 = shard < 0 ? 0 : host_at(p, fcp::TB_BSHARD, shard);
+  int64_t sum = 0, longest = 0;
+  for (int32_t i = 0; i < n_items; ++i) {
+    const int64_t t = (int64_t)(t0 + i) * fcp::kBwdTileInts;
+    const int64_t nq = (int64_t)host_at(p, fcp::TB_BTILES, t + 6) + host_at(p, fcp::TB_BTILES, t + 9);
+    sum += nq;
+    longest = std::max(longest, nq);
+  }
+  double best = INFINITY;
+  for (int heads = G; heads >= 1; --heads) {
+    const int parts = (G + heads - 1) / heads;
+    if ((G + parts - 1) / parts != heads) continue;  // as many parts with fewer heads
+    const double mean = ((double)sum * G + kEnds * n_items * parts) * dims.hkv / sms;
+    const double cost = std::max(longest * heads + kEnds, mean);
+    if (cost < best) {
+      best = cost;
+      b->parts = parts;
+      b->part_heads = heads;
+    }
+  }
+}
+
 // Forward over the plan's gathered key layout (ring < -1: own rows from K/V,
 // received rows from kbuf/vbuf) or in ring order (ring >= -1: every needed key
 // from its owner's rows of K/V, owners visited by ring distance; ring = -1 all
@@ -653,7 +690,10 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
   bp.wait_ns = g_wait_ns;
   a.d = dims.d;
   a.num_sms = num_sms();
-  if ((a.has_bias = bias != nullptr)) set_bias(&a.bias, bias, dbias, reinterpret_cast<float*>(wsb + wl.by_distance));
+  if ((a.has_bias = bias != nullptr)) {
+    set_bias(&a.bias, bias, dbias, reinterpret_cast<float*>(wsb + wl.by_distance));
+    cut_groups(&a.bias, p, shard, bp.n_items, dims, a.num_sms);
+  }
   return fcp::launch_attn_bwd(a, s);
 }
 

@@ -98,6 +98,7 @@ struct BwdCfg {
 struct BwdItem {
   int key0, n, src, src_row, qa0, qa_end, na, qb0, qb_end, nb, nq, g;
   bool bad;  // checked build: the unit's table entries are out of range (skip it)
+  int h0, heads;  // the unit's query heads
 };
 
 // Query tiles q0, q0 + 128, ... (n of them) lie inside [0, q_end] and q_end <= T.
@@ -105,8 +106,15 @@ __device__ __forceinline__ bool qrange_ok(int q0, int q_end, int n, int T) {
   return n == 0 || (n > 0 && q0 >= 0 && q_end <= T && (int64_t)q0 + (int64_t)(n - 1) * 128 < q_end);
 }
 
-__device__ __forceinline__ BwdItem decode(const BwdParams& p, int w) {
-  const WorkSlot ws = work_slot(w, p.n_items, p.hkv, p.order_block);
+// Parts that the query heads of a KV head are cut into, a unit each: with a bias
+// as many as the launch says (the form without one adds up dK and dV over the
+// heads of a group in TMEM, in one order).
+__host__ __device__ __forceinline__ int group_parts(const NoBias&) { return 1; }
+__host__ __device__ __forceinline__ int group_parts(const BiasParams& bp) { return bp.parts; }
+
+template <class Bias>
+__device__ __forceinline__ BwdItem decode(const BwdParams& p, const Bias& bias, int G, int w) {
+  const WorkSlot ws = work_slot(w, p.n_items, p.hkv * group_parts(bias), p.order_block);
   const int item = __ldg(p.order + ws.pos);
   BwdItem it;
   it.bad = false;
@@ -129,6 +137,14 @@ __device__ __forceinline__ BwdItem decode(const BwdParams& p, int w) {
   it.nb = __ldg(t + 9);
   it.nq = it.na + it.nb;
   it.g = ws.head;
+  it.h0 = ws.head * G;
+  it.heads = G;
+  if constexpr (std::is_same_v<Bias, BiasParams>) {
+    it.g = ws.head / bias.parts;
+    const int first = (ws.head - it.g * bias.parts) * bias.part_heads;
+    it.h0 = it.g * G + first;
+    it.heads = min(bias.part_heads, G - first);
+  }
   if constexpr (kDeviceChecks) {
     const int rows = it.src ? p.kb_rows : p.T;
     it.bad = it.n < 1 || it.n > 128 || it.key0 < 0 || it.key0 > p.T - it.n || (it.src != 0 && it.src != 1) ||
@@ -145,7 +161,7 @@ struct StepRows {
 };
 struct Steps {
   int h, idx;
-  __device__ __forceinline__ Steps(const BwdItem& it, int G) : h(it.g * G), idx(0) {}
+  __device__ __forceinline__ explicit Steps(const BwdItem& it) : h(it.h0), idx(0) {}
   __device__ __forceinline__ StepRows rows(const BwdItem& it) const {
     return idx < it.na ? StepRows{h, it.qa0 + 128 * idx, it.qa_end} : StepRows{h, it.qb0 + 128 * (idx - it.na), it.qb_end};
   }
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   const WaitCtl wc{&abort_sh, p.err, p.wait_ns};
-  const int n_work = p.n_items * p.hkv;
+  const int n_work = p.n_items * p.hkv * group_parts(bp);
   const int G = p.hq / p.hkv;
   float* stat = reinterpret_cast<float*>(smem + C::kStat);
 
@@ -393,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int w_next = 0;
       if (lane == 0) w_next = next_work(p.work_counter);
       w_next = __shfl_sync(0xffffffffu, w_next, 0);
-      const BwdItem it = decode(p, w);
+      const BwdItem it = decode(p, bp, G, w);
       if (it.bad) {  // checked build: skipped by every role
         if (lane == 0) atomicOr(p.err, kErrBadTable);
         w = w_next;
@@ -413,11 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       ++kv_items;
-      const int nsteps = G * it.nq;
+      const int nsteps = it.heads * it.nq;
       // No L2 prefetches: issued through the tensor-memory accelerator, which
       // also carries this CTA's loads and dQ reduce-adds, they cost more in its
       // queue than they saved.
-      Steps steps(it, G);
+      Steps steps(it);
       for (int j = 0; j < nsteps; ++j, steps.next(it)) {
         const StepRows sr = steps.rows(it);
         const int h = sr.h, q0 = sr.q0;
@@ -504,9 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = ring.get(k, w, wc))) break;
         ring.release(k);
         if (w >= n_work) break;
-        const BwdItem it = decode(p, w);
+        const BwdItem it = decode(p, bp, G, w);
         if (it.bad) continue;
-        const int nsteps = G * it.nq;
+        const int nsteps = it.heads * it.nq;
         if (!(ok = mbar_wait(&bar_kv_conv, kv_items & 1, wc))) break;
         tc_fence_after();
         // Prologue of the unit: S_0 and dP_0.
@@ -586,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w >= n_work) break;
       BwdItem it;
       if constexpr (kDeviceChecks || kBias) {
-        it = decode(p, w);
+        it = decode(p, bp, G, w);
         if (it.bad) continue;
       }
       auto convert = [&]() {
@@ -615,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // barriers of S and of dP, so the compute warps wait no more often),
         // and the dS tile of a step of one bucket is summed beside its dK and
         // dQ products, half of the columns by each warp.
-        const int nsteps = G * it.nq;
-        Steps steps(it, G);
+        const int nsteps = it.heads * it.nq;
+        Steps steps(it);
         for (int j = -1; j < nsteps; ++j) {
           const bool more = j + 1 < nsteps;
           float* one_bucket = bias.one_bucket;  // of step j
@@ -673,12 +689,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) ring.release(k);
       if (w >= n_work) break;
-      const BwdItem it = decode(p, w);
+      const BwdItem it = decode(p, bp, G, w);
       if (it.bad) continue;
-      const int nsteps = G * it.nq;
+      const int nsteps = it.heads * it.nq;
       const bool key_valid = kr < it.n;
       const int key = it.key0 + kr;
-      Steps steps(it, G);
+      Steps steps(it);
       for (int j = 0; j < nsteps; ++j, ++gstep, steps.next(it)) {
         const uint32_t c = qc + j, s = c & 1;
         const int q0 = steps.rows(it).q0;
@@ -870,10 +886,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) ring.release(k);
       if (w >= n_work) break;
-      const BwdItem it = decode(p, w);
+      const BwdItem it = decode(p, bp, G, w);
       if (it.bad) continue;
-      const int nsteps = G * it.nq;
-      Steps steps(it, G);
+      const int nsteps = it.heads * it.nq;
+      Steps steps(it);
       for (int j = 0; j < nsteps; ++j, ++gstep, steps.next(it)) {
         const StepRows sr = steps.rows(it);
         const int h = sr.h, q0 = sr.q0;
@@ -964,13 +980,19 @@ static int launch_bwd_impl(const BwdLaunch& a, const Bias& bias, cudaStream_t st
       return FCP_ERR_CUDA;
     attr_set[dev] = true;
   }
-  const int n_work = a.p.n_items * a.p.hkv;
+  const int parts = group_parts(bias);
+  const int n_work = a.p.n_items * a.p.hkv * parts;
   if (n_work == 0) return FCP_OK;
   const int grid = n_work < a.num_sms ? n_work : a.num_sms;
   // Blocks of key tiles that fill the grid with one KV head: the CTAs running
   // together stream the same query rows (Q, dO, dQ) of that head group.
   BwdParams p = a.p;
-  p.order_block = grid;
+  // Few units go item by item instead, so that the longest come first (4096
+  // tokens of 12 heads of 64, with a bias, 7.7 units a CTA: 93 us for 105; one
+  // document of 16K, 16 heads, 10.5: 2.91 ms for 2.97). With many the rows that
+  // are shared count for more (one of 16K, 32 heads, 42 units: 5.13 ms in blocks,
+  // 5.15 item by item; of 64K 75.6 and 78.8).
+  p.order_block = n_work < 16 * grid ? 1 : grid;
   if constexpr (std::is_same_v<Bias, BiasParams>) {
     if (cudaMemsetAsync(bias.by_distance, 0, sizeof(float) * p.hq * bias.n_distances, st) != cudaSuccess)
       return FCP_ERR_CUDA;

@@ -58,6 +58,7 @@ struct BiasParams {
   float* dbias;            // backward: [hq][n], accumulated
   float* by_distance;      // backward: [hq][n_distances] sums of dS (set to zero by the launch)
   int32_t n_distances;
+  int32_t parts, part_heads;  // backward: units a KV head's query heads are cut into, heads of a unit
   int32_t n;
   int32_t starts[kMaxBuckets];
 };

@@ -115,6 +115,7 @@ CASES = [
     ("each_its_own", [200, 57], 2, "perdoc", 3, 1, 64, list(range(128)), 1.0),
     ("far_reaching", [1700, 40, 300], 4, "perdoc", 6, 2, 128, (128, 1500), 1.0),
     ("large_biases", [333, 180], 1, "perdoc", 4, 4, 128, (16, 100), 1e3),
+    ("many_documents", [1, 2, 3] * 240, 1, "perdoc", 4, 2, 64, (4, 3), 1.0),
     ("mha_wholedoc", [300, 212, 500, 12], 2, "wholedoc", 4, 4, 64, (32, 128), 1.0),
 ]
 
@@ -297,12 +298,12 @@ def test_captured_with_new_biases_and_on_another_stream(cuda):
     assert s.device_status() == 0
 
 
-@pytest.mark.parametrize("which", ["usual", "narrow far off"])
-def test_one_long_document(cuda, which):
+@pytest.mark.parametrize("which,hq", [("usual", 2), ("narrow far off", 2), ("usual", 8)])
+def test_one_long_document(cuda, which, hq):
     """16,385 tokens on four shards against a plain form in 64 bits on the GPU;
     buckets by logarithms up to 8192, and narrow ones past that."""
     from context_document_masked_gb300 import fcp
-    T, hq, hkv, d = 16385, 2, 1, 64
+    T, hkv, d = 16385, 1, 64
     far = [0, 1, 100, 5000, 8180, 8200, 9000, 9003, 9004, 9040, 9041, 12000, 16300]
     starts = fcp.rel_buckets(64, 8192) if which == "usual" else np.array(far)
     x = make([T], hq, hkv, d, len(starts), seed=7)
