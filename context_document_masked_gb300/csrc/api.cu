@@ -350,7 +350,7 @@ static bool ranges_meet(const float* a, const float* b, int64_t n) {
 static int check_bias(const fcp_rel_bias* b, const fcp_dims& dims) {
   if (softmax_scale(dims) < 1e-30f) return FCP_ERR_UNSUPPORTED;  // the kernels add biases over the scale
   if (!b || !b->bias || !b->starts || (reinterpret_cast<uintptr_t>(b->bias) & 3)) return FCP_ERR_INVALID_ARG;
-  if (b->n_buckets < 1) return FCP_ERR_INVALID_ARG;
+  if (b->n_buckets < 1 || (b->zero_grads != 0 && b->zero_grads != 1)) return FCP_ERR_INVALID_ARG;
   if (b->n_buckets > FCP_MAX_BUCKETS) return FCP_ERR_UNSUPPORTED;
   if (b->starts[0] != 0) return FCP_ERR_INVALID_ARG;
   for (int32_t u = 1; u < b->n_buckets; ++u)
@@ -633,6 +633,12 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
   void* q16 = wsb + wl.q16;
   void* do16 = wsb + wl.do16;
 
+  if (bias && bias->zero_grads) {
+    const int64_t n = (int64_t)dims.T * dims.hkv * dims.d * sizeof(float);
+    if (cudaMemsetAsync(dk, 0, n, s) != cudaSuccess || cudaMemsetAsync(dv, 0, n, s) != cudaSuccess ||
+        cudaMemsetAsync(dbias, 0, sizeof(float) * dims.hq * bias->n_buckets, s) != cudaSuccess)
+      return FCP_ERR_CUDA;
+  }
   // Row statistics D_i and dQ = 0 for the shard's query rows.
   int32_t r0 = 0, r1 = plan->counts[fcp::TB_ROWS];
   if (shard >= 0) {

@@ -88,7 +88,8 @@ class NormRope(C.Structure):
 
 
 class RelBias(C.Structure):
-    _fields_ = [("bias", C.c_void_p), ("starts", C.POINTER(C.c_int32)), ("n_buckets", C.c_int32)]
+    _fields_ = [("bias", C.c_void_p), ("starts", C.POINTER(C.c_int32)), ("n_buckets", C.c_int32),
+                ("zero_grads", C.c_int32)]
 
 
 def _load():
@@ -488,7 +489,7 @@ def rel_buckets(n_buckets: int, max_distance: int) -> np.ndarray:
     return out
 
 
-def _rel_bias(bias, starts, hq):
+def _rel_bias(bias, starts, hq, zero_grads=0):
     """The C struct, and the host array it points to (kept for the call)."""
     try:
         s = array.array("i", starts.tolist() if hasattr(starts, "tolist") else starts)
@@ -498,7 +499,7 @@ def _rel_bias(bias, starts, hq):
         raise ValueError("starts: one whole number a bucket, the first 0")
     a = (C.c_int32 * len(s)).from_buffer(s)
     _t(bias, "bias", _F32, (hq, len(s)))
-    return RelBias(_ptr(bias), a, len(s)), a
+    return RelBias(_ptr(bias), a, len(s), int(zero_grads)), a
 
 
 def attn_fwd_bias(q, k, v, kbuf, vbuf, bias, starts, dplan: DevicePlan, shard: int, out, lse, ws, kv_lo: int = 0,
@@ -520,9 +521,9 @@ def attn_fwd_bias(q, k, v, kbuf, vbuf, bias, starts, dplan: DevicePlan, shard: i
 
 
 def attn_bwd_bias(q, k, v, kbuf, vbuf, bias, starts, out, lse, dout, dplan: DevicePlan, shard: int, dq, dk, dv, dbias, ws,
-                  scale: float = 0.0, stream=None):
+                  scale: float = 0.0, zero_grads: bool = False, stream=None):
     """fcp_attn_bwd_bias: attn_bwd of attn_fwd_bias; dbias (fp32 [hq][n]) is
-    accumulated like dk and dv."""
+    accumulated like dk and dv (zero_grads: all three set to zero first)."""
     T, hq, hkv, d = _qkv(q, k, v)
     _kbuf(kbuf, vbuf, dplan, shard, hkv, d)
     _out_lse(out, lse, T, hq, d)
@@ -531,7 +532,7 @@ def attn_bwd_bias(q, k, v, kbuf, vbuf, bias, starts, out, lse, dout, dplan: Devi
     _t(dk, "dk", _F32, (T, hkv, d))
     _t(dv, "dv", _F32, (T, hkv, d))
     _t(ws, "ws")
-    rb, keep = _rel_bias(bias, starts, hq)
+    rb, keep = _rel_bias(bias, starts, hq, zero_grads)
     _t(dbias, "dbias", _F32, tuple(bias.shape))
     out_dtype = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
     with _on(q, k, v, kbuf, vbuf, bias, out, lse, dout, dq, dk, dv, dbias, ws, dplan.buf):

@@ -125,21 +125,13 @@ class CPAttention:
         with _on_stream(stream):
             if dq is None:
                 dq = torch.empty(self.T, self.hq, self.d, dtype=torch.float32, device=self.device)
-            if dk is None and dv is None and dbias is None:  # one fill for the three
-                n = self.T * self.hkv * self.d
-                new = torch.zeros(2 * n + bias.numel(), dtype=torch.float32, device=self.device)
-                dk, dv = new[:2 * n].view(2, self.T, self.hkv, self.d)
-                dbias = new[2 * n:].view(bias.shape)
-            else:
-                given = [x for x in (dk, dv, dbias) if x is not None]
-                dk, dv = (torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device) if x is None else x
-                          for x in (dk, dv))
-                dbias = torch.zeros_like(bias) if dbias is None else dbias
-                if zero_grads:
-                    for x in given:
-                        x.zero_()
+            make = torch.empty if zero_grads else torch.zeros
+            dk, dv = (make(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device) if x is None else x
+                      for x in (dk, dv))
+            if dbias is None:
+                dbias = make(bias.shape, dtype=torch.float32, device=self.device)
         fcp.attn_bwd_bias(q, k, v, self.kbuf, self.vbuf, bias, starts, out, lse, dout, self.dplan, shard, dq, dk, dv, dbias,
-                          self.ws, scale=self.scale, stream=stream)
+                          self.ws, scale=self.scale, zero_grads=zero_grads, stream=stream)
         return dq, dk, dv, dbias
 
     def backward(self, q, k, v, out, lse, dout, shard: int = -1, dq=None, dk=None, dv=None,

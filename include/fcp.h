@@ -395,6 +395,7 @@ typedef struct {
   const float* bias;      /* device fp32 [hq][n_buckets], 4-byte aligned               */
   const int32_t* starts;  /* host int32[n_buckets]: starts[0] = 0, none below the last */
   int32_t n_buckets;      /* 1 .. FCP_MAX_BUCKETS                                      */
+  int32_t zero_grads;     /* backward: 1 sets all of dk, dv and dbias to zero first    */
 } fcp_rel_bias;
 
 /*
@@ -434,7 +435,8 @@ int fcp_attn_fwd_bias(const void* q, const void* k, const void* v, const void* k
  * Arguments and results as fcp_attn_bwd, and
  *   dbias  fp32 [hq][n_buckets], ACCUMULATED (+=): dbias[h][u] = sum of dS_ij
  *          over the pairs whose distance is in bucket u (0 for a masked one);
- *          zero it before the first shard; it may not overlap the biases. Its terms are the fp16 dS that the
+ *          zero it (and dk, dv) before the first shard, or let the call do it
+ *          (zero_grads = 1); it may not overlap the biases. Its terms are the fp16 dS that the
  *          dQ and dK products take, added in fp32; like dq, dk and dv it is
  *          added up by atomics, whose order can change its last bits.
  */

@@ -433,6 +433,11 @@ def test_refusals_on_gpu_tensors(cuda):
         with pytest.raises((ValueError, fcp.FcpError)):
             s.forward_bias(q, k, v, b, starts)
     out, lse = s.forward_bias(q, k, v, b, [0, 1], out_dtype=torch.float32)
+    g = [torch.full_like(t, 5.0) for t in s.backward_bias(q, k, v, out, lse, do, b, [0, 1])]
+    given = dict(zip(("dq", "dk", "dv", "dbias"), g))
+    want = s.backward_bias(q, k, v, out, lse, do, b, [0, 1])
+    for name, t, w in zip(given, s.backward_bias(q, k, v, out, lse, do, b, [0, 1], **given), want):   # set to zero first
+        assert t is given[name] and torch.allclose(t, w, rtol=0, atol=1e-5)
     with pytest.raises(ValueError):
         s.backward_bias(q, k, v, out, lse, do, b, [0, 1], dbias=torch.zeros(hq, 3, device="cuda"))
     with pytest.raises(ValueError):

@@ -43,6 +43,10 @@ def test_bias_table_and_starts(lib, bound):
                    (rel(lib, []), inv), (rel(lib, [0, 1], n=0), inv), (rel(lib, [0, 1], n=-3), inv), (rel(lib, [1, 2]), inv),
                    (rel(lib, [-1, 2]), inv), (rel(lib, [0, 5, 4]), inv), (rel(lib, list(range(129))), uns)):
         assert calls(lib, dp, dm, rb) == (st, st)
+    for flag in (-1, 2):
+        rb = rel(lib, [0, 1])
+        rb.zero_grads = flag
+        assert calls(lib, dp, dm, rb) == (inv, inv)
     good = rel(lib, [0, 0, 7])
     assert calls(lib, dp, dm, good, dbias=None)[1] == inv
     assert calls(lib, dp, dm, good, dbias=C.c_void_p((1 << 24) + 1))[1] == inv
