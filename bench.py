@@ -61,8 +61,8 @@ BWD_TRAFFIC_SOURCES = [
     ("context_document_masked_gb300/csrc/tables.cpp", None, None),
 ]
 BWD_TRAFFIC = {   # workload -> {"sha256": ..., "bytes": ...}
-    5: {"sha256": "1e783b49d793b4b90fcbfee5463709a1805087d20e2ff9669b91947a5a5da9b8",
-        "bytes": (17.46 + 17.42 + 239.92 + 144.11) * 1e9},   # preprocess + main kernel
+    5: {"sha256": "9399f6ec8d945887f97c1f4f488c8c79ea07c45ae7fd77a7f5c949c4a0edfcc2",
+        "bytes": (17.46 + 17.42 + 239.54 + 143.77) * 1e9},   # preprocess + main kernel
 }
 
 

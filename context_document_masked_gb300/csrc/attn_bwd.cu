@@ -49,9 +49,9 @@
 // of one bucket (TileSums). The compute warps are the critical path, so they
 // have only the window's adds and, in tiles of several buckets, the sums along
 // the diagonals (add_block). One document of 16K (16 query and 2 KV heads of
-// 128, 64 buckets): 2.90 ms against 2.64 without; the 32K workload 4.73
+// 128, 64 buckets): 2.92 ms against 2.58 without; the 32K workload 4.81
 // against 4.60; 4096 tokens of 12 heads of 64, most of whose tiles hold several
-// buckets: 103 us against 76. The steps' code of all roles together does not
+// buckets: 93 us against 72. The steps' code of all roles together does not
 // fit the instruction cache, so what a step executes counts by its length (the
 // bias took 4.9 ms on the 32K workload with masks and MMAs written out, and
 // another 0.4 to 0.8 with a loop or a call in BiasSteps::load). Slower: the sums

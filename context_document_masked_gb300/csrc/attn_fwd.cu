@@ -46,8 +46,8 @@
 // memory before it waits for S, and each row adds its 128 entries to S. Rows
 // whose buckets are all masked have no finite score: O = 0, LSE = -inf.
 // 32K workload (32/8 heads, d = 128, 32 buckets): 1.57 ms against 1.48 without;
-// one document of 16K, where more tiles hold several buckets: 1.03 against
-// 0.80. Folding columns of one bucket inside such a tile: 1.69 ms for 1.57, for
+// one document of 16K, where more tiles hold several buckets: 1.01 against
+// 0.78. Folding columns of one bucket inside such a tile: 1.69 ms for 1.57, for
 // the spills that it brings at 168 registers a thread.
 #include <cuda.h>
 #include <cuda_runtime.h>

@@ -13,7 +13,7 @@
 // element, 10 KB of code) left the warps waiting for instructions and took
 // 2.05 ms against the plain forward's 1.48 ms on the 32K workload, and 1.6 ms
 // against 0.8 ms on one document of 16K (16 query and 2 KV heads of 128, 64
-// buckets). Through shared memory: 1.57 and 1.03 ms; the eight warps read
+// buckets). Through shared memory: 1.57 and 1.01 ms; the eight warps read
 // a tile's windows in 1,024 cycles, half as many as its products take.
 #pragma once
 
