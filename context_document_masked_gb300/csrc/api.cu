@@ -645,11 +645,16 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
     r0 = host_at(p, fcp::TB_RSHARD, shard);
     r1 = host_at(p, fcp::TB_RSHARD, shard + 1);
   }
+  int32_t piece0 = 0, n_pieces = 0;  // this shard's pieces in the table
+  for (int32_t j = 0; j <= shard; ++j) {
+    piece0 += n_pieces;
+    n_pieces = (int32_t)p->shards[j].pieces.size();
+  }
   st = fcp::launch_bwd_preprocess(out, out_dtype == FCP_OUT_F32, dout, q, table(plan, fcp::TB_ROWS),
                                   table(plan, fcp::TB_IDENT) + r0, r1 - r0, plan->counts[fcp::TB_ROWS], dims.T,
                                   dims.hq, dims.d,
-                                  delta, dq, q16, do16, static_cast<int*>(ws),
-                                  reinterpret_cast<int*>(wsb + kWorkCounterOff), s);
+                                  delta, dq, q16, do16, table(plan, fcp::TB_PIECES) + 8 * (int64_t)piece0, n_pieces,
+                                  static_cast<int*>(ws), reinterpret_cast<int*>(wsb + kWorkCounterOff), s);
   if (st) return st;
 
   fcp::BwdLaunch a;

@@ -201,7 +201,10 @@ __global__ void __launch_bounds__(kMergeThreads)
 // D_i = <dO_i, O_i> (the row term of dS = P (dP - D)), dQ rows zeroed so the
 // backward kernel can accumulate into them, and fp16 copies of Q and dO (the
 // backward's tensor-core operands; exact for bf16 values inside the fp16
-// range, error bit 4 otherwise).
+// range, error bit 4 otherwise). A one-shard call also clears the copies' rows
+// between each piece's end and the end of its last query tile, as far as the
+// shard's next piece leaves them to others: the backward loads whole tiles, and
+// whatever the workspace held there would meet P = 0, where 0 x NaN is NaN.
 constexpr int kPreThreads = 256;
 
 __device__ __forceinline__ uint32_t cvt_pair(uint32_t x, bool& ovf) {
@@ -217,7 +220,8 @@ __global__ void __launch_bounds__(kPreThreads)
                       const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ rows,
                       const int32_t* __restrict__ order, int n_chunks, int n_rows_table, int T, int hq,
                       float* __restrict__ delta, float* __restrict__ dq, __half* __restrict__ q16,
-                      __half* __restrict__ do16, int* __restrict__ err, int* __restrict__ zero_word) {
+                      __half* __restrict__ do16, const int32_t* __restrict__ pieces, int n_pieces,
+                      int* __restrict__ err, int* __restrict__ zero_word) {
   if (zero_word && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *zero_word = 0;
   // A chunk's rows, all heads, are one contiguous [rows][hq][D] block. Each
   // thread takes 8 consecutive elements (16-byte loads of dO and Q, 16 or 32
@@ -291,6 +295,23 @@ __global__ void __launch_bounds__(kPreThreads)
         const int u = g / L;  // (row, head) within the chunk
         delta[(int64_t)(u % hq) * T + r0 + u / hq] = s;
       }
+    }
+  }
+  for (int k = blockIdx.x; k < n_pieces; k += gridDim.x) {
+    const int32_t* piece = pieces + 8 * k;
+    const int start = __ldg(piece + 2), end = __ldg(piece + 3);
+    const int64_t tile_end = start + ((int64_t)end - start + 127) / 128 * 128;
+    const int stop = (int)min(tile_end, (int64_t)(k + 1 < n_pieces ? __ldg(piece + 8 + 2) : T));
+    if constexpr (kDeviceChecks) {
+      if (start < 0 || end <= start || end > T || stop > T) {
+        if (threadIdx.x == 0) atomicOr(err, kErrBadTable);
+        continue;
+      }
+    }
+    const int64_t e1 = (int64_t)stop * hq * D;
+    for (int64_t e = (int64_t)end * hq * D + 8 * (threadIdx.x + kPreThreads * blockIdx.y); e < e1; e += 8 * stride) {
+      *reinterpret_cast<uint4*>(q16 + e) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(do16 + e) = make_uint4(0, 0, 0, 0);
     }
   }
   if (ovf) atomicOr(err, 4);
@@ -484,15 +505,15 @@ int launch_bwd_preprocess(const void* out, bool out_f32, const void* dout, const
                           const int32_t* rows, const int32_t* order, int32_t n_chunks, int32_t n_rows_table,
                           int32_t T,
                           int32_t hq, int32_t d, float* delta, float* dq, void* q16, void* do16,
-                          int* err, int* zero_word, cudaStream_t st) {
+                          const int32_t* pieces, int32_t n_pieces, int* err, int* zero_word, cudaStream_t st) {
   if (n_chunks == 0 && !zero_word) return FCP_OK;
   const dim3 grid(n_chunks > 0 ? n_chunks : 1, 8);  // a chunk's (row, head) pairs over 8 blocks
   using B = __nv_bfloat16;
   auto go = [&](auto kernel) {
     kernel<<<grid, kPreThreads, 0, st>>>(out, static_cast<const B*>(dout), static_cast<const B*>(q),
                                          rows, order, n_chunks, n_rows_table, T, hq, delta, dq,
-                                         static_cast<__half*>(q16), static_cast<__half*>(do16), err,
-                                         zero_word);
+                                         static_cast<__half*>(q16), static_cast<__half*>(do16), pieces, n_pieces,
+                                         err, zero_word);
   };
   if (d == 128)
     out_f32 ? go(preprocess_kernel<128, true>) : go(preprocess_kernel<128, false>);

@@ -117,12 +117,15 @@ int64_t wait_limit_ns();
 // *zero_word (if not null) is set to 0: the work counter of the kernel that
 // follows in the same stream.
 // n_rows_table: entries of `rows` (the checked build bounds the chunk indices).
+// pieces: the shard's n_pieces entries of the piece table, ascending, whose last
+// tiles' rows past the pieces are set to zero in the copies; none (0) for a
+// call over all shards, which writes every row.
 int launch_bwd_preprocess(const void* out, bool out_f32, const void* dout, const void* q,
                           const int32_t* rows,
                           const int32_t* order, int32_t n_chunks, int32_t n_rows_table, int32_t T, int32_t hq,
                           int32_t d,
-                          float* delta, float* dq, void* q16, void* do16, int* err, int* zero_word,
-                          cudaStream_t st);
+                          float* delta, float* dq, void* q16, void* do16, const int32_t* pieces,
+                          int32_t n_pieces, int* err, int* zero_word, cudaStream_t st);
 
 // fp16 copy of a bf16 array of n_elems (a multiple of 8) elements; *zero_word
 // (if not null) is set to 0, as above.

@@ -224,11 +224,9 @@ typedef struct {
  * sums of the norm weights' gradients (fcp_qk_norm_rope_bwd). The caller
  * zero-fills a new workspace once before its first call: the error word and
  * the counters beside it in the first 256 bytes must start at zero
- * (fcp_get_device_status clears the word after reporting an error),
- * and a one-shard backward reads the fp16 Q and dO rows of whole 128-row
- * tiles, rows of other shards included, which must hold finite values (their
- * probabilities are zero, but 0 * NaN is not); each call writes the rows of
- * its own shard before reading them. Calls that share a workspace must be
+ * (fcp_get_device_status clears the word after reporting an error). Behind
+ * these each call writes what it reads, so one workspace that is large enough
+ * serves several plans and shapes. Calls that share a workspace must be
  * ordered on the GPU (one stream, or synchronised): two at once would race on
  * these contents. */
 int64_t fcp_workspace_bytes(fcp_dims dims, const fcp_plan_t* plan);
