@@ -268,8 +268,8 @@ int fcp_plan_upload(const fcp_plan_t* plan, void* dev_buf, int64_t bytes, void* 
 }
 
 // Workspace layout (each region 256-byte aligned): [0, 256) error word (byte
-// 0) and the persistent kernels' work counter (byte kWorkCounterOff); D_i
-// (fp32 [Hq][T]); fp16 copies of Q and dO ([T][Hq][d] each, backward); fp16
+// 0) and the persistent kernels' work counter (byte kWorkCounterOff); the
+// backward's row statistics D_i and LSE (fp32 [Hq][T] each); fp16 copies of Q and dO ([T][Hq][d] each, backward); fp16
 // copies of V ([T][Hkv][d]) and of the received V rows ([R][Hkv][d], R = all
 // shards' remote rows of the plan), the forward's P*V operands; e4m3 copies
 // of Q, K and the received K rows; partial sums of the norm weights' gradients;
@@ -279,18 +279,21 @@ int fcp_plan_upload(const fcp_plan_t* plan, void* dev_buf, int64_t bytes, void* 
 constexpr int64_t kWorkCounterOff = 64;
 
 struct WsLayout {
-  int64_t delta, q16, do16, v16, vb16, q8, k8, kb8, partial, by_distance, total;
+  int64_t delta, lse2, q16, do16, v16, vb16, q8, k8, kb8, partial, by_distance, total;
 };
 
 // Header words of the e4m3 Q K^T forward: amax bits of Q and K, then their
 // scales 2^kq and 2^kk.
 constexpr int64_t kQkAmaxOff = 128;
 constexpr int64_t kQkScaleOff = 136;
+// Range of the backward's operands (zero between calls).
+constexpr int64_t kRangeOff = 144;
 // Diagnostic counter of the forward: online-softmax rescales of O after a
 // query tile's first key tile (one count per warp and event).
 constexpr int64_t kRescaleCountOff = 192;
 // Tickets of the norm weights' gradients (zero between calls).
 constexpr int64_t kTicketsOff = 68;
+static_assert(kRangeOff + (int64_t)sizeof(fcp::BwdRange) <= kRescaleCountOff, "range inside the header");
 static_assert(kTicketsOff + (1 + fcp::kNormRopeGroups) * 4 <= kQkAmaxOff, "tickets inside the header");
 
 static int64_t ws_align(int64_t x) { return (x + 255) / 256 * 256; }
@@ -300,7 +303,8 @@ static WsLayout ws_layout(const fcp_dims& d, int64_t remote_rows) {
                 dd = std::max(d.d, 0);
   WsLayout w;
   w.delta = 256;
-  w.q16 = w.delta + ws_align(hq * T * 4);
+  w.lse2 = w.delta + ws_align(hq * T * 4);
+  w.q16 = w.lse2 + ws_align(hq * T * 4);
   w.do16 = w.q16 + ws_align(T * hq * dd * 2);
   w.v16 = w.do16 + ws_align(T * hq * dd * 2);
   w.vb16 = w.v16 + ws_align(T * hkv * dd * 2);
@@ -630,6 +634,8 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* wsb = static_cast<char*>(ws);
   float* delta = reinterpret_cast<float*>(wsb + wl.delta);
+  float* lse2 = reinterpret_cast<float*>(wsb + wl.lse2);
+  fcp::BwdRange* range = reinterpret_cast<fcp::BwdRange*>(wsb + kRangeOff);
   void* q16 = wsb + wl.q16;
   void* do16 = wsb + wl.do16;
 
@@ -639,7 +645,7 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
         cudaMemsetAsync(dbias, 0, sizeof(float) * dims.hq * bias->n_buckets, s) != cudaSuccess)
       return FCP_ERR_CUDA;
   }
-  // Row statistics D_i and dQ = 0 for the shard's query rows.
+  // Row statistics and dQ = 0 for the shard's query rows, and the operands' range.
   int32_t r0 = 0, r1 = plan->counts[fcp::TB_ROWS];
   if (shard >= 0) {
     r0 = host_at(p, fcp::TB_RSHARD, shard);
@@ -650,11 +656,35 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
     piece0 += n_pieces;
     n_pieces = (int32_t)p->shards[j].pieces.size();
   }
-  st = fcp::launch_bwd_preprocess(out, out_dtype == FCP_OUT_F32, dout, q, table(plan, fcp::TB_ROWS),
-                                  table(plan, fcp::TB_IDENT) + r0, r1 - r0, plan->counts[fcp::TB_ROWS], dims.T,
-                                  dims.hq, dims.d,
-                                  delta, dq, q16, do16, table(plan, fcp::TB_PIECES) + 8 * (int64_t)piece0, n_pieces,
-                                  static_cast<int*>(ws), reinterpret_cast<int*>(wsb + kWorkCounterOff), s);
+  fcp::PreLaunch pre;
+  std::memset(&pre, 0, sizeof(pre));
+  pre.out = out;
+  pre.out_f32 = out_dtype == FCP_OUT_F32;
+  pre.lse = lse;
+  pre.dout = static_cast<const __nv_bfloat16*>(dout);
+  pre.q = static_cast<const __nv_bfloat16*>(q);
+  pre.v = static_cast<const __nv_bfloat16*>(v);
+  pre.vbuf = static_cast<const __nv_bfloat16*>(vbuf);
+  pre.v_rows = shard < 0 ? 0 : rrows;  // over all shards they are copies of V's own rows
+  pre.rows = table(plan, fcp::TB_ROWS);
+  pre.order = table(plan, fcp::TB_IDENT) + r0;
+  pre.n_chunks = r1 - r0;
+  pre.n_rows_table = plan->counts[fcp::TB_ROWS];
+  pre.T = dims.T;
+  pre.hq = dims.hq;
+  pre.hkv = dims.hkv;
+  pre.delta = delta;
+  pre.lse2 = lse2;
+  pre.dq = dq;
+  pre.q16 = static_cast<__half*>(q16);
+  pre.do16 = static_cast<__half*>(do16);
+  pre.range = range;
+  pre.pieces = table(plan, fcp::TB_PIECES) + 8 * (int64_t)piece0;
+  pre.n_pieces = n_pieces;
+  pre.num_sms = num_sms();
+  pre.err = static_cast<int*>(ws);
+  pre.zero_word = reinterpret_cast<int*>(wsb + kWorkCounterOff);
+  st = fcp::launch_bwd_preprocess(pre, dims.d, s);
   if (st) return st;
 
   fcp::BwdLaunch a;
@@ -689,11 +719,12 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
   bp.hkv = dims.hkv;
   bp.scale = softmax_scale(dims);
   bp.scale_log2 = bp.scale * 1.4426950408889634f;
-  bp.lse = lse;
+  bp.lse2 = lse2;
   bp.delta = delta;
   bp.dq = dq;
   bp.dk = dk;
   bp.dv = dv;
+  bp.range = range;
   bp.err = static_cast<int*>(ws);
   bp.work_counter = reinterpret_cast<int*>(wsb + kWorkCounterOff);
   bp.n_tiles = plan->counts[fcp::TB_BTILES];

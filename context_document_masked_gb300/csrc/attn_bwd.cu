@@ -25,8 +25,17 @@
 // Tensor-core operands are fp16 (11 significant bits against bf16's 8): Q and
 // dO arrive as fp16 copies made by the preprocess pass, K and V tiles are
 // converted from bf16 in shared memory once per work unit, and P and dS are
-// rounded to fp16. Every bf16 input inside the fp16 range converts exactly;
-// P <= 1 and |dS| stay far inside it.
+// rounded to fp16. fp16 keeps its 11 bits from 2^-14 up and a call's gradients
+// may be of any size, so dO, V, P and dS are scaled by powers of two. With e_i
+// the exponent that the preprocess took out of row i of dO (its norm is then in
+// [1, 2)), E the largest of them and 2^v above every |V_j| of the call,
+//   P_ij 2^(10 + e_i - E) <= 2^10,  |dP_ij - D_i| 2^(-e_i - v) < 2^2,
+// and their product, dS 2^(10 - E - v), is below 2^12: there is room for
+// probabilities of up to 8 (an LSE of another precision's scores), and P keeps
+// all its bits down to 2^-24. Results are scaled back where they leave the
+// kernel. The factors ride on operations that were there: the exponent of P,
+// V's conversion, the epilogues' products. Q and K are as they are: exact from
+// 2^-17 up, below that off by 2^-25 at most.
 //
 // CTA roles (512 threads, persistent):
 //   warp 0       loads (TMA for K, V, Q, dO; plain loads for LSE and D)
@@ -73,6 +82,27 @@ using namespace dev;
 namespace {
 
 constexpr int kThreads = 512;
+
+// The call's scaling (see above), made by one thread of each CTA.
+constexpr int kProbExp = 10;
+struct Scaling {
+  float lse_add;   // 10 - E
+  float v;         // 2^-v
+  float dv;        // 2^(E - 10)
+  float ds;        // 2^(E - 10 + v)
+  float dqk;       // that times the softmax scale
+  __device__ __forceinline__ void init(const BwdRange* r, float scale) {
+    const int e_max = (int)__ldcg(&r->e_max);
+    const int field = (int)(__ldcg(&r->v2) >> 23);  // exponent of |V|^2: 255 for inf and NaN
+    const int E = e_max ? e_max - kRowExpBias : 0;
+    const int ve = field == 255 ? 20 : ((field - 127) >> 1) + 1;
+    lse_add = (float)(kProbExp - E);
+    v = scalbnf(1.f, -ve);
+    dv = scalbnf(1.f, E - kProbExp);
+    ds = scalbnf(1.f, E - kProbExp + ve);
+    dqk = scale * ds;
+  }
+};
 
 template <int D>
 struct BwdCfg {
@@ -197,7 +227,7 @@ struct BiasSteps {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const bool valid = t + 64 * u < sr.q_end - sr.q0;
-      lse[u] = valid ? __ldg(p.lse + row + 64 * u) : -INFINITY;
+      lse[u] = valid ? __ldg(p.lse2 + row + 64 * u) : -INFINITY;
       delta[u] = valid ? __ldg(p.delta + row + 64 * u) : 0.f;
     }
     if (windowed) {
@@ -208,21 +238,21 @@ struct BiasSteps {
       }
     }
   }
-  __device__ __forceinline__ void store_lse(float* stat, int* windowed_sh, float inv_scale, int t) const {
-    const float add = one <= kMaskBelow ? -INFINITY : one * kLog2e;
-    // Negated, as without a bias. A row whose buckets are all masked (LSE =
-    // -inf) gets P = 0, as the rows past the piece do.
+  __device__ __forceinline__ void store_lse(float* stat, int* windowed_sh, float inv_scale, float lse_add, int t) const {
+    const float add = (one <= kMaskBelow ? -INFINITY : one * kLog2e) + lse_add;
+    // Negated, as without a bias. A row whose buckets are all masked (-inf)
+    // gets P = 0, as the rows past the piece do.
 #pragma unroll
-    for (int u = 0; u < 2; ++u) stat[t + 64 * u] = lse[u] == -INFINITY ? -INFINITY : add - lse[u] * kLog2e;
+    for (int u = 0; u < 2; ++u) stat[t + 64 * u] = add + lse[u];
     if (windowed) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) stat[256 + t + 64 * u] = win[u] <= kMaskBelow ? -INFINITY : win[u] * inv_scale;
     }
     if (t == 0) *reinterpret_cast<volatile int*>(windowed_sh) = windowed;
   }
-  __device__ __forceinline__ void store_delta(float* stat, int t) const {
+  __device__ __forceinline__ void store_delta(float* stat, float v_scale, int t) const {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) stat[128 + t + 64 * u] = -delta[u];
+    for (int u = 0; u < 2; ++u) stat[128 + t + 64 * u] = -delta[u] * v_scale;
   }
 };
 
@@ -238,15 +268,15 @@ struct TileSums {
   float sum = 0.f;
   float* at = nullptr;  // the bucket's place in dbias
 
-  __device__ __forceinline__ void add(uint32_t panel, float* to, int lane) {
+  __device__ __forceinline__ void add(uint32_t panel, float* to, const Buckets& bk, int lane) {
     if (to != at) {
-      flush(lane);
+      flush(bk, lane);
       at = to;
     }
     sum += panel_sum(panel, lane);
   }
-  __device__ __forceinline__ void flush(int lane) {
-    if (at) add_run(at, sum, lane);
+  __device__ __forceinline__ void flush(const Buckets& bk, int lane) {
+    if (at) add_run(at, sum, bk.ds_scale, lane);
   }
 };
 // block: the stored dS; base: distance of its diagonal 0 (column 0, row 31).
@@ -257,6 +287,8 @@ static __device__ __noinline__ void add_block(uint32_t block, int h, const Bucke
   __syncwarp();  // the warp's rows are stored
   float d[3];
   diagonal_sums(block, lane, d);
+#pragma unroll
+  for (int w = 0; w < 3; ++w) d[w] *= bk.ds_scale;
 #pragma unroll 1
   for (int w = 0; w < 3; ++w, base += 32) {
     const int dist = base + lane;
@@ -332,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ WorkRing<4> ring;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
+  __shared__ Scaling scaling;
   __shared__ std::conditional_t<kBias, Buckets, NoBias> buckets;
   __shared__ int windowed_sh;  // bias: the step's tile spans several buckets
 
@@ -367,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ring.init(1 + 2 + 8 + 4);  // MMA thread, conversion, compute and dQ warps
     abort_sh = 0;
+    scaling.init(p.range, p.scale);
+    if constexpr (kBias) buckets.ds_scale = scaling.ds;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -397,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ loads
     uint32_t kv_items = 0, qc = 0, dc = 0;
     uint32_t issued_q[2] = {0, 0};
+    const float lse_add = scaling.lse_add, v_scale = scaling.v;
     bool ok = true;
     uint32_t k = 0;
     for (int w = blockIdx.x; ok;) {
@@ -458,8 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool valid = r < q_rows;
             // Stored negated (-LSE log2 e, -D): the compute warps add them with
             // packed f32x2 arithmetic. Rows past the piece get P = 0.
-            st[r] = valid ? -__ldg(p.lse + (size_t)h * p.T + q0 + r) * kLog2e : -INFINITY;
-            st[128 + r] = valid ? -__ldg(p.delta + (size_t)h * p.T + q0 + r) : 0.f;
+            st[r] = valid ? __ldg(p.lse2 + (size_t)h * p.T + q0 + r) + lse_add : -INFINITY;
+            st[128 + r] = valid ? -__ldg(p.delta + (size_t)h * p.T + q0 + r) * v_scale : 0.f;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar_q_full[s]);
@@ -590,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t items = 0, gstep = 0;
     bool ok = true, ovf = false;
     uint4* kv = reinterpret_cast<uint4*>(smem + C::kK);  // K and V tiles are contiguous
+    const float v_scale = scaling.v;
     BiasSteps bias;
     TileSums sums;
     const uint32_t ds_panel = smem_u32(smem + C::kDS) + (warp - 2) * 16384;
@@ -608,14 +645,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto convert = [&]() {
         ok = mbar_wait(&bar_kv_full, items & 1, wc);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; return; }
-#pragma unroll 4
-        for (int i = t; i < 2 * C::kTile / 16; i += 64) {
+        constexpr int kVecs = C::kTile / 16;
+        auto one = [&](int i, float mul) {
           uint4 x = kv[i];
-          x.x = bf16x2_to_f16x2(x.x, ovf);
-          x.y = bf16x2_to_f16x2(x.y, ovf);
-          x.z = bf16x2_to_f16x2(x.z, ovf);
-          x.w = bf16x2_to_f16x2(x.w, ovf);
+          x.x = bf16x2_to_f16x2(x.x, mul, ovf);
+          x.y = bf16x2_to_f16x2(x.y, mul, ovf);
+          x.z = bf16x2_to_f16x2(x.z, mul, ovf);
+          x.w = bf16x2_to_f16x2(x.w, mul, ovf);
           kv[i] = x;
+        };
+        // K as it is, V scaled. With a bias the shorter code wins (the 32K
+        // workload: 4.84 ms for 4.95), without one the longer (4.62 for 4.64).
+        if constexpr (kBias) {
+          float mul = 1.f;
+#pragma unroll 1
+          for (int of_v = 0; of_v < 2; ++of_v, mul = v_scale)
+#pragma unroll 2
+            for (int i = t + of_v * kVecs; i < (of_v + 1) * kVecs; i += 64) one(i, mul);
+        } else {
+#pragma unroll 4
+          for (int i = t; i < 2 * kVecs; i += 64) one(i, i < kVecs ? 1.f : v_scale);
         }
         fence_proxy_async_smem();
         mbar_arrive(&bar_kv_conv);
@@ -648,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           if (more) {
-            bias.store_lse(stat, &windowed_sh, 1.f / p.scale, t);
+            bias.store_lse(stat, &windowed_sh, 1.f / p.scale, scaling.lse_add, t);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_s_full);
           }
@@ -658,19 +707,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++gstep;
           }
           if (more) {
-            bias.store_delta(stat, t);
+            bias.store_delta(stat, scaling.v, t);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_dp_full);
           }
           if (j >= 0) {
-            if (one_bucket) sums.add(ds_panel, one_bucket, lane);
+            if (one_bucket) sums.add(ds_panel, one_bucket, buckets, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_ds_free);
           }
         }
       }
     }
-    if constexpr (kBias) sums.flush(lane);
+    if constexpr (kBias) sums.flush(buckets, lane);
     if (ovf) atomicOr(p.err, 4);
   } else if (warp < 12) {
     // ------------------------------------------------------------ P and dS
@@ -769,8 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && gstep > 0) ok = mbar_wait(&bar_ds_free, (gstep - 1) & 1, wc);
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
         tc_fence_after();
-        // dS = P (dP - D) in packed fp16: (dP - D) and the product are each
-        // rounded to fp16, the operand type of the dK and dQ products.
+        // dS = P (dP - D), scaled, in packed fp16: (dP - D) and the product are
+        // each rounded to fp16, the operand type of the dK and dQ products.
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           float v[32];
@@ -784,11 +833,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             float a0, a1, a2, a3;
             f2_split(f2_add(f2(v[e], v[e + 1]), f2(d4.x, d4.y)), a0, a1);
             f2_split(f2_add(f2(v[e + 2], v[e + 3]), f2(d4.z, d4.w)), a2, a3);
-            const __half2 x01 = __floats2half2_rn(a0, a1);
-            const __half2 x23 = __floats2half2_rn(a2, a3);
+            // Saturated: rows of other keys in the tile may pass the range, and
+            // their P = 0 is to give 0.
+            const uint32_t x01 = pack_f16_sat(a0, a1), x23 = pack_f16_sat(a2, a3);
             const uint32_t p01 = pk[col >> 1], p23 = pk[(col >> 1) + 1];
-            const __half2 r01 = __hmul2(*reinterpret_cast<const __half2*>(&p01), x01);
-            const __half2 r23 = __hmul2(*reinterpret_cast<const __half2*>(&p23), x23);
+            const __half2 r01 = __hmul2(*reinterpret_cast<const __half2*>(&p01), *reinterpret_cast<const __half2*>(&x01));
+            const __half2 r23 = __hmul2(*reinterpret_cast<const __half2*>(&p23), *reinterpret_cast<const __half2*>(&x23));
             o[e >> 1] = *reinterpret_cast<const uint32_t*>(&r01);
             o[(e >> 1) + 1] = *reinterpret_cast<const uint32_t*>(&r23);
           }
@@ -818,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc_fence_after();
       const uint32_t src_col = lane_base + (half == 0 ? C::kColDV : C::kColDK);
-      const float mul = half == 0 ? 1.f : p.scale;
+      const float mul = half == 0 ? scaling.dv : scaling.dqk;
       const CUtensorMap* tm_out = half == 0 ? &tm_dv : &tm_dk;
       // Two chunks in registers: the TMEM read of chunk cc + 2 is issued once
       // chunk cc is staged and waited for two chunks later, so its latency
@@ -877,6 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     uint8_t* stage = smem + C::kStage;
+    const float mul = scaling.dqk;
     uint32_t gstep = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
@@ -914,12 +965,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t b0 = smem_u32(stage), b1 = smem_u32(stage + 16384);
 #pragma unroll
           for (int q4 = 0; q4 < 8; ++q4) {
-            st_shared_v4(b0 + sw128_offset(r, q4), __float_as_uint(a[4 * q4] * p.scale),
-                         __float_as_uint(a[4 * q4 + 1] * p.scale), __float_as_uint(a[4 * q4 + 2] * p.scale),
-                         __float_as_uint(a[4 * q4 + 3] * p.scale));
-            st_shared_v4(b1 + sw128_offset(r, q4), __float_as_uint(b[4 * q4] * p.scale),
-                         __float_as_uint(b[4 * q4 + 1] * p.scale), __float_as_uint(b[4 * q4 + 2] * p.scale),
-                         __float_as_uint(b[4 * q4 + 3] * p.scale));
+            st_shared_v4(b0 + sw128_offset(r, q4), __float_as_uint(a[4 * q4] * mul),
+                         __float_as_uint(a[4 * q4 + 1] * mul), __float_as_uint(a[4 * q4 + 2] * mul),
+                         __float_as_uint(a[4 * q4 + 3] * mul));
+            st_shared_v4(b1 + sw128_offset(r, q4), __float_as_uint(b[4 * q4] * mul),
+                         __float_as_uint(b[4 * q4 + 1] * mul), __float_as_uint(b[4 * q4 + 2] * mul),
+                         __float_as_uint(b[4 * q4 + 3] * mul));
           }
           if (pr + 1 < kPairs) {
             tmem_ld32(lane_base + C::kColDP + 64 * (pr + 1), a);
@@ -949,6 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  // The last CTA leaves the range as the next call expects it (every CTA has
+  // read it: its scaling is older than its share of `done`).
+  if (tid == 0 && atomicAdd(&p.range->done, 1) == (int)gridDim.x - 1) *p.range = BwdRange{0, 0, 0};
 }
 
 }  // namespace

@@ -37,6 +37,7 @@ constexpr int kNear = 128;
 struct Buckets {
   int starts[kMaxBuckets];
   uint8_t near[kNear];
+  float ds_scale;  // backward: what the stored dS are multiplied by
 
   __device__ __forceinline__ void init(const BiasParams& bp, int tid, int threads) {
     for (int i = tid; i < bp.n; i += threads) starts[i] = bp.starts[i];
@@ -124,11 +125,11 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Adds the warp's sum of v to *at and sets v back to zero.
-__device__ __forceinline__ void add_run(float* at, float& v, int lane) {
+// Adds the warp's sum of v, times mul, to *at and sets v back to zero.
+__device__ __forceinline__ void add_run(float* at, float& v, float mul, int lane) {
   if (!__any_sync(0xffffffffu, v != 0.f)) return;
   const float sum = warp_sum(v);
-  if (lane == 0 && sum != 0.f) red_add(at, sum);
+  if (lane == 0 && sum != 0.f) red_add(at, sum * mul);
   v = 0.f;
 }
 

@@ -200,12 +200,20 @@ __global__ void __launch_bounds__(kMergeThreads)
 // ------------------------------------------------------- bwd preprocess
 // D_i = <dO_i, O_i> (the row term of dS = P (dP - D)), dQ rows zeroed so the
 // backward kernel can accumulate into them, and fp16 copies of Q and dO (the
-// backward's tensor-core operands; exact for bf16 values inside the fp16
-// range, error bit 4 otherwise). A one-shard call also clears the copies' rows
+// backward's tensor-core operands; error bit 4 for a value beyond the fp16
+// range). A one-shard call also clears the copies' rows
 // between each piece's end and the end of its last query tile, as far as the
 // shard's next piece leaves them to others: the backward loads whole tiles, and
 // whatever the workspace held there would meet P = 0, where 0 x NaN is NaN.
+//
+// Sizes. fp16 keeps 11 bits from 2^-14 up, and a loss averaged over a long
+// sequence gives gradients far below. So a row's dO_i is divided by the power of
+// two 2^e that brings its norm to [1, 2) (exact, and so is every product
+// with it), D_i with it, and e goes into the exponent of the row's
+// probabilities: P_ij 2^e times dO_i 2^-e. The backward takes the largest e and
+// the largest |V_j| of the call from `range` (BwdRange).
 constexpr int kPreThreads = 256;
+constexpr int kSquareExp = 40;  // squares are of dO 2^40: no underflow down to 2^-103
 
 __device__ __forceinline__ uint32_t cvt_pair(uint32_t x, bool& ovf) {
   const float lo = __uint_as_float(x << 16), hi = __uint_as_float(x & 0xFFFF0000u);
@@ -214,56 +222,77 @@ __device__ __forceinline__ uint32_t cvt_pair(uint32_t x, bool& ovf) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// Largest |V_j|^2 of n 16-byte groups (L of them a row and head), as this
+// thread's share; first and step are the same for a warp's lanes but for the lane.
+template <int L>
+__device__ __forceinline__ void v_norms(const uint4* v, int64_t n, int64_t first, int64_t step, int lane, float& most) {
+  for (int64_t g = first; g - lane < n; g += step) {
+    const uint4 x = g < n ? __ldg(v + g) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
+      s = fmaf(lo, lo, fmaf(hi, hi, s));
+    }
+#pragma unroll
+    for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    most = s > most || s != s ? s : most;
+  }
+}
+
 template <int D, bool OF32>
-__global__ void __launch_bounds__(kPreThreads)
-    preprocess_kernel(const void* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
-                      const __nv_bfloat16* __restrict__ q, const int32_t* __restrict__ rows,
-                      const int32_t* __restrict__ order, int n_chunks, int n_rows_table, int T, int hq,
-                      float* __restrict__ delta, float* __restrict__ dq, __half* __restrict__ q16,
-                      __half* __restrict__ do16, const int32_t* __restrict__ pieces, int n_pieces,
-                      int* __restrict__ err, int* __restrict__ zero_word) {
-  if (zero_word && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *zero_word = 0;
+__global__ void __launch_bounds__(kPreThreads) preprocess_kernel(const PreLaunch p) {
+  if (p.zero_word && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.zero_word = 0;
   // A chunk's rows, all heads, are one contiguous [rows][hq][D] block. Each
   // thread takes 8 consecutive elements (16-byte loads of dO and Q, 16 or 32
   // bytes of O); L = D / 8 lanes hold one (row, head) and reduce its D_i.
   constexpr int L = D / 8;
+  constexpr float kLog2e = 1.4426950408889634f;
   const int lane = threadIdx.x & 31;
   const int stride = kPreThreads * gridDim.y;
+  const int first = threadIdx.x + kPreThreads * blockIdx.y;
   bool ovf = false;
-  for (int c = blockIdx.x; c < n_chunks; c += gridDim.x) {
-    const int chunk = __ldg(order + c);
+  unsigned e_max = 0;
+  float v2 = 0.f;
+  for (int c = blockIdx.x; c < p.n_chunks; c += gridDim.x) {
+    const int chunk = __ldg(p.order + c);
     if constexpr (kDeviceChecks) {
-      if (chunk < 0 || chunk >= n_rows_table) {
-        if (threadIdx.x == 0) atomicOr(err, kErrBadTable);
+      if (chunk < 0 || chunk >= p.n_rows_table) {
+        if (threadIdx.x == 0) atomicOr(p.err, kErrBadTable);
         continue;
       }
     }
-    const int r0 = __ldg(rows + 2 * chunk), nr = __ldg(rows + 2 * chunk + 1);
+    const int r0 = __ldg(p.rows + 2 * chunk), nr = __ldg(p.rows + 2 * chunk + 1);
     if constexpr (kDeviceChecks) {
-      if (nr < 0 || r0 < 0 || r0 > T - nr) {
-        if (threadIdx.x == 0) atomicOr(err, kErrBadTable);
+      if (nr < 0 || r0 < 0 || r0 > p.T - nr) {
+        if (threadIdx.x == 0) atomicOr(p.err, kErrBadTable);
         continue;
       }
     }
-    const int total = nr * hq * L;  // 16-byte groups of the chunk
-    const int64_t e0 = (int64_t)r0 * hq * D;
+    const int total = nr * p.hq * L;  // 16-byte groups of the chunk
+    const int64_t e0 = (int64_t)r0 * p.hq * D;
     // Warp-uniform trip count: every lane of a warp takes part in the
     // shuffles; lanes past the end hold s = 0 and store nothing.
-    for (int g = threadIdx.x + kPreThreads * blockIdx.y; g - lane < total; g += stride) {
+    for (int g = first; g - lane < total; g += stride) {
       const bool live = g < total;
       const int64_t base = e0 + (int64_t)g * 8;
+      const int u = g / L;  // (row, head) within the chunk
+      const int64_t stat = (int64_t)(u % p.hq) * p.T + r0 + u / p.hq;
       uint4 b = make_uint4(0, 0, 0, 0), x = b;
       float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      float lse = 0.f;
       if (live) {
-        b = __ldg(reinterpret_cast<const uint4*>(dout + base));
-        x = __ldg(reinterpret_cast<const uint4*>(q + base));
+        b = __ldg(reinterpret_cast<const uint4*>(p.dout + base));
+        x = __ldg(reinterpret_cast<const uint4*>(p.q + base));
+        if (g % L == 0) lse = __ldg(p.lse + stat);
         if constexpr (OF32) {
-          const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(out) + base);
-          const float4 a0 = __ldg(p), a1 = __ldg(p + 1);
+          const float4* po = reinterpret_cast<const float4*>(static_cast<const float*>(p.out) + base);
+          const float4 a0 = __ldg(po), a1 = __ldg(po + 1);
           o[0] = a0.x; o[1] = a0.y; o[2] = a0.z; o[3] = a0.w;
           o[4] = a1.x; o[5] = a1.y; o[6] = a1.z; o[7] = a1.w;
         } else {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(out) + base));
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.out) + base));
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -274,52 +303,90 @@ __global__ void __launch_bounds__(kPreThreads)
       }
       const uint32_t bw[4] = {b.x, b.y, b.z, b.w}, xw[4] = {x.x, x.y, x.z, x.w};
       uint32_t oq[4], od[4];
-      float s = 0.f;
+      float y[8], s = 0.f, s2 = 0.f;  // dO 2^40, its products with O and its squares
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s = fmaf(o[2 * i], __uint_as_float(bw[i] << 16), s);
-        s = fmaf(o[2 * i + 1], __uint_as_float(bw[i] & 0xFFFF0000u), s);
+        const float lo = __uint_as_float(bw[i] << 16), hi = __uint_as_float(bw[i] & 0xFFFF0000u);
+        ovf |= fabsf(lo) > 65504.f || fabsf(hi) > 65504.f;
+        y[2 * i] = lo * __int_as_float((127 + kSquareExp) << 23);
+        y[2 * i + 1] = hi * __int_as_float((127 + kSquareExp) << 23);
+        s = fmaf(o[2 * i], y[2 * i], s);
+        s = fmaf(o[2 * i + 1], y[2 * i + 1], s);
+        s2 = fmaf(y[2 * i], y[2 * i], s2);
+        s2 = fmaf(y[2 * i + 1], y[2 * i + 1], s2);
         oq[i] = cvt_pair(xw[i], ovf);
-        od[i] = cvt_pair(bw[i], ovf);
+      }
+#pragma unroll
+      for (int m = L / 2; m > 0; m >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, m);
+        s2 += __shfl_xor_sync(0xffffffffu, s2, m);
+      }
+      // |dO_i| 2^40 is in [2^h, 2^(h + 1)), h = floor(log2(s2) / 2) from s2's
+      // exponent field (0 for a row of zeros: the smallest e, -104).
+      const int h = (((__float_as_int(s2) >> 23) & 255) - 127) >> 1;
+      const int e = h - kSquareExp;
+      const float f = __int_as_float((127 - h) << 23);  // 2^(-e - 40), in [2^-64, 2^64]
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 r = __floats2half2_rn(y[2 * i] * f, y[2 * i + 1] * f);
+        od[i] = *reinterpret_cast<const uint32_t*>(&r);
       }
       if (live) {
-        *reinterpret_cast<uint4*>(q16 + base) = make_uint4(oq[0], oq[1], oq[2], oq[3]);
-        *reinterpret_cast<uint4*>(do16 + base) = make_uint4(od[0], od[1], od[2], od[3]);
-        float4* z = reinterpret_cast<float4*>(dq + base);
+        *reinterpret_cast<uint4*>(p.q16 + base) = make_uint4(oq[0], oq[1], oq[2], oq[3]);
+        *reinterpret_cast<uint4*>(p.do16 + base) = make_uint4(od[0], od[1], od[2], od[3]);
+        float4* z = reinterpret_cast<float4*>(p.dq + base);
         z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
         z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-#pragma unroll
-      for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
       if (live && (g % L) == 0) {
-        const int u = g / L;  // (row, head) within the chunk
-        delta[(int64_t)(u % hq) * T + r0 + u / hq] = s;
+        p.delta[stat] = s * f;
+        const bool sees = lse != -INFINITY;  // -inf: every key masked by its bias
+        p.lse2[stat] = sees ? fmaf(-lse, kLog2e, (float)e) : -INFINITY;
+        if (sees) e_max = max(e_max, (unsigned)(e + kRowExpBias));
       }
     }
+    v_norms<L>(reinterpret_cast<const uint4*>(p.v + (int64_t)r0 * p.hkv * D), (int64_t)nr * p.hkv * L, first, stride, lane,
+               v2);
   }
-  for (int k = blockIdx.x; k < n_pieces; k += gridDim.x) {
-    const int32_t* piece = pieces + 8 * k;
+  v_norms<L>(reinterpret_cast<const uint4*>(p.vbuf), p.v_rows * p.hkv * L, first + (int64_t)stride * blockIdx.x,
+             (int64_t)stride * gridDim.x, lane, v2);
+  for (int k = blockIdx.x; k < p.n_pieces; k += gridDim.x) {
+    const int32_t* piece = p.pieces + 8 * k;
     const int start = __ldg(piece + 2), end = __ldg(piece + 3);
     const int64_t tile_end = start + ((int64_t)end - start + 127) / 128 * 128;
-    const int stop = (int)min(tile_end, (int64_t)(k + 1 < n_pieces ? __ldg(piece + 8 + 2) : T));
+    const int stop = (int)min(tile_end, (int64_t)(k + 1 < p.n_pieces ? __ldg(piece + 8 + 2) : p.T));
     if constexpr (kDeviceChecks) {
-      if (start < 0 || end <= start || end > T || stop > T) {
-        if (threadIdx.x == 0) atomicOr(err, kErrBadTable);
+      if (start < 0 || end <= start || end > p.T || stop > p.T) {
+        if (threadIdx.x == 0) atomicOr(p.err, kErrBadTable);
         continue;
       }
     }
-    const int64_t e1 = (int64_t)stop * hq * D;
-    for (int64_t e = (int64_t)end * hq * D + 8 * (threadIdx.x + kPreThreads * blockIdx.y); e < e1; e += 8 * stride) {
-      *reinterpret_cast<uint4*>(q16 + e) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(do16 + e) = make_uint4(0, 0, 0, 0);
+    const int64_t e1 = (int64_t)stop * p.hq * D;
+    for (int64_t e = (int64_t)end * p.hq * D + 8 * first; e < e1; e += 8 * stride) {
+      *reinterpret_cast<uint4*>(p.q16 + e) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(p.do16 + e) = make_uint4(0, 0, 0, 0);
     }
   }
-  if (ovf) atomicOr(err, 4);
+  if (ovf) atomicOr(p.err, 4);
+  // The block's maxima into the range (fp32 bits of numbers >= 0 order as the
+  // numbers, a NaN above them).
+  __shared__ unsigned most[2][kPreThreads / 32];
+  e_max = __reduce_max_sync(0xffffffffu, e_max);
+  const unsigned v_max = __reduce_max_sync(0xffffffffu, __float_as_uint(v2) & 0x7FFFFFFFu);
+  if (lane == 0) most[0][threadIdx.x >> 5] = e_max, most[1][threadIdx.x >> 5] = v_max;
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    unsigned m = 0;
+#pragma unroll
+    for (int w = 0; w < kPreThreads / 32; ++w) m = max(m, most[threadIdx.x][w]);
+    unsigned* at = threadIdx.x ? &p.range->v2 : &p.range->e_max;
+    if (m > __ldcg(at)) atomicMax(at, m);
+  }
 }
 
 // ------------------------------------------------------- bf16 -> fp16
-// fp16 copy of a bf16 tensor (exact inside the fp16 range; error bit 4 when a
-// value exceeds it). The forward's P*V product runs on fp16 operands.
+// fp16 copy of a bf16 tensor (exact from 2^-17 up, below that off by 2^-25 at
+// most; error bit 4 when a value exceeds the fp16 range). The forward's P*V product runs on fp16 operands.
 constexpr int kCvtThreads = 256;
 
 __global__ void __launch_bounds__(kCvtThreads)
@@ -501,24 +568,17 @@ int launch_merge(const float* o_parts, const float* lse_parts, int32_t B, int64_
   return cudaGetLastError() == cudaSuccess ? FCP_OK : FCP_ERR_CUDA;
 }
 
-int launch_bwd_preprocess(const void* out, bool out_f32, const void* dout, const void* q,
-                          const int32_t* rows, const int32_t* order, int32_t n_chunks, int32_t n_rows_table,
-                          int32_t T,
-                          int32_t hq, int32_t d, float* delta, float* dq, void* q16, void* do16,
-                          const int32_t* pieces, int32_t n_pieces, int* err, int* zero_word, cudaStream_t st) {
-  if (n_chunks == 0 && !zero_word) return FCP_OK;
-  const dim3 grid(n_chunks > 0 ? n_chunks : 1, 8);  // a chunk's (row, head) pairs over 8 blocks
-  using B = __nv_bfloat16;
-  auto go = [&](auto kernel) {
-    kernel<<<grid, kPreThreads, 0, st>>>(out, static_cast<const B*>(dout), static_cast<const B*>(q),
-                                         rows, order, n_chunks, n_rows_table, T, hq, delta, dq,
-                                         static_cast<__half*>(q16), static_cast<__half*>(do16), pieces, n_pieces,
-                                         err, zero_word);
-  };
+int launch_bwd_preprocess(const PreLaunch& a, int32_t d, cudaStream_t st) {
+  if (a.n_chunks == 0 && !a.zero_word) return FCP_OK;
+  // A chunk's (row, head) pairs over 8 blocks, over more where that leaves SMs idle.
+  int parts = 8;
+  while (parts < 32 && (int64_t)a.n_chunks * parts < 8 * (int64_t)a.num_sms) parts *= 2;
+  const dim3 grid(a.n_chunks > 0 ? a.n_chunks : 1, parts);
+  auto go = [&](auto kernel) { kernel<<<grid, kPreThreads, 0, st>>>(a); };
   if (d == 128)
-    out_f32 ? go(preprocess_kernel<128, true>) : go(preprocess_kernel<128, false>);
+    a.out_f32 ? go(preprocess_kernel<128, true>) : go(preprocess_kernel<128, false>);
   else
-    out_f32 ? go(preprocess_kernel<64, true>) : go(preprocess_kernel<64, false>);
+    a.out_f32 ? go(preprocess_kernel<64, true>) : go(preprocess_kernel<64, false>);
   return cudaGetLastError() == cudaSuccess ? FCP_OK : FCP_ERR_CUDA;
 }
 

@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
@@ -74,6 +75,16 @@ struct FwdLaunch {
   BiasParams bias;
 };
 
+// Sizes of a backward's operands, found by its preprocess: each row of dO is
+// divided by a power of two 2^e, and the kernel scales by these, so that the
+// fp16 operands keep their bits whatever the gradient's size. Zero between calls.
+struct BwdRange {
+  unsigned e_max;          // largest e of a row that sees a key, + kRowExpBias (0: no such row)
+  unsigned v2;             // bits of the largest |V_j|^2 (fp32)
+  int done;                // CTAs of the backward that have ended
+};
+constexpr int kRowExpBias = 256;
+
 struct BwdParams {
   const int32_t* pieces;
   const int32_t* tiles;    // backward units, kBwdTileInts ints each (plan.h, TB_BTILES)
@@ -83,11 +94,12 @@ struct BwdParams {
   int32_t T, hq, hkv;
   float scale;             // softmax scale
   float scale_log2;
-  const float* lse;        // [Hq][T]
-  const float* delta;      // [Hq][T] rowsum(dO * O)
+  const float* lse2;       // [Hq][T] -LSE log2 e + e, e the exponent taken out of the row's dO (BwdRange)
+  const float* delta;      // [Hq][T] rowsum(dO * O) 2^-e
   float* dq;               // [T][Hq][d] fp32, accumulated
   float* dk;               // [T][Hkv][d] fp32, accumulated
   float* dv;
+  BwdRange* range;
   int* err;
   int* work_counter;       // zero at launch (set by the preprocess)
   int32_t order_block;     // work decode: items per block (set by the launch, see work_slot)
@@ -112,20 +124,36 @@ int launch_attn_bwd(const BwdLaunch& a, cudaStream_t st);
 // Limit of every bounded device wait (fcp_debug_set_wait_limit), in ns.
 int64_t wait_limit_ns();
 
-// Row statistics D_i = <dO_i, O_i> for the rows of the given row chunks, dQ
-// rows set to zero, and fp16 copies of Q and dO for the backward's MMAs.
+// Row statistics D_i = <dO_i, O_i> and LSE for the rows of the given row chunks,
+// dQ rows set to zero, fp16 copies of Q and dO for the backward's MMAs (dO,
+// delta and lse2 with the rows' exponents taken out, see BwdRange), and the
+// range: V's from its rows [T][hkv][d] of the chunks and `v_rows` received rows
+// of vbuf.
 // *zero_word (if not null) is set to 0: the work counter of the kernel that
 // follows in the same stream.
 // n_rows_table: entries of `rows` (the checked build bounds the chunk indices).
 // pieces: the shard's n_pieces entries of the piece table, ascending, whose last
 // tiles' rows past the pieces are set to zero in the copies; none (0) for a
 // call over all shards, which writes every row.
-int launch_bwd_preprocess(const void* out, bool out_f32, const void* dout, const void* q,
-                          const int32_t* rows,
-                          const int32_t* order, int32_t n_chunks, int32_t n_rows_table, int32_t T, int32_t hq,
-                          int32_t d,
-                          float* delta, float* dq, void* q16, void* do16, const int32_t* pieces,
-                          int32_t n_pieces, int* err, int* zero_word, cudaStream_t st);
+struct PreLaunch {
+  const void* out;
+  bool out_f32;
+  const float* lse;        // [Hq][T]
+  const __nv_bfloat16 *dout, *q, *v, *vbuf;
+  int64_t v_rows;
+  const int32_t* rows;
+  const int32_t* order;
+  int32_t n_chunks, n_rows_table, T, hq, hkv;
+  float *delta, *lse2, *dq;
+  __half *q16, *do16;
+  BwdRange* range;
+  const int32_t* pieces;
+  int32_t n_pieces;
+  int num_sms;
+  int* err;
+  int* zero_word;
+};
+int launch_bwd_preprocess(const PreLaunch& a, int32_t d, cudaStream_t st);
 
 // fp16 copy of a bf16 array of n_elems (a multiple of 8) elements; *zero_word
 // (if not null) is set to 0, as above.

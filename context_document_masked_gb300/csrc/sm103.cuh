@@ -409,6 +409,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// The same, beyond the fp16 range its largest value.
+__device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 __device__ __forceinline__ float f16_lo(uint32_t x) {
   return __half2float(__ushort_as_half((unsigned short)(x & 0xFFFFu)));
 }
@@ -419,12 +426,12 @@ __device__ __forceinline__ float f16_hi(uint32_t x) {
 // Largest finite fp16 magnitude; bf16 inputs beyond it cannot be fp16 operands.
 constexpr float kF16Max = 65504.0f;
 
-// Convert a pair of bf16 (packed) to a pair of fp16 (packed), exactly for
-// values inside the fp16 normal range; sets *overflow if |x| > 65504.
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x, bool& overflow) {
+// A pair of bf16 (packed) times mul as a pair of fp16 (packed); sets *overflow
+// if |x| > 65504 before the product.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x, float mul, bool& overflow) {
   const float lo = __uint_as_float(x << 16), hi = __uint_as_float(x & 0xFFFF0000u);
   overflow |= fabsf(lo) > kF16Max || fabsf(hi) > kF16Max;
-  return pack_f16(lo, hi);
+  return pack_f16_sat(lo * mul, hi * mul);
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,

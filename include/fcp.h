@@ -218,7 +218,8 @@ typedef struct {
 /* Workspace the device calls on `plan` need, in bytes: an error word and the
  * attention kernels' work counter (set by each call before use), e4m3 copies
  * of Q, K and the received K rows with their scales (fcp_attn_fwd_qk8), the
- * backward's row statistics D_i = <dO_i, O_i> ([Hq][T] fp32), fp16 copies of
+ * backward's row statistics (D_i = <dO_i, O_i> and LSE_i with the rows' scales,
+ * [Hq][T] fp32 each) and its operands' largest exponents, fp16 copies of
  * Q and dO ([T][Hq][d] each, the backward's tensor-core operands) and of V and
  * the plan's received V rows (the forward's P*V operands), and the partial
  * sums of the norm weights' gradients (fcp_qk_norm_rope_bwd). The caller
@@ -379,6 +380,10 @@ int fcp_merge_ring(const fcp_dev_plan* plan, const float* o_parts, const float* 
  *   dq        fp32 [T][Hq][d]: written (=) at the shard's query rows.
  *   dk, dv    fp32 [T][Hkv][d]: ACCUMULATED (+=) at global key rows, remote
  *             keys included; zero them before the first shard.
+ * dO and V may be of any size up to 65504 (fp16's largest value, see
+ * fcp_get_device_status): the fp16 operands are scaled by powers of two taken
+ * from the call's rows. Rows of dO far smaller than its largest one (2^-10 and
+ * below) lose relative accuracy, not absolute.
  */
 int fcp_attn_bwd(const void* q, const void* k, const void* v, const void* kbuf,
                  const void* vbuf, const void* out, int32_t out_dtype, const float* lse,
