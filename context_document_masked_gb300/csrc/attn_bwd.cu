@@ -1013,10 +1013,12 @@ static __global__ void __launch_bounds__(kTableThreads) table_sums_kernel(const 
   const float* table = bp.by_distance + (size_t)blockIdx.x * bp.n_distances;
   const int lane = threadIdx.x & 31;
   for (int b = threadIdx.x >> 5; b < bp.n; b += kTableThreads / 32) {
+    // (Starts reach 2^31 - 1: cut to the table before anything is added to them.)
+    const int begin = min(bp.starts[b], bp.n_distances);
     const int end = b + 1 < bp.n ? min(bp.starts[b + 1], bp.n_distances) : bp.n_distances;
     float v = 0.f;
 #pragma unroll 4
-    for (int x = bp.starts[b] + lane; x < end; x += 32) v += __ldcg(table + x);
+    for (int x = begin + lane; x < end; x += 32) v += __ldcg(table + x);
     v = warp_sum(v);
     if (lane == 0) bp.dbias[(size_t)blockIdx.x * bp.n + b] += v;
   }
