@@ -1007,7 +1007,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-// dbias += the table's sums by distance: one block a head, a warp a bucket.
+// dbias += the table's sums by distance: one block a head, a warp a bucket. By
+// atomics, as the kernel before adds to it: another call (with a workspace of
+// its own, on another stream) may add to the same gradients.
 constexpr int kTableThreads = 512;
 static __global__ void __launch_bounds__(kTableThreads) table_sums_kernel(const __grid_constant__ BiasParams bp) {
   const float* table = bp.by_distance + (size_t)blockIdx.x * bp.n_distances;
@@ -1020,7 +1022,7 @@ static __global__ void __launch_bounds__(kTableThreads) table_sums_kernel(const 
 #pragma unroll 4
     for (int x = begin + lane; x < end; x += 32) v += __ldcg(table + x);
     v = warp_sum(v);
-    if (lane == 0) bp.dbias[(size_t)blockIdx.x * bp.n + b] += v;
+    if (lane == 0 && v != 0.f) red_add(bp.dbias + (size_t)blockIdx.x * bp.n + b, v);
   }
 }
 

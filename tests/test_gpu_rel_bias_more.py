@@ -26,3 +26,37 @@ def test_starts_at_the_end_of_the_type(cuda, starts):
         within(t, want, name)
     beyond = [u for u, first in enumerate(starts) if first >= 300]
     assert (got[5][:, beyond] == 0).all() and s.device_status() == 0
+
+
+def test_two_calls_add_to_one_gradient(cuda):
+    """Micro-batches in two sessions on two streams, all adding to one dk, dv and dbias:
+    what each adds alone, as often as it was called."""
+    from context_document_masked_gb300 import fcp
+    docs, hq, hkv, d, rounds = [700, 1, 323], 4, 2, 64, 16
+    starts, T = fcp.rel_buckets(32, 128), sum(docs)
+    runs = []
+    for n in range(2):
+        x = make(docs, hq, hkv, d, 32, seed=80 + n)
+        s, (q, k, v, do, b) = session(docs, 2, hq, hkv, d), [t.cuda() for t in x]
+        s.gather(k, v)
+        out, lse = s.forward_bias(q, k, v, b, starts, out_dtype=torch.float32)
+        alone = s.backward_bias(q, k, v, out, lse, do, b, starts)
+        runs.append((s, (q, k, v, out, lse, do, b, starts), alone, reference(*x, starts, docs), torch.cuda.Stream()))
+    sums = [torch.zeros(T, hkv, d, device="cuda"), torch.zeros(T, hkv, d, device="cuda"), torch.zeros(hq, 32, device="cuda")]
+    torch.cuda.synchronize()
+    for _ in range(rounds):
+        for s, x, alone, _w, st in runs:
+            with torch.cuda.stream(st):
+                s.backward_bias(*x, dq=alone[0], dk=sums[0], dv=sums[1], dbias=sums[2], zero_grads=False)
+    torch.cuda.synchronize()
+    for i, name in enumerate(("dk", "dv", "dbias")):
+        # The terms are the same, their order is not. A term goes through n additions at most, each off by 2^-24 of a
+        # partial sum: 64 along its diagonal, 64 tiles that share a distance, 40 distances and lanes of a bucket, and
+        # the two sessions' rounds. The terms' sizes are at most 2^11 / 3 of a call's bound, which has 3 2^-11 of them.
+        n = 64 + 64 + 40 + 2 * rounds
+        ref = rounds * sum(r[2][i + 1].double().cpu() for r in runs)
+        size = sum(torch.from_numpy(r[3][name][1]) for r in runs) * 2.0 ** 11 / 3
+        tol = rounds * n * 2.0 ** -24 * size
+        assert ((sums[i].double().cpu() - ref).abs() <= tol).all(), name
+        if name == "dbias":  # a call's share would be missed in most buckets
+            assert ((torch.minimum(*(r[2][3].double().cpu().abs() for r in runs)) > tol).double().mean() > 0.5)
