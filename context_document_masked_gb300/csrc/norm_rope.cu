@@ -318,7 +318,9 @@ __device__ __forceinline__ void heads_backward(const float* dy, const __nv_bfloa
 
 // Sum over the CTAs of `n` rows of 2 * D floats, rows stride apart, into out
 // (fixed order). All threads of the CTA; every row was written before the
-// ticket that let this CTA in was drawn.
+// ticket that let this CTA in was drawn. Added by one atomic an element: another
+// call (with a workspace of its own, on another stream) may add to the same
+// gradient.
 template <int D>
 __device__ __forceinline__ void sum_rows(const float* rows, int n, float* out_q, float* out_k, bool add) {
   for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
@@ -330,7 +332,8 @@ __device__ __forceinline__ void sum_rows(const float* rows, int n, float* out_q,
 #pragma unroll
       for (int r = 0; r < m; ++r) v[r] += v[r + m];
     float* o = i < D ? out_q + i : out_k + i - D;
-    if (o) *o = add ? *o + v[0] : v[0];
+    if (o && add) atomicAdd(o, v[0]);
+    if (o && !add) *o = v[0];
   }
 }
 

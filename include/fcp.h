@@ -503,7 +503,9 @@ int fcp_qk_norm_rope(const void* q_in, int64_t q_stride, const void* k_in, int64
  *             (same stride), dk_in k_in; no other overlap.
  *   dwq, dwk  fp32 [d] or NULL, written (add_dw = 0) or accumulated (add_dw =
  *             1, for one shard after another); not the same array. Summed in
- *             a fixed order: equal inputs give equal bits.
+ *             a fixed order: equal inputs give equal bits. Two calls may add to
+ *             one array at once (each with a workspace of its own; which comes
+ *             first can then change its last bits).
  *   ws        workspace of fcp_workspace_bytes(dims, plan) bytes.
  * Errors as fcp_qk_norm_rope; FCP_ERR_CAPACITY if the workspace is too small.
  */

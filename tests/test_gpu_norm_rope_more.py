@@ -1,0 +1,34 @@
+"""More of the head norm and rotation's gradient: calls that share what they add to."""
+import pytest
+import torch
+
+from test_gpu_norm_rope import make, session, slices
+
+pytestmark = pytest.mark.gpu
+
+
+def test_two_calls_add_to_one_gradient(cuda):
+    """Micro-batches in two sessions on two streams, adding to one dwq and dwk: what
+    each gives alone, as often as it was called."""
+    docs, hq, hkv, d, rounds = [300, 1, 83], 6, 2, 64, 64
+    runs = []
+    for n in range(2):
+        qkv, w, f, g = make(docs, hq, hkv, d, d, seed=90 + n)
+        s, x = session(docs, 2, hq, hkv, d), qkv.cuda()
+        args = (*(t.cuda() for t in g), *slices(x, hq, hkv)[:2])
+        kw = dict(wq=w[0].cuda(), wk=w[1].cuda(), inv_freq=f.cuda())
+        own = s.qk_norm_rope_backward(*args, **kw)
+        runs.append((s, args, dict(kw, dq_in=own[0], dk_in=own[1], dv_in=own[2]), own[3:], torch.cuda.Stream()))
+    sums = [torch.zeros(d, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(rounds):
+        for s, args, kw, _own, st in runs:
+            with torch.cuda.stream(st):
+                s.qk_norm_rope_backward(*args, **kw, dwq=sums[0], dwk=sums[1])
+    torch.cuda.synchronize()
+    for i, t in enumerate(sums):
+        a, b = (r[3][i].double() for r in runs)
+        # 2 rounds additions of equal terms in some order, each off by half a step of a sum no larger than all terms.
+        tol = 2 * rounds * 2.0 ** -24 * rounds * (a.abs() + b.abs())
+        assert ((t.double() - rounds * (a + b)).abs() <= tol).all()
+        assert (torch.minimum(a.abs(), b.abs()) > tol).double().mean() > 0.9  # one call's share would be missed
