@@ -68,12 +68,18 @@ class CPAttention:
     def gather(self, k, v, shard: int = -1, stream=None):
         fcp.gather_kv(k, v, self.dplan, shard, self.kbuf, self.vbuf, stream)
 
+    def _out_lse(self, out, lse, out_dtype, stream):
+        """The given tensors, or new ones made in the order of the call's stream."""
+        with _on_stream(stream):
+            if out is None:
+                out = torch.empty(self.T, self.hq, self.d, dtype=out_dtype, device=self.device)
+            if lse is None:
+                lse = torch.empty(self.hq, self.T, dtype=torch.float32, device=self.device)
+        return out, lse
+
     def forward(self, q, k, v, shard: int = -1, out=None, lse=None, kv_block=None,
                 out_dtype=torch.bfloat16, stream=None):
-        if out is None:
-            out = torch.empty(self.T, self.hq, self.d, dtype=out_dtype, device=self.device)
-        if lse is None:
-            lse = torch.empty(self.hq, self.T, dtype=torch.float32, device=self.device)
+        out, lse = self._out_lse(out, lse, out_dtype, stream)
         lo, hi = (0, self.T) if kv_block is None else kv_block
         fcp.attn_fwd(q, k, v, self.kbuf, self.vbuf, self.dplan, shard, out, lse, self.ws,
                      kv_lo=lo, kv_hi=hi, scale=self.scale, stream=stream)
@@ -82,10 +88,7 @@ class CPAttention:
     def forward_qk8(self, q, k, v, shard: int = -1, out=None, lse=None, kv_block=None,
                     out_dtype=torch.bfloat16, stream=None):
         """forward() with Q K^T on e4m3 copies of Q and K (d = 128)."""
-        if out is None:
-            out = torch.empty(self.T, self.hq, self.d, dtype=out_dtype, device=self.device)
-        if lse is None:
-            lse = torch.empty(self.hq, self.T, dtype=torch.float32, device=self.device)
+        out, lse = self._out_lse(out, lse, out_dtype, stream)
         lo, hi = (0, self.T) if kv_block is None else kv_block
         fcp.attn_fwd_qk8(q, k, v, self.kbuf, self.vbuf, self.dplan, shard, out, lse, self.ws,
                          kv_lo=lo, kv_hi=hi, scale=self.scale, stream=stream)
@@ -95,10 +98,7 @@ class CPAttention:
                      out_dtype=torch.bfloat16, stream=None):
         """Forward in ring order without the gathered buffer: ring_step -1 visits
         every owner's keys in one pass, s >= 0 gives ring step s's partial."""
-        if out is None:
-            out = torch.empty(self.T, self.hq, self.d, dtype=out_dtype, device=self.device)
-        if lse is None:
-            lse = torch.empty(self.hq, self.T, dtype=torch.float32, device=self.device)
+        out, lse = self._out_lse(out, lse, out_dtype, stream)
         fcp.attn_fwd_ring(q, k, v, self.dplan, shard, ring_step, out, lse, self.ws, scale=self.scale,
                           stream=stream)
         return out, lse
@@ -108,11 +108,7 @@ class CPAttention:
         """forward() with the learned bias[h, bucket(i - j)] (fp32 [hq][buckets])
         added to the scores; starts: the buckets' first distances (host), for
         instance fcp.rel_buckets(n, max_distance)."""
-        with _on_stream(stream):
-            if out is None:
-                out = torch.empty(self.T, self.hq, self.d, dtype=out_dtype, device=self.device)
-            if lse is None:
-                lse = torch.empty(self.hq, self.T, dtype=torch.float32, device=self.device)
+        out, lse = self._out_lse(out, lse, out_dtype, stream)
         lo, hi = (0, self.T) if kv_block is None else kv_block
         fcp.attn_fwd_bias(q, k, v, self.kbuf, self.vbuf, bias, starts, self.dplan, shard, out, lse, self.ws, kv_lo=lo,
                           kv_hi=hi, scale=self.scale, stream=stream)
@@ -136,16 +132,17 @@ class CPAttention:
 
     def backward(self, q, k, v, out, lse, dout, shard: int = -1, dq=None, dk=None, dv=None,
                  zero_kv_grads: bool = True, stream=None):
-        if dq is None:
-            dq = torch.empty(self.T, self.hq, self.d, dtype=torch.float32, device=self.device)
-        if dk is None:
-            dk = torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
-        elif zero_kv_grads:
-            dk.zero_()
-        if dv is None:
-            dv = torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
-        elif zero_kv_grads:
-            dv.zero_()
+        with _on_stream(stream):
+            if dq is None:
+                dq = torch.empty(self.T, self.hq, self.d, dtype=torch.float32, device=self.device)
+            if dk is None:
+                dk = torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
+            elif zero_kv_grads:
+                dk.zero_()
+            if dv is None:
+                dv = torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
+            elif zero_kv_grads:
+                dv.zero_()
         fcp.attn_bwd(q, k, v, self.kbuf, self.vbuf, out, lse, dout, self.dplan, shard, dq, dk, dv,
                      self.ws, scale=self.scale, stream=stream)
         return dq, dk, dv

@@ -1,0 +1,77 @@
+"""Session calls on a stream that is not the current one: what torch does for a
+call (new tensors, zero fills) runs in the order of that stream.
+
+The current stream is kept busy meanwhile, so that work left on it would come
+after the call's own. Bounds as derived in test_gpu_rel_bias."""
+import pytest
+import torch
+
+from test_gpu_rel_bias import make, reference, session, within
+
+pytestmark = pytest.mark.gpu
+
+DOCS, SHAPE = [700, 1, 323], (4, 2, 128)
+BUSY = 100_000_000  # cycles of the current stream
+
+
+@pytest.fixture(scope="module")
+def data():
+    x = make(DOCS, *SHAPE, 1, seed=21)
+    x[4].zero_()
+    want = reference(*x, [0], DOCS)
+    torch.cuda.synchronize()
+    return [t.cuda() for t in x[:4]], want
+
+
+@pytest.mark.parametrize("given", [False, True], ids=["new", "given"])
+def test_step(cuda, data, given):
+    (q, k, v, do), want = data
+    s = session(DOCS, 2, *SHAPE)
+    full = lambda t, *n: torch.full((*t.shape, *n), 5.0, device="cuda")  # noqa: E731
+    kw = dict(dq=full(q), dk=full(k), dv=full(v)) if given else {}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    s.gather(k, v, stream=side)
+    out, lse = s.forward(q, k, v, out_dtype=torch.float32, stream=side)
+    grads = s.backward(q, k, v, out, lse, do, stream=side, **kw)
+    with torch.cuda.stream(side):
+        got = [t.clone() for t in (out, lse, *grads)]
+    torch.cuda.synchronize()
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), got):
+        within(t, want, name)
+    for name, t in zip(("dq", "dk", "dv"), grads):  # nothing came after the call either
+        within(t, want, name)
+
+
+@pytest.mark.parametrize("how", ["forward", "forward_ring", "forward_qk8"])
+def test_outputs_are_made_in_the_streams_order(cuda, data, how):
+    """A block that the current stream's queued work has just given back is not the
+    other stream's output."""
+    (q, k, v, _), want = data
+    s = session(DOCS, 2, *SHAPE)
+    side = torch.cuda.Stream()
+    s.gather(k, v)
+    plain = getattr(s, how)(q, k, v, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    old = [torch.full_like(t, 7.0) for t in plain]  # written when the sleep ends
+    del old
+    got = getattr(s, how)(q, k, v, out_dtype=torch.float32, stream=side)
+    torch.cuda.synchronize()
+    for a, b in zip(plain, got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("which", ["default", "side"])
+def test_streams_as_raw_handles(cuda, data, which):
+    (q, k, v, do), want = data
+    s = session(DOCS, 2, *SHAPE)
+    st = torch.cuda.default_stream() if which == "default" else torch.cuda.Stream()
+    torch.cuda.synchronize()
+    s.gather(k, v, stream=st.cuda_stream)
+    out, lse = s.forward(q, k, v, out_dtype=torch.float32, stream=st.cuda_stream)
+    got = out, lse, *s.backward(q, k, v, out, lse, do, stream=st.cuda_stream)
+    st.synchronize()
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), got):
+        within(t, want, name)
