@@ -75,3 +75,31 @@ def test_streams_as_raw_handles(cuda, data, which):
     st.synchronize()
     for name, t in zip(("out", "lse", "dq", "dk", "dv"), got):
         within(t, want, name)
+
+
+def test_set_plan_makes_its_buffers_in_the_streams_order(cuda):
+    """A larger workspace starts from zeros on the stream of the plan's upload."""
+    docs = [1024]
+    x = make(docs, *SHAPE, 1, seed=22)
+    x[4].zero_()
+    want = reference(*x, [0], docs)
+    q, k, v, do = (t.cuda() for t in x[:4])
+    s = session([256] * 4, 4, *SHAPE, "wholedoc")
+    small = s.ws, s.kbuf
+    side = torch.cuda.Stream()
+    # Memory whose last writer waits behind the sleep.
+    old = [torch.empty(1 << 24, dtype=torch.int32, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    for t in old:
+        t.fill_(-1)
+    del old, t
+    s.set_plan(docs, stream=side)
+    assert s.ws is not small[0] and s.kbuf is not small[1]
+    s.gather(k, v, stream=side)
+    out, lse = s.forward(q, k, v, out_dtype=torch.float32, stream=side)
+    got = out, lse, *s.backward(q, k, v, out, lse, do, stream=side)
+    torch.cuda.synchronize()
+    assert s.device_status() == 0
+    for name, t in zip(("out", "lse", "dq", "dk", "dv"), got):
+        within(t, want, name)
