@@ -116,9 +116,17 @@ class CPAttention:
         return out, lse
 
     def backward_bias(self, q, k, v, out, lse, dout, bias, starts, shard: int = -1, dq=None, dk=None, dv=None,
-                      dbias=None, zero_grads: bool = True, stream=None):
-        """backward() of forward_bias(); also returns the bias's gradient
-        (zero_grads: dk, dv and dbias are set to zero first, else added to)."""
+                      dbias=None, zero_grads: bool | None = None, stream=None):
+        """backward() of forward_bias(); also returns the bias's gradient. zero_grads:
+        dk, dv and dbias are set to zero first (all of their rows), else added to.
+        It may be left out (then they are set to zero) but for one shard's call
+        with given dk, dv or dbias: in a loop over shards that would keep the last
+        one's share."""
+        if zero_grads is None:
+            if shard >= 0 and not (dk is None and dv is None and dbias is None):
+                raise ValueError("backward_bias: one shard's gradients into given tensors: zero_grads says whether they "
+                                 "are set to zero first (True) or added to (False)")
+            zero_grads = True
         with _on_stream(stream):
             if dq is None:
                 dq = torch.empty(self.T, self.hq, self.d, dtype=torch.float32, device=self.device)
@@ -167,18 +175,19 @@ class CPAttention:
 
     def qk_norm_rope_backward(self, dq, dk, dv, q_in, k_in, wq=None, wk=None, inv_freq=None, norm: bool = True,
                               eps: float = 1e-6, interleaved: bool = False, shard: int = -1, dq_in=None, dk_in=None,
-                              dv_in=None, dwq=None, dwk=None, stream=None):
+                              dv_in=None, dwq=None, dwk=None, zero_grads: bool = False, stream=None):
         """Gradient of qk_norm_rope from backward()'s dq, dk and dv (None: no V):
         the bf16 gradients of its inputs, written into dq_in, dk_in and dv_in
         (slices of one fused gradient, for instance) or new tensors, and the fp32
-        gradients of the weights, added to dwq and dwk where they are given."""
+        gradients of the weights, added to dwq and dwk where they are given
+        (zero_grads: written there)."""
         def rows(heads):
             return torch.empty(self.T, heads, self.d, dtype=torch.bfloat16, device=self.device)
         with _on_stream(stream):
             dq_in = rows(self.hq) if dq_in is None else dq_in
             dk_in = rows(self.hkv) if dk_in is None else dk_in
             dv_in = rows(self.hkv) if dv_in is None and dv is not None else dv_in
-            add = dwq is not None or dwk is not None  # to the given ones: new ones start at zero
+            add = not zero_grads and (dwq is not None or dwk is not None)  # to the given ones: new ones start at zero
             make = torch.zeros if add else torch.empty
             if dwq is None and wq is not None:
                 dwq = make(self.d, dtype=torch.float32, device=self.device)

@@ -32,3 +32,20 @@ def test_two_calls_add_to_one_gradient(cuda):
         tol = 2 * rounds * 2.0 ** -24 * rounds * (a.abs() + b.abs())
         assert ((t.double() - rounds * (a + b)).abs() <= tol).all()
         assert (torch.minimum(a.abs(), b.abs()) > tol).double().mean() > 0.9  # one call's share would be missed
+
+
+def test_given_weight_gradients_added_to_or_written(cuda):
+    docs, hq, hkv, d = [300, 1, 83], 6, 2, 64
+    qkv, w, f, g = make(docs, hq, hkv, d, d, seed=92)
+    s, x = session(docs, 2, hq, hkv, d), qkv.cuda()
+    args = (*(t.cuda() for t in g), *slices(x, hq, hkv)[:2])
+    kw = dict(wq=w[0].cuda(), wk=w[1].cuda(), inv_freq=f.cuda())
+    alone = s.qk_norm_rope_backward(*args, **kw)[3:]
+    dw = [torch.full((d,), float("nan"), device="cuda") for _ in range(2)]
+    got = s.qk_norm_rope_backward(*args, **kw, dwq=dw[0], dwk=dw[1], zero_grads=True)[3:]
+    assert got[0] is dw[0] and got[1] is dw[1] and torch.equal(dw[0], alone[0]) and torch.equal(dw[1], alone[1])
+    s.qk_norm_rope_backward(*args, **kw, dwq=dw[0], dwk=dw[1])
+    assert torch.equal(dw[0], 2 * alone[0]) and torch.equal(dw[1], 2 * alone[1])
+    one = torch.full((d,), float("nan"), device="cuda")
+    got = s.qk_norm_rope_backward(*args, **kw, dwk=one, zero_grads=True)[3:]
+    assert got[1] is one and torch.equal(got[0], alone[0]) and torch.equal(one, alone[1])

@@ -60,3 +60,31 @@ def test_two_calls_add_to_one_gradient(cuda):
         assert ((sums[i].double().cpu() - ref).abs() <= tol).all(), name
         if name == "dbias":  # a call's share would be missed in most buckets
             assert ((torch.minimum(*(r[2][3].double().cpu().abs() for r in runs)) > tol).double().mean() > 0.5)
+
+
+def test_one_shard_into_given_gradients_says_how(cuda):
+    """A loop over shards must not keep the last one's share by a default."""
+    docs, hq, hkv, d, starts = [300, 84], 4, 2, 64, [0, 1, 50]
+    x = make(docs, hq, hkv, d, 3, seed=12)
+    want = reference(*x, starts, docs)
+    q, k, v, do, b = (t.cuda() for t in x)
+    s = session(docs, 2, hq, hkv, d)
+    s.gather(k, v)
+    out, lse = s.forward_bias(q, k, v, b, starts, out_dtype=torch.float32)
+    T, nan = sum(docs), float("nan")
+    g = dict(dq=torch.empty(T, hq, d, device="cuda"), dk=torch.full((T, hkv, d), nan, device="cuda"),
+             dv=torch.full((T, hkv, d), nan, device="cuda"), dbias=torch.full((hq, 3), nan, device="cuda"))
+    for name in ("dk", "dv", "dbias"):
+        with pytest.raises(ValueError, match="zero_grads"):
+            s.backward_bias(q, k, v, out, lse, do, b, starts, shard=0, **{name: g[name]})
+        assert g[name].isnan().all()
+    for j in range(2):
+        s.gather(k, v, shard=j)
+        s.backward_bias(q, k, v, out, lse, do, b, starts, shard=j, zero_grads=j == 0, **g)
+    for name, t in g.items():
+        within(t, want, name)
+    s.gather(k, v, shard=1)
+    new = s.backward_bias(q, k, v, out, lse, do, b, starts, shard=1)[1:]  # new ones start from zero
+    s.backward_bias(q, k, v, out, lse, do, b, starts, shard=1, zero_grads=True, **g)
+    for a, t in zip(new, (g["dk"], g["dv"], g["dbias"])):
+        assert torch.allclose(a, t, rtol=0, atol=1e-5)
