@@ -2,7 +2,8 @@
 
 Every computation runs in the C++ planner or the CUDA kernels of libfcp.so;
 PyTorch supplies device memory and streams. Importing this module loads the
-library and raises if it has not been built: there is no fallback path.
+library and raises if it has not been built: there is no fallback path. Planning
+needs numpy alone: torch is imported by the first call that takes tensors.
 """
 from __future__ import annotations
 
@@ -11,7 +12,6 @@ import ctypes as C
 import os
 
 import numpy as np
-import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # FCP_DEVICE_CHECKS=1 selects the checked build (device-side bounds checks on
@@ -35,8 +35,16 @@ EXPORTED = (
 )
 MAX_BUCKETS = 128
 
+torch = None
+_BF16, _F32, _BF16_F32, _U8, _I32 = range(5)  # places in _DTYPES
+_DTYPES = ()
 
-_BF16, _F32, _BF16_F32 = (torch.bfloat16,), (torch.float32,), (torch.bfloat16, torch.float32)
+
+def _import_torch():
+    global torch, _DTYPES
+    import torch as t
+    _DTYPES = ((t.bfloat16,), (t.float32,), (t.bfloat16, t.float32), (t.uint8,), (t.int32,))
+    torch = t
 
 
 class FcpError(RuntimeError):
@@ -239,6 +247,8 @@ class Plan:
         """Copy the work tables into `buf` (an int32 device tensor of >= device_bytes()
         bytes) on `stream`, staged through pinned host memory so that the host does
         not wait for the stream's earlier work."""
+        if torch is None:
+            _import_torch()
         n = self.device_bytes() // 4
         dp = self.bind(buf)
         host = torch.empty(n, dtype=torch.int32, pin_memory=True)
@@ -290,14 +300,16 @@ def _t(t, name, dtypes=None, shape=None):
     """Checks a tensor before its raw pointer goes to the library, which cannot
     see dtypes, strides or devices: a contiguous CUDA tensor of one of
     `dtypes`, of `shape` (None entries free). Raises ValueError."""
+    if torch is None:
+        _import_torch()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {tuple(str(x) for x in dtypes)}")
+    if dtypes is not None and t.dtype not in _DTYPES[dtypes]:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected one of {tuple(str(x) for x in _DTYPES[dtypes])}")
     if shape is not None:
         got = t.shape
         ok = len(got) == len(shape)
@@ -382,9 +394,9 @@ def attn_fwd_qk8(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, lse, w
 def quant_e4m3(x, out, scale_out, scratch, stream=None):
     """fcp_quant_e4m3: out (uint8, x.numel() bytes) = e4m3(x * 2^k); scale_out[0] = 2^k."""
     _t(x, "x", _BF16)
-    _t(out, "out", (torch.uint8,))
+    _t(out, "out", _U8)
     _t(scale_out, "scale_out", _F32)
-    _t(scratch, "scratch", (torch.int32,))
+    _t(scratch, "scratch", _I32)
     if out.numel() < x.numel() or scale_out.numel() < 1 or scratch.numel() < 1:
         raise ValueError("quant_e4m3: out holds x.numel() bytes, scale_out and scratch one element each")
     _check(_lib.fcp_quant_e4m3(_ptr(x), x.numel(), _ptr(out), _ptr(scale_out), _ptr(scratch), _stream(stream)),
