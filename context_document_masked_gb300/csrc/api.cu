@@ -631,6 +631,7 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
   for (const void* ptr : {q, k, v, out, (const void*)lse, dout, (const void*)dq, (const void*)dk,
                           (const void*)dv, (const void*)ws})
     if (!aligned16(ptr)) return FCP_ERR_INVALID_ARG;
+  if (rrows > 0 && (!aligned16(kbuf) || !aligned16(vbuf))) return FCP_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* wsb = static_cast<char*>(ws);
   float* delta = reinterpret_cast<float*>(wsb + wl.delta);
