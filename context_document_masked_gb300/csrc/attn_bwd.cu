@@ -93,9 +93,9 @@ struct Scaling {
   float dqk;       // that times the softmax scale
   __device__ __forceinline__ void init(const BwdRange* r, float scale) {
     const int e_max = (int)__ldcg(&r->e_max);
-    const int field = (int)(__ldcg(&r->v2) >> 23);  // exponent of |V|^2: 255 for inf and NaN
+    const int field = (int)(__ldcg(&r->v2) >> 23);  // exponent of |V|^2
     const int E = e_max ? e_max - kRowExpBias : 0;
-    const int ve = field == 255 ? 20 : ((field - 127) >> 1) + 1;
+    const int ve = ((field - 127) >> 1) + 1;
     lse_add = (float)(kProbExp - E);
     v = scalbnf(1.f, -ve);
     dv = scalbnf(1.f, E - kProbExp);

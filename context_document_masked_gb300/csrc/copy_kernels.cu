@@ -224,6 +224,8 @@ __device__ __forceinline__ uint32_t cvt_pair(uint32_t x, bool& ovf) {
 
 // Largest |V_j|^2 of n 16-byte groups (L of them a row and head), as this
 // thread's share; first and step are the same for a warp's lanes but for the lane.
+// Rows that are not finite do not count, as those of dO do not: they spoil their
+// own document, not the scaling of the others.
 template <int L>
 __device__ __forceinline__ void v_norms(const uint4* v, int64_t n, int64_t first, int64_t step, int lane, float& most) {
   for (int64_t g = first; g - lane < n; g += step) {
@@ -237,7 +239,7 @@ __device__ __forceinline__ void v_norms(const uint4* v, int64_t n, int64_t first
     }
 #pragma unroll
     for (int m = L / 2; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    most = s > most || s != s ? s : most;
+    most = s > most && s < INFINITY ? s : most;
   }
 }
 
@@ -323,7 +325,8 @@ __global__ void __launch_bounds__(kPreThreads) preprocess_kernel(const PreLaunch
       }
       // |dO_i| 2^40 is in [2^h, 2^(h + 1)), h = floor(log2(s2) / 2) from s2's
       // exponent field (0 for a row of zeros: the smallest e, -104).
-      const int h = (((__float_as_int(s2) >> 23) & 255) - 127) >> 1;
+      const int field = (__float_as_int(s2) >> 23) & 255;  // 255: not finite
+      const int h = (field - 127) >> 1;
       const int e = h - kSquareExp;
       const float f = __int_as_float((127 - h) << 23);  // 2^(-e - 40), in [2^-64, 2^64]
 #pragma unroll
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kPreThreads) preprocess_kernel(const PreLaunch
         p.delta[stat] = s * f;
         const bool sees = lse != -INFINITY;  // -inf: every key masked by its bias
         p.lse2[stat] = sees ? fmaf(-lse, kLog2e, (float)e) : -INFINITY;
-        if (sees) e_max = max(e_max, (unsigned)(e + kRowExpBias));
+        if (sees && field < 255) e_max = max(e_max, (unsigned)(e + kRowExpBias));
       }
     }
     v_norms<L>(reinterpret_cast<const uint4*>(p.v + (int64_t)r0 * p.hkv * D), (int64_t)nr * p.hkv * L, first, stride, lane,
@@ -369,10 +372,10 @@ __global__ void __launch_bounds__(kPreThreads) preprocess_kernel(const PreLaunch
   }
   if (ovf) atomicOr(p.err, 4);
   // The block's maxima into the range (fp32 bits of numbers >= 0 order as the
-  // numbers, a NaN above them).
+  // numbers).
   __shared__ unsigned most[2][kPreThreads / 32];
   e_max = __reduce_max_sync(0xffffffffu, e_max);
-  const unsigned v_max = __reduce_max_sync(0xffffffffu, __float_as_uint(v2) & 0x7FFFFFFFu);
+  const unsigned v_max = __reduce_max_sync(0xffffffffu, __float_as_uint(v2));
   if (lane == 0) most[0][threadIdx.x >> 5] = e_max, most[1][threadIdx.x >> 5] = v_max;
   __syncthreads();
   if (threadIdx.x < 2) {

@@ -103,3 +103,32 @@ def test_nothing_comes_back(cuda, biased):
     for name, t in zip(NAMES, big):
         within(t, scaled(want, 12, 0), name)
     assert s.device_status() == 0
+
+
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "biased"])
+@pytest.mark.parametrize("where", ["do nan", "do inf", "v nan", "v inf"])
+def test_one_document_that_is_not_finite(cuda, where, biased):
+    """It does not cost the others their bits. Documents of whole tiles on one shard:
+    what shares a tile with it has to be finite (P = 0 times NaN is NaN)."""
+    docs, d = [256, 128, 384, 256], 64
+    q, k, v, do, b = x = make(docs, 4, 2, d, len(STARTS), seed=80)
+    if not biased:
+        b.zero_()
+    want = reference(*x, STARTS, docs)
+    name, value = where.split()
+    v, do = v.clone(), do.clone()
+    {"do": do, "v": v}[name][300, 1, 5] = float(value)
+    s = session(docs, 1, 4, 2, d)
+    got = run(s, (q, k, v, do, b), STARTS, biased)
+    s.device_status()  # an infinity is reported, as beyond the fp16 range
+    rest = torch.ones(sum(docs), dtype=torch.bool)
+    rest[256:384] = False
+    for name, t in zip(NAMES[:5], got):
+        if name == "lse":
+            continue
+        ref, err = want[name]
+        within(t[rest.cuda()], {name: (ref[rest.numpy()], err[rest.numpy()])}, name)
+    clean = run(s, x, STARTS, biased)  # nothing is left for the next call
+    for name, t in zip(NAMES, clean):
+        within(t, want, name)
+    assert s.device_status() == 0
