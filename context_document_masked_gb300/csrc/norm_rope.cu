@@ -112,7 +112,7 @@ __device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
   return (uint64_t)((t - floor(t)) * 18446744073709551616.0);
 }
 
-// Cosines and sines of this lane's pairs at position `pos`; f0 and f1 are the
+// Cosines and sines of this lane's pairs at position `pos` (1 and 0 where it turns none); f0 and f1 are the
 // frequencies of pairs 2 * lane and 2 * lane + 1.
 template <bool INTER>
 __device__ __forceinline__ void row_angles(uint32_t pos, uint64_t f0, uint64_t f1, const Lane& ln, int rot_dim,
@@ -135,16 +135,20 @@ __device__ __forceinline__ void row_angles(uint32_t pos, uint64_t f0, uint64_t f
 }
 
 // The kE values of chunk a (the first kE / 4 pairs of registers) and chunk b
-// turned in place: forwards for kSign = 1, backwards for -1.
+// turned in place: forwards for kSign = 1, backwards for -1. Where a lane turns
+// none, its products with the sine take 0 for the value (an infinity times 0
+// would not pass).
+__device__ __forceinline__ uint64_t value_if(bool turns, uint64_t x) { return turns ? x : 0; }
 template <bool INTER, int kSign>
-__device__ __forceinline__ void turn(uint64_t (&x)[kE / 2], const float (&c)[kE / 2], const float (&s)[kE / 2]) {
+__device__ __forceinline__ void turn(uint64_t (&x)[kE / 2], const float (&c)[kE / 2], const float (&s)[kE / 2], bool turns) {
   if constexpr (INTER) {  // pairs (2i, 2i + 1)
 #pragma unroll
     for (int e = 0; e < kE / 2; ++e) {
-      float a, b;
+      float a, b, sa, sb;
       f2_split(x[e], a, b);
+      f2_split(value_if(turns, x[e]), sa, sb);
       const float sn = kSign * s[e];
-      x[e] = f2(a * c[e] - b * sn, a * sn + b * c[e]);
+      x[e] = f2(a * c[e] - sb * sn, sa * sn + b * c[e]);
     }
   } else {  // value i of chunk a with value i of chunk b
 #pragma unroll
@@ -152,8 +156,8 @@ __device__ __forceinline__ void turn(uint64_t (&x)[kE / 2], const float (&c)[kE 
       const uint64_t c2 = f2(c[2 * i], c[2 * i + 1]), s2 = f2(s[2 * i], s[2 * i + 1]);
       const uint64_t n2 = f2(-s[2 * i], -s[2 * i + 1]);
       const uint64_t a = x[i], b = x[kE / 4 + i];
-      x[i] = f2_fma(b, kSign > 0 ? n2 : s2, f2_mul(a, c2));
-      x[kE / 4 + i] = f2_fma(a, kSign > 0 ? s2 : n2, f2_mul(b, c2));
+      x[i] = f2_fma(value_if(turns, b), kSign > 0 ? n2 : s2, f2_mul(a, c2));
+      x[kE / 4 + i] = f2_fma(value_if(turns, a), kSign > 0 ? s2 : n2, f2_mul(b, c2));
     }
   }
 }
@@ -228,7 +232,7 @@ __device__ __forceinline__ void heads_forward(const __nv_bfloat16* in, __nv_bflo
 #pragma unroll
         for (int i = 0; i < kE / 2; ++i) x[i] = f2_mul(f2_mul(x[i], r2), wl[i]);
       }
-      turn<INTER, 1>(x, c, s);
+      turn<INTER, 1>(x, c, s, ln.turns);
       if (h < n_heads) store_bf16(out + (size_t)h * D, ln, x);
     }
   }
@@ -288,7 +292,7 @@ __device__ __forceinline__ void heads_backward(const float* dy, const __nv_bfloa
       if (u > 0 && h0 + u * kHeads >= n_heads) break;
       const int h = h0 + u * kHeads + ln.head;
       uint64_t(&z)[kE / 2] = zz[u];
-      turn<INTER, -1>(z, c, s);
+      turn<INTER, -1>(z, c, s, ln.turns);
       if (p.norm) {
         uint64_t x[kE / 2], wl[kE / 2];
 #pragma unroll

@@ -49,3 +49,31 @@ def test_given_weight_gradients_added_to_or_written(cuda):
     one = torch.full((d,), float("nan"), device="cuda")
     got = s.qk_norm_rope_backward(*args, **kw, dwk=one, zero_grads=True)[3:]
     assert got[1] is one and torch.equal(got[0], alone[0]) and torch.equal(one, alone[1])
+
+
+@pytest.mark.parametrize("inter", [False, True], ids=["halves", "pairs"])
+@pytest.mark.parametrize("rot", [0, 32])
+def test_infinities_in_dimensions_that_pass(cuda, rot, inter):
+    """Rotation alone: a dimension that does not turn passes whatever it holds, and no
+    other one sees it; the same for the gradient."""
+    docs, hq, hkv, d = [40, 1, 23], 3, 1, 64
+    qkv, _, f, _ = make(docs, hq, hkv, d, rot, seed=93)
+    s, x = session(docs, 2, hq, hkv, d), qkv.cuda()
+    kw = dict(inv_freq=f.cuda() if rot else None, norm=False, interleaved=inter)
+    plain = s.qk_norm_rope(*slices(x, hq, hkv), **kw)
+    bad = x.clone()
+    at = [rot, rot + 5, 63]
+    bad[3, 1, at[0]], bad[20, 3, at[1]], bad[50, 2, at[2]] = float("inf"), float("nan"), float("-inf")
+    got = s.qk_norm_rope(*slices(bad, hq, hkv), **kw)
+    for a, b, xin, xbad in zip(plain, got, slices(x, hq, hkv), slices(bad, hq, hkv)):
+        hit = ~torch.isfinite(xbad)
+        assert torch.equal(a[~hit], b[~hit])
+        assert torch.allclose(b[hit], xbad[hit], rtol=0, atol=0, equal_nan=True)  # infinities with their sign, NaN as NaN
+    g = [t.float() for t in plain[:2]]
+    gbad = [t.clone() for t in g]
+    gbad[0][3, 1, at[0]], gbad[1][50, 0, at[2]] = float("inf"), float("nan")
+    a = s.qk_norm_rope_backward(*g, None, None, None, **kw)[:2]
+    b = s.qk_norm_rope_backward(*gbad, None, None, None, **kw)[:2]
+    for m, n, t in zip(a, b, gbad):
+        hit = ~torch.isfinite(t)
+        assert hit.sum() == 1 and torch.equal(m[~hit], n[~hit]) and not torch.isfinite(n[hit]).any()
