@@ -113,12 +113,6 @@ __device__ __forceinline__ const float4* window_row(const float* win, int lane) 
   return reinterpret_cast<const float4*>(win + k * kWindowCopy + first - k);
 }
 
-// (An atomicAdd through a pointer of unknown space brings code for shared
-// memory with it.)
-__device__ __forceinline__ void red_add(float* at, float v) {
-  asm volatile("red.global.add.f32 [%0], %1;" ::"l"(__cvta_generic_to_global(at)), "f"(v) : "memory");
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);

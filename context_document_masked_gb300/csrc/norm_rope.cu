@@ -336,7 +336,7 @@ __device__ __forceinline__ void sum_rows(const float* rows, int n, float* out_q,
 #pragma unroll
       for (int r = 0; r < m; ++r) v[r] += v[r + m];
     float* o = i < D ? out_q + i : out_k + i - D;
-    if (o && add) atomicAdd(o, v[0]);
+    if (o && add) red_add(o, v[0]);
     if (o && !add) *o = v[0];
   }
 }

@@ -409,7 +409,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// The same, beyond the fp16 range its largest value.
+// (An atomicAdd through a pointer of unknown space brings code for shared
+// memory with it.)
+__device__ __forceinline__ void red_add(float* at, float v) {
+  asm volatile("red.global.add.f32 [%0], %1;" ::"l"(__cvta_generic_to_global(at)), "f"(v) : "memory");
+}
+
+// pack_f16, beyond the fp16 range its largest value.
 __device__ __forceinline__ uint32_t pack_f16_sat(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
