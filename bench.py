@@ -57,12 +57,12 @@ BWD_TRAFFIC_SOURCES = [
     ("context_document_masked_gb300/csrc/copy_kernels.cu", None, None),
     ("context_document_masked_gb300/csrc/sm103.cuh", None, None),
     ("context_document_masked_gb300/csrc/kernels.h", "struct BwdParams", "int launch_attn_fwd"),
-    ("context_document_masked_gb300/csrc/api.cu", "int fcp_attn_bwd(", "int fcp_get_device_status("),
+    ("context_document_masked_gb300/csrc/api.cu", "static int attn_bwd_impl(", "int fcp_attn_bwd_bias("),
     ("context_document_masked_gb300/csrc/tables.cpp", None, None),
 ]
 BWD_TRAFFIC = {   # workload -> {"sha256": ..., "bytes": ...}
-    5: {"sha256": "9399f6ec8d945887f97c1f4f488c8c79ea07c45ae7fd77a7f5c949c4a0edfcc2",
-        "bytes": (17.46 + 17.42 + 239.54 + 143.77) * 1e9},   # preprocess + main kernel
+    5: {"sha256": "f4c159bc24554e6894682bd290b4aea0b0684f347e884b120b6693072a3e692a",
+        "bytes": (19.18 + 17.71 + 239.99 + 144.00) * 1e9},   # preprocess + main kernel
 }
 
 

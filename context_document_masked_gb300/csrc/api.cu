@@ -378,10 +378,11 @@ static void set_bias(fcp::BiasParams* p, const fcp_rel_bias* b, float* dbias, fl
 // V once, but where a long document's first key tiles are a large share of the
 // work the other CTAs wait for them. Estimated as the longer of the longest unit
 // and the mean a CTA, a unit's beginning and end counted as three steps. 7001
-// tokens in documents of up to 4096, groups of three heads: 215 us in one unit,
-// 178 in two, 123 in three; one document of 16K, groups of eight: 2.95 ms, four
-// heads a unit 2.84, two 2.89; the 32K workload, which has units enough: 4.80 ms,
-// two heads a unit 5.10.
+// tokens in documents of up to 4096, groups of three heads: 224 us in one unit,
+// 198 in two, 136 in three. With eight units a CTA and more there is nothing to
+// even out: one document of 16K, groups of eight, 10.5 a CTA, 2.91 ms whole,
+// four heads a unit 2.94, two 3.05, one 3.36; the 32K workload, groups of four,
+// 4.83 whole, two heads a unit 5.13, one 5.78.
 static void cut_groups(fcp::BiasParams* b, const Plan* p, int32_t shard, int32_t n_items, const fcp_dims& dims, int sms) {
   const int G = dims.hq / dims.hkv;
   b->parts = 1;

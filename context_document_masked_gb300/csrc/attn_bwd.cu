@@ -58,12 +58,12 @@
 // of one bucket (TileSums). The compute warps are the critical path, so they
 // have only the window's adds and, in tiles of several buckets, the sums along
 // the diagonals (add_block). One document of 16K (16 query and 2 KV heads of
-// 128, 64 buckets): 2.92 ms against 2.58 without; the 32K workload 4.81
-// against 4.60; 4096 tokens of 12 heads of 64, most of whose tiles hold several
-// buckets: 93 us against 72. The steps' code of all roles together does not
-// fit the instruction cache, so what a step executes counts by its length (the
-// bias took 4.9 ms on the 32K workload with masks and MMAs written out, and
-// another 0.4 to 0.8 with a loop or a call in BiasSteps::load). Slower: the sums
+// 128, 64 buckets): 2.90 ms against 2.57 without; the 32K workload 4.84
+// against 4.62; 4096 tokens of 12 heads of 64, most of whose tiles hold several
+// buckets: 94 us against 74. The steps' code of all roles together does not
+// fit the instruction cache, so what a step executes counts by its length (on
+// the 32K workload masks and MMAs written out took 0.2 ms more each, a loop or a call
+// in BiasSteps::load another 0.4 to 0.8). Slower: the sums
 // in the compute warps, by matrix instructions (no faster, for their set-up),
 // in a table for each CTA.
 #include <cuda.h>
@@ -346,9 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = BwdCfg<D>;
   constexpr bool kBias = std::is_same_v<Bias, BiasParams>;
   // The bias's code does not leave the room in the instruction cache that all
-  // MMAs of a step written out would take (d = 128, the 32K workload: 4.94 ms
-  // for 4.75, two at a time 4.84; d = 64, 4096 tokens of 12 heads: 106 us for
-  // 102). Without a bias they measured as fast or faster written out.
+  // MMAs of a step written out would take (0.19 ms more at d = 128 on the 32K
+  // workload, two at a time 0.09; 4 us at d = 64 on 4096 tokens of 12 heads).
+  // Without a bias they measured as fast or faster written out.
   constexpr int kMmaUnroll = kBias ? D / 32 : 8;
   // For the same reason masks have a place of their own there, off the way of
   // tiles that need none (one document of 16K 3.44 -> 3.13 ms), and for d = 64

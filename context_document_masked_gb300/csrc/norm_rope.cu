@@ -29,9 +29,9 @@
 // Bound: device memory, one read of each input and one write of each output,
 // and its latency: four passes are loaded before the first is worked on, and
 // the arithmetic runs on pairs of values (f32x2) to keep the registers that
-// this takes. 65536 tokens of 64 + 8 + 8 heads of 128: 419 us, 6.40 TB/s (0.96
+// this takes. 65536 tokens of 64 + 8 + 8 heads of 128: 420 us, 6.39 TB/s (0.96
 // of the copy rate measured on this part); gradient of 32768 tokens of 32 + 8
-// + 8: 261 us, 5.91 TB/s (0.88). Slower: sixteen values a lane (gradient 287
+// + 8: 266 us, 5.80 TB/s (0.87). Slower: sixteen values a lane (gradient 287
 // us, two passes do not fit), asynchronous copies into shared memory (485 and
 // 370 us, for their instructions), units looked up ahead by the CTA (the same).
 #include <cuda_bf16.h>
@@ -176,7 +176,9 @@ __device__ __forceinline__ float load_w(const void* w, int w_f32, int i) {
 }
 
 // A unit of work: `chunk` rows of one query tile. Tiles are at most 128 rows
-// of one piece; n_rows is 0 past the tile's end.
+// of one piece; n_rows is 0 past the tile's end. (Checked build: a tile out of
+// range is skipped. The forward has no error word; the attention calls read the
+// same tables and report it.)
 struct Rows {
   int first, n, pos;  // first row, rows, position of the first row in its document
 };
@@ -450,7 +452,10 @@ int launch_norm_rope(const NormRopeLaunch& a, cudaStream_t st) {
   }
   // Rows a CTA takes at a time: 8, one a warp, as a small sequence has to
   // spread over all SMs; whole tiles where tiles are short (documents of a
-  // few tokens), whose units would otherwise mostly be empty.
+  // few tokens), whose units would otherwise mostly be empty (32768 tokens of 32 +
+  // 8 + 8 heads of 128, forward and gradient: documents of one token 505 us and
+  // 1.14 ms, in units of 8 rows 7.49 and 17.2; of 12 157 and 284 us for 736 and
+  // 1776; of 63, below the border of 64, 145 and 269 for 189 and 386).
   const bool short_tiles = (int64_t)a.rows < (int64_t)a.n_tiles * 64 && a.n_tiles >= 2 * a.num_sms;
   p.chunk = short_tiles ? 128 : kWarps;
   p.chunks = 128 / p.chunk;

@@ -221,8 +221,9 @@ typedef struct {
  * backward's row statistics (D_i = <dO_i, O_i> and LSE_i with the rows' scales,
  * [Hq][T] fp32 each) and its operands' largest exponents, fp16 copies of
  * Q and dO ([T][Hq][d] each, the backward's tensor-core operands) and of V and
- * the plan's received V rows (the forward's P*V operands), and the partial
- * sums of the norm weights' gradients (fcp_qk_norm_rope_bwd). The caller
+ * the plan's received V rows (the forward's P*V operands), the partial sums
+ * of the norm weights' gradients (fcp_qk_norm_rope_bwd), and the biased
+ * backward's sums of dS by distance ([Hq][8192] fp32). The caller
  * zero-fills a new workspace once before its first call: the error word and
  * the counters beside it in the first 256 bytes must start at zero
  * (fcp_get_device_status clears the word after reporting an error). Behind
@@ -482,7 +483,10 @@ typedef struct {
  *             q_in itself where that is contiguous (and k, v likewise); no
  *             other overlap of an output with an input or an output.
  * Errors, before any launch: FCP_ERR_INVALID_ARG (also an overlap),
- * FCP_ERR_UNSUPPORTED (d, heads, rot_dim not a multiple of 16).
+ * FCP_ERR_UNSUPPORTED (d, heads, rot_dim not a multiple of 16). The call has no
+ * workspace: where the checked build skips a plan-table entry out of range, its
+ * rows stay as they were without a report (the attention calls, which read the
+ * same tables, report it).
  */
 int fcp_qk_norm_rope(const void* q_in, int64_t q_stride, const void* k_in, int64_t k_stride, const void* v_in,
                      int64_t v_stride, const void* wq, const void* wk, const float* inv_freq,
