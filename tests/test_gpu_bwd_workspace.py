@@ -79,3 +79,36 @@ def test_shapes_in_turn(cuda):
         for name, t in shard_by_shard(s, xc, starts, True, lambda: None).items():
             within(t, want, name)
         assert s.device_status() == 0
+
+
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "biased"])
+def test_after_a_wait_that_gave_up(cuda, biased):
+    """A backward whose waits give up at once reports it and leaves the header as the
+    next call expects it."""
+    from context_document_masked_gb300 import fcp
+    docs, starts = [300, 1, 83], [0, 1, 3, 50]
+    x = make(docs, 4, 2, 64, 4, seed=45)
+    if not biased:
+        x[4].zero_()
+    want = reference(*x, starts, docs)
+    s = session(docs, 2, 4, 2, 64)
+    q, k, v, do, b = (t.cuda() for t in x)
+    s.gather(k, v)
+    if biased:
+        out, lse = s.forward_bias(q, k, v, b, starts, out_dtype=torch.float32)
+        back = lambda d: s.backward_bias(q, k, v, out, lse, d, b, starts)  # noqa: E731
+    else:
+        out, lse = s.forward(q, k, v, out_dtype=torch.float32)
+        back = lambda d: s.backward(q, k, v, out, lse, d)  # noqa: E731
+    torch.cuda.synchronize()
+    fcp.debug_set_wait_limit(-1)
+    try:
+        back(do * 1024)
+        torch.cuda.synchronize()
+        assert s.device_status() == fcp.ERR_TIMEOUT
+    finally:
+        fcp.debug_set_wait_limit(0)
+    assert (s.ws[36:39] == 0).all()  # bytes 144 to 155: the range of the operands
+    for name, t in zip(("dq", "dk", "dv", "dbias"), back(do)):
+        within(t, want, name)
+    assert s.device_status() == 0
