@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "kernels.h"
@@ -49,28 +50,28 @@ int num_sms() {
   return n;
 }
 
-// Token-major [rows][heads][d] 16-bit tensor, boxes of 64 x 1 x 128 with the
-// 128-byte swizzle (one swizzle panel of a 128-row tile).
-bool make_map(CUtensorMap* m, const void* ptr, int d, int heads, int64_t rows, bool f16 = false) {
+// Token-major [rows][heads][d] 16-bit tensor, boxes of 64 x 1 x box_rows with the
+// 128-byte swizzle (one swizzle panel of a 128-row tile, or of a part of one).
+bool make_map(CUtensorMap* m, const void* ptr, int d, int heads, int64_t rows, bool f16 = false, int box_rows = 128) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
-  cuuint32_t box[3] = {64, 1, 128};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// fp32 [rows][heads][d] tensor, boxes of 32 x 1 x 128 with the 128-byte
-// swizzle: the target of the backward's dQ reduce-adds.
-bool make_map_f32(CUtensorMap* m, void* ptr, int d, int heads, int64_t rows) {
+// fp32 [rows][heads][d] tensor, boxes of 32 x 1 x box_rows with the 128-byte
+// swizzle: the target of the backward's reduce-adds.
+bool make_map_f32(CUtensorMap* m, void* ptr, int d, int heads, int64_t rows, int box_rows = 128) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)d * 4, (cuuint64_t)heads * d * 4};
-  cuuint32_t box[3] = {32, 1, 128};
+  cuuint32_t box[3] = {32, 1, (cuuint32_t)box_rows};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr, dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -160,6 +161,17 @@ int fcp_plan(const int32_t* doclens, int32_t n_docs, int32_t cp, int32_t policy,
   if (!out) return FCP_ERR_INVALID_ARG;
   *out = nullptr;
   return fcp::make_plan(doclens, n_docs, cp, policy, target_imbalance, out);
+}
+
+int fcp_plan_window(const fcp_plan_t* plan, int32_t window, int32_t sinks, fcp_plan_t** out) {
+  if (!out) return FCP_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!plan) return FCP_ERR_INVALID_ARG;
+  try {
+    return fcp::make_window_plan(*plan, window, sinks, out);
+  } catch (const std::bad_alloc&) {  // no host memory for the tables
+    return FCP_ERR_CAPACITY;
+  }
 }
 
 void fcp_plan_free(fcp_plan_t* plan) { delete plan; }
@@ -411,6 +423,30 @@ static void cut_groups(fcp::BiasParams* b, const Plan* p, int32_t shard, int32_t
   }
 }
 
+// The window of a plan and the maps of tiles that hold sinks: k, v and the
+// received kb, vb as the launch's own maps name them (v's as fp16 copies in the
+// forward), dk and dv for a backward.
+static bool set_window(fcp::WindowParams* w, const Plan* p, const fcp_dims& dims, const void* k, const void* v,
+                       const void* kb, const void* vb, int64_t kb_rows, bool v_f16, float* dk, float* dv) {
+  w->window = p->window;
+  w->sinks = p->sinks;
+  w->slots = fcp::sink_slots(p->sinks);
+  if (w->slots == 0) return true;
+  const int rest = fcp::kTileN - w->slots;
+  auto both = [&](CUtensorMap* sinks, CUtensorMap* others, const void* at, int64_t rows, bool f16) {
+    return make_map(sinks, at, dims.d, dims.hkv, rows, f16, w->slots) &&
+           make_map(others, at, dims.d, dims.hkv, rows, f16, rest);
+  };
+  bool ok = both(&w->k_sinks, &w->k_rest, k, dims.T, false) && both(&w->v_sinks, &w->v_rest, v, dims.T, v_f16) &&
+            both(&w->kb_sinks, &w->kb_rest, kb, kb_rows, false) && both(&w->vb_sinks, &w->vb_rest, vb, kb_rows, v_f16);
+  if (dk)
+    ok = ok && make_map_f32(&w->dk_sinks, dk, dims.d, dims.hkv, dims.T, w->slots) &&
+         make_map_f32(&w->dk_rest, dk, dims.d, dims.hkv, dims.T, rest) &&
+         make_map_f32(&w->dv_sinks, dv, dims.d, dims.hkv, dims.T, w->slots) &&
+         make_map_f32(&w->dv_rest, dv, dims.d, dims.hkv, dims.T, rest);
+  return ok;
+}
+
 // Forward over the plan's gathered key layout (ring < -1: own rows from K/V,
 // received rows from kbuf/vbuf) or in ring order (ring >= -1: every needed key
 // from its owner's rows of K/V, owners visited by ring distance; ring = -1 all
@@ -425,6 +461,7 @@ static int attn_fwd_impl(const void* q, const void* k, const void* v, const void
   if (st) return st;
   const Plan* p = plan->host;
   if ((st = check_dims(dims, p))) return st;
+  if (p->window > 0 && (ring_order || qk8 || bias)) return FCP_ERR_UNSUPPORTED;
   if (!q || !k || !v || !out || !lse || !ws) return FCP_ERR_INVALID_ARG;
   if (out_dtype != FCP_OUT_BF16 && out_dtype != FCP_OUT_F32) return FCP_ERR_INVALID_ARG;
   if (kv_lo < 0 || kv_hi > dims.T || kv_lo > kv_hi) return FCP_ERR_INVALID_ARG;
@@ -516,6 +553,10 @@ static int attn_fwd_impl(const void* q, const void* k, const void* v, const void
   a.d = dims.d;
   a.num_sms = num_sms();
   if ((a.has_bias = bias != nullptr)) set_bias(&a.bias, bias, nullptr, nullptr);
+  if ((a.has_window = p->window > 0) &&
+      !set_window(&a.window, p, dims, k, v16, rrows > 0 ? kbuf : k, rrows > 0 ? vb16 : v16, rrows > 0 ? rrows : dims.T, true,
+                  nullptr, nullptr))
+    return FCP_ERR_CUDA;
   return fcp::launch_attn_fwd(a, cs);
 }
 
@@ -623,6 +664,7 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
   if (st) return st;
   const Plan* p = plan->host;
   if ((st = check_dims(dims, p))) return st;
+  if (p->window > 0 && bias) return FCP_ERR_UNSUPPORTED;
   if (!q || !k || !v || !out || !lse || !dout || !dq || !dk || !dv || !ws) return FCP_ERR_INVALID_ARG;
   if (out_dtype != FCP_OUT_BF16 && out_dtype != FCP_OUT_F32) return FCP_ERR_INVALID_ARG;
   const WsLayout wl = ws_layout(dims, p->total_remote);
@@ -683,6 +725,7 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
   pre.range = range;
   pre.pieces = table(plan, fcp::TB_PIECES) + 8 * (int64_t)piece0;
   pre.n_pieces = n_pieces;
+  pre.any_tiles = p->window > 0;
   pre.num_sms = num_sms();
   pre.err = static_cast<int*>(ws);
   pre.zero_word = reinterpret_cast<int*>(wsb + kWorkCounterOff);
@@ -738,6 +781,10 @@ static int attn_bwd_impl(const void* q, const void* k, const void* v, const void
     set_bias(&a.bias, bias, dbias, reinterpret_cast<float*>(wsb + wl.by_distance));
     cut_groups(&a.bias, p, shard, bp.n_items, dims, a.num_sms);
   }
+  if ((a.has_window = p->window > 0) &&
+      !set_window(&a.window, p, dims, k, v, rrows > 0 ? kbuf : k, rrows > 0 ? vbuf : v, rrows > 0 ? rrows : dims.T, false, dk,
+                  dv))
+    return FCP_ERR_CUDA;
   return fcp::launch_attn_bwd(a, s);
 }
 

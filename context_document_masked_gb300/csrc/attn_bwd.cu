@@ -69,6 +69,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <type_traits>
 
 #include "bias.cuh"
@@ -129,6 +130,9 @@ struct BwdItem {
   int key0, n, src, src_row, qa0, qa_end, na, qb0, qb_end, nb, nq, g;
   bool bad;  // checked build: the unit's table entries are out of range (skip it)
   int h0, heads;  // the unit's query heads
+  // Under a window (qa0: the document's start where the unit has sinks, else -1;
+  // qa_end: their row in the received ones, -1 for own): rows the sinks take.
+  int slots;
 };
 
 // Query tiles q0, q0 + 128, ... (n of them) lie inside [0, q_end] and q_end <= T.
@@ -140,7 +144,13 @@ __device__ __forceinline__ bool qrange_ok(int q0, int q_end, int n, int T) {
 // as many as the launch says (the form without one adds up dK and dV over the
 // heads of a group in TMEM, in one order).
 __host__ __device__ __forceinline__ int group_parts(const NoBias&) { return 1; }
+__host__ __device__ __forceinline__ int group_parts(const WindowParams&) { return 1; }
 __host__ __device__ __forceinline__ int group_parts(const BiasParams& bp) { return bp.parts; }
+template <class Bias>
+__device__ __forceinline__ int window_of(const Bias& bp) {
+  if constexpr (std::is_same_v<Bias, WindowParams>) return bp.window;
+  else return INT_MAX;
+}
 
 template <class Bias>
 __device__ __forceinline__ BwdItem decode(const BwdParams& p, const Bias& bias, int G, int w) {
@@ -150,7 +160,7 @@ __device__ __forceinline__ BwdItem decode(const BwdParams& p, const Bias& bias, 
   it.bad = false;
   if constexpr (kDeviceChecks) {
     if (item < 0 || item >= p.n_tiles) {
-      it = BwdItem{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, true};
+      it = BwdItem{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, true, 0, 0, 0};
       return it;
     }
   }
@@ -175,11 +185,21 @@ __device__ __forceinline__ BwdItem decode(const BwdParams& p, const Bias& bias, 
     it.h0 = it.g * G + first;
     it.heads = min(bias.part_heads, G - first);
   }
+  it.slots = 0;
+  if constexpr (std::is_same_v<Bias, WindowParams>) {
+    if (it.qa0 >= 0) {
+      it.slots = bias.slots;
+      if (it.qa_end >= 0) it.qa_end -= p.kbuf_shift;
+    }
+  }
   if constexpr (kDeviceChecks) {
     const int rows = it.src ? p.kb_rows : p.T;
     it.bad = it.n < 1 || it.n > 128 || it.key0 < 0 || it.key0 > p.T - it.n || (it.src != 0 && it.src != 1) ||
              it.src_row < 0 || it.src_row > rows - it.n || !qrange_ok(it.qa0, it.qa_end, it.na, p.T) ||
              !qrange_ok(it.qb0, it.qb_end, it.nb, p.T);
+    if constexpr (std::is_same_v<Bias, WindowParams>)
+      it.bad = it.bad || it.na != 0 || it.n > 128 - it.slots ||
+               (it.slots && (it.qa0 >= p.T || it.qa_end >= p.kb_rows || it.qa_end < -1));
   }
   return it;
 }
@@ -345,6 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ Bias bp) {
   using C = BwdCfg<D>;
   constexpr bool kBias = std::is_same_v<Bias, BiasParams>;
+  constexpr bool kWindow = std::is_same_v<Bias, WindowParams>;
   // The bias's code does not leave the room in the instruction cache that all
   // MMAs of a step written out would take (0.19 ms more at d = 128 on the 32K
   // workload, two at a time 0.09; 4 us at d = 64 on 4096 tokens of 12 heads).
@@ -354,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tiles that need none (one document of 16K 3.44 -> 3.13 ms), and for d = 64
   // (4096 tokens of 12 heads, without a bias 84 -> 77 us); at d = 128 without a
   // bias they are as well beside the values (512K workload 1.475 s, apart 1.485).
-  constexpr bool kMaskApart = kBias || D == 64;
+  constexpr bool kMaskApart = kBias || kWindow || D == 64;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ __align__(8) uint64_t bar_kv_full, bar_kv_conv, bar_kv_empty, bar_drain;
   __shared__ __align__(8) uint64_t bar_q_full[2], bar_q_empty[2], bar_do_full, bar_do_empty;
@@ -459,9 +480,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx(&bar_kv_full, 2 * C::kTile);
         const CUtensorMap* tk = it.src ? &tm_kb : &tm_k;
         const CUtensorMap* tv = it.src ? &tm_vb : &tm_v;
+        if constexpr (kWindow) {
+          if (it.slots) {  // the sinks' rows first
+            const bool rcv = it.qa_end >= 0;
+            const int row = rcv ? it.qa_end : it.qa0;
+            for (int pn = 0; pn < C::kPanels; ++pn) {
+              tma_load_3d(smem + C::kK + pn * 16384, rcv ? &bp.kb_sinks : &bp.k_sinks, &bar_kv_full, pn * 64, it.g, row);
+              tma_load_3d(smem + C::kV + pn * 16384, rcv ? &bp.vb_sinks : &bp.v_sinks, &bar_kv_full, pn * 64, it.g, row);
+            }
+            tk = it.src ? &bp.kb_rest : &bp.k_rest;
+            tv = it.src ? &bp.vb_rest : &bp.v_rest;
+          }
+        }
         for (int pn = 0; pn < C::kPanels; ++pn) {
-          tma_load_3d(smem + C::kK + pn * 16384, tk, &bar_kv_full, pn * 64, it.g, it.src_row);
-          tma_load_3d(smem + C::kV + pn * 16384, tv, &bar_kv_full, pn * 64, it.g, it.src_row);
+          tma_load_3d(smem + C::kK + pn * 16384 + it.slots * 128, tk, &bar_kv_full, pn * 64, it.g, it.src_row);
+          tma_load_3d(smem + C::kV + pn * 16384 + it.slots * 128, tv, &bar_kv_full, pn * 64, it.g, it.src_row);
         }
       }
       ++kv_items;
@@ -741,16 +774,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const BwdItem it = decode(p, bp, G, w);
       if (it.bad) continue;
       const int nsteps = it.heads * it.nq;
-      const bool key_valid = kr < it.n;
+      bool key_valid = kr < it.n;
       const int key = it.key0 + kr;
+      // Under a window: the queries [q_first, q_end) that see this row's key. A
+      // sink's are those of the unit's own rows whose window it is before.
+      int q_first = key, q_end = 0;
+      if constexpr (kWindow) {
+        const bool sink = kr < it.slots;
+        q_first = sink ? max(it.key0, it.qa0 + kr + window_of(bp)) : key - it.slots;
+        q_end = sink ? it.key0 + it.n : q_first + window_of(bp);
+        key_valid = sink ? kr < bp.sinks : kr - it.slots < it.n;
+        if (!key_valid) q_end = q_first;
+      }
       Steps steps(it);
       for (int j = 0; j < nsteps; ++j, ++gstep, steps.next(it)) {
         const uint32_t c = qc + j, s = c & 1;
         const int q0 = steps.rows(it).q0;
-        const int lim = key - q0 - 64 * half;  // local columns below lim cannot see this key
+        const int lim = q_first - q0 - 64 * half;  // local columns below lim cannot see this key
         // Whole tile below the diagonal with 128 keys: no element needs a mask
         // (query rows past the piece end have LSE = +inf, hence P = 0).
-        const bool unmasked = it.n == 128 && it.key0 + 127 <= q0;
+        const bool unmasked = it.n == 128 && it.key0 + 127 <= q0 && (!kWindow || q0 + 127 - it.key0 < window_of(bp));
         ok = mbar_wait(&bar_s_full, gstep & 1, wc) &&
              (kBias || mbar_wait(&bar_q_full[s], (c >> 1) & 1, wc));
         if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -799,10 +842,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[(e >> 1) + 1] = pack_f16(p2, p3);
           }
           if (kMaskApart && !unmasked) {
-            const int first = key_valid ? lim : 64;
+            if constexpr (kWindow) {
+              const int end = q_end - q0 - 64 * half;
+              uint64_t seen = end <= 0 ? 0 : ~0ull >> (64 - min(end, 64));
+              seen = lim >= 64 ? 0 : seen & (~0ull << max(lim, 0));
 #pragma unroll
-            for (int e = 0; e < 64; e += 2)
-              pk[e >> 1] &= (e >= first ? 0xFFFFu : 0u) | (e + 1 >= first ? 0xFFFF0000u : 0u);
+              for (int e = 0; e < 64; e += 2)
+                pk[e >> 1] &= (seen >> e & 1 ? 0xFFFFu : 0u) | (seen >> (e + 1) & 1 ? 0xFFFF0000u : 0u);
+            } else {
+              const int first = key_valid ? lim : 64;
+#pragma unroll
+              for (int e = 0; e < 64; e += 2)
+                pk[e >> 1] &= (e >= first ? 0xFFFFu : 0u) | (e + 1 >= first ? 0xFFFF0000u : 0u);
+            }
           }
         }
         {
@@ -901,7 +953,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kr == 0) {
           ok = mbar_wait(&bar_stg_full[half], stg & 1, wc);
           if (ok) {
-            tma_reduce_add_3d(tm_out, smem + C::kDS + half * 16384, cc * 32, it.g, it.key0);
+            uint8_t* tile = smem + C::kDS + half * 16384;
+            if constexpr (kWindow) {
+              if (it.slots) {  // the sinks' rows, then the others
+                tma_reduce_add_3d(half == 0 ? &bp.dv_sinks : &bp.dk_sinks, tile, cc * 32, it.g, it.qa0);
+                tma_reduce_add_3d(half == 0 ? &bp.dv_rest : &bp.dk_rest, tile + it.slots * 128, cc * 32, it.g, it.key0);
+              } else {
+                tma_reduce_add_3d(tm_out, tile, cc * 32, it.g, it.key0);
+              }
+            } else {
+              tma_reduce_add_3d(tm_out, tile, cc * 32, it.g, it.key0);
+            }
             bulk_commit();
             bulk_wait_read_all();
           }
@@ -1062,6 +1124,11 @@ static int launch_bwd_impl(const BwdLaunch& a, const Bias& bias, cudaStream_t st
 }
 
 int launch_attn_bwd(const BwdLaunch& a, cudaStream_t st) {
+  if (a.has_window) {
+    if (a.has_bias) return FCP_ERR_UNSUPPORTED;
+    if (a.d == 128) return launch_bwd_impl<128>(a, a.window, st);
+    return a.d == 64 ? launch_bwd_impl<64>(a, a.window, st) : FCP_ERR_UNSUPPORTED;
+  }
   if (a.d == 128) return a.has_bias ? launch_bwd_impl<128>(a, a.bias, st) : launch_bwd_impl<128>(a, NoBias{}, st);
   if (a.d == 64) return a.has_bias ? launch_bwd_impl<64>(a, a.bias, st) : launch_bwd_impl<64>(a, NoBias{}, st);
   return FCP_ERR_UNSUPPORTED;

@@ -49,6 +49,12 @@
 // one document of 16K, where more tiles hold several buckets: 1.01 against
 // 0.78. Folding columns of one bucket inside such a tile: 1.69 ms for 1.57, for
 // the spills that it brings at 168 registers a thread.
+//
+// Under a window (a separate instantiation, for windowed plans), query i sees the
+// keys i - window < j <= i and, of those before, its document's first `sinks`.
+// A query tile walks the keys from its first row's window on; the sinks have the
+// first rows of its first key tile (TMA boxes of their own), and the plan makes
+// the query tiles as long as the key tiles then hold (WindowWalker).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -126,6 +132,54 @@ struct Walker {
   }
 };
 
+// Key tiles of one query tile under a window: its segments' keys from the first
+// row's window on, [q_start - window + 1, q_last], and where a row sees sinks
+// outside its window (`slots` > 0) the first tile begins with their rows, so that
+// they cost no tile of their own. `off` of a tile: its first row that holds a
+// window key (its sinks' rows before it).
+struct WindowWalker {
+  const int32_t* seg;
+  int s, s_end, q_last, lo, hi, shift, slots;
+  int pos, end, ks, src, srow;
+
+  __device__ void init(const int32_t* segs, int seg_begin, int seg_count, int q_last_, int lo_, int hi_, int shift_,
+                       int slots_) {
+    seg = segs;
+    s = seg_begin - 1;
+    s_end = seg_begin + seg_count;
+    q_last = q_last_;
+    lo = lo_;
+    hi = hi_;
+    shift = shift_;
+    slots = slots_;
+    pos = end = 0;
+  }
+  __device__ bool next(int& src_o, int& row_o, int& key_o, int& n_o, int& off_o) {
+    off_o = slots;
+    slots = 0;
+    while (pos >= end) {
+      if (++s >= s_end) {
+        // No key in the key block: a tile of sinks alone (what lies behind them is masked).
+        src_o = n_o = 0;
+        row_o = key_o = q_last;
+        return off_o > 0;
+      }
+      const int* g = seg + 4 * s;
+      ks = __ldg(g + 2);
+      src = __ldg(g + 0);
+      srow = __ldg(g + 1) - (src ? shift : 0);
+      pos = max(ks, lo);
+      end = min(min(ks + __ldg(g + 3), hi), q_last + 1);
+    }
+    src_o = src;
+    row_o = srow + (pos - ks);
+    key_o = pos;
+    n_o = min(128 - off_o, end - pos);
+    pos += n_o;
+    return true;
+  }
+};
+
 // A key segment's keys and source rows lie inside the sequence and inside
 // the tensor its source names (own K/V rows, or the received rows behind
 // tm_kb, `shift` rows into them). Checked build only.
@@ -155,18 +209,49 @@ __device__ __forceinline__ int count_key_tiles(const FwdParams& p, const int32_t
   return n;
 }
 
+// The tiles that WindowWalker gives; -1 as above.
+__device__ __forceinline__ int count_window_tiles(const FwdParams& p, const int32_t* segs, int seg_begin, int seg_count,
+                                                  int q_last, int lo, int hi, int slots) {
+  int n = 0;
+  for (int s = seg_begin; s < seg_begin + seg_count; ++s) {
+    const int* g = segs + 4 * s;
+    if constexpr (kDeviceChecks) {
+      if (!segment_ok(p, g)) return -1;
+    }
+    const int ks = __ldg(g + 2);
+    const int len = min(min(ks + __ldg(g + 3), hi), q_last + 1) - max(ks, lo);
+    if (len <= 0) continue;
+    // The first tile's sinks take `slots` of its rows.
+    n += len <= 128 - slots ? 1 : (len + slots + 127) / 128;
+    slots = 0;
+  }
+  return n + (slots > 0);
+}
+
 struct WorkItem {
   int q_start, q_rows, seg_begin, seg_count, h0, h1, g;
   bool bad;  // checked build: the unit's table entries are out of range (skip it)
+  // Under a window: where the piece's document starts, and its sinks' row in the
+  // received ones (-1: at doc in K and V); first key of the tile's windows.
+  int doc, sink_row, lo, slots;
 };
+
+// Bits [a, b) of 128 set (none for a >= b; the ends may lie outside).
+__device__ __forceinline__ void set_bits(uint32_t (&m)[4], int a, int b) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int lo = min(max(a - 32 * w, 0), 32), hi = min(max(b - 32 * w, 0), 32);
+    if (hi > lo) m[w] |= (0xffffffffu >> (32 - (hi - lo))) << lo;
+  }
+}
 
 // Head pairs per query tile: each GQA group's heads two at a time; an odd
 // group's last pair holds one head (its second slot repeats the first and
 // stores nothing).
 __host__ __device__ __forceinline__ int head_pairs(int hq, int hkv) { return hkv * ((hq / hkv + 1) / 2); }
 
-template <bool ODD>
-__device__ __forceinline__ WorkItem decode(const FwdParams& p, int w) {
+template <bool ODD, class Bias>
+__device__ __forceinline__ WorkItem decode(const FwdParams& p, const Bias& bias, int w) {
   const int hp_count = ODD ? head_pairs(p.hq, p.hkv) : p.hq / 2;
   const WorkSlot ws = work_slot(w, p.n_items, hp_count, p.order_block);
   const int item = __ldg(p.order + ws.pos);
@@ -175,7 +260,7 @@ __device__ __forceinline__ WorkItem decode(const FwdParams& p, int w) {
   it.bad = false;
   if constexpr (kDeviceChecks) {
     if (item < 0 || item >= p.n_tiles) {
-      it = WorkItem{0, 0, 0, 0, 0, 0, 0, true};
+      it = WorkItem{0, 0, 0, 0, 0, 0, 0, true, 0, 0, 0, 0};
       return it;
     }
   }
@@ -183,7 +268,7 @@ __device__ __forceinline__ WorkItem decode(const FwdParams& p, int w) {
   const int piece = __ldg(t + 0);
   if constexpr (kDeviceChecks) {
     if (piece < 0 || piece >= p.n_pieces) {
-      it = WorkItem{0, 0, 0, 0, 0, 0, 0, true};
+      it = WorkItem{0, 0, 0, 0, 0, 0, 0, true, 0, 0, 0, 0};
       return it;
     }
   }
@@ -205,7 +290,30 @@ __device__ __forceinline__ WorkItem decode(const FwdParams& p, int w) {
     it.h1 = it.h0 + 1;
     it.g = it.h0 / (p.hq / p.hkv);
   }
+  if constexpr (std::is_same_v<Bias, WindowParams>) {
+    const int q_last = it.q_start + it.q_rows - 1;
+    it.doc = __ldg(p.pieces + 8 * piece + 4);
+    it.lo = max(p.kv_lo, it.q_start - bias.window + 1);
+    it.slots = q_last - bias.window >= it.doc ? bias.slots : 0;
+    it.sink_row = __ldg(p.pieces + 8 * piece + 7);
+    if constexpr (kDeviceChecks) {
+      it.bad = it.bad || it.doc < 0 || it.doc > it.q_start;
+      if (it.slots && it.sink_row >= 0) it.bad = it.bad || it.sink_row - p.kbuf_shift < 0 || it.sink_row - p.kbuf_shift >= p.kb_rows;
+    }
+    if (it.sink_row >= 0) it.sink_row -= p.kbuf_shift;
+  }
   return it;
+}
+
+// Key tiles of a unit, -1 for one that is skipped (checked build).
+template <class Bias>
+__device__ __forceinline__ int unit_tiles(const FwdParams& p, const WorkItem& it) {
+  const int q_last = it.q_start + it.q_rows - 1;
+  if (it.bad) return -1;
+  if constexpr (std::is_same_v<Bias, WindowParams>)
+    return count_window_tiles(p, p.segs, it.seg_begin, it.seg_count, q_last, it.lo, p.kv_hi, it.slots);
+  else
+    return count_key_tiles(p, p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.seg_filter);
 }
 
 template <int D, bool QK8, bool ODD, class Bias>
@@ -214,6 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_kb,
                     const __grid_constant__ CUtensorMap tm_vb, const FwdParams p, const __grid_constant__ Bias bp) {
   constexpr bool kBias = std::is_same_v<Bias, BiasParams>;
+  constexpr bool kWindow = std::is_same_v<Bias, WindowParams>;
+  using Walk = std::conditional_t<kWindow, WindowWalker, Walker>;
   using C = FwdCfg<D, kBias>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -280,9 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t k = 0;
       for (int w = blockIdx.x; ok; w = next_work(p.work_counter)) {
         if (!(ok = ring.put<true>(k++, w, wc)) || w >= n_work) break;
-        const WorkItem it = decode<ODD>(p, w);
+        const WorkItem it = decode<ODD>(p, bp, w);
         const int q_last = it.q_start + it.q_rows - 1;
-        const int nt = it.bad ? -1 : count_key_tiles(p, p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.seg_filter);
+        const int nt = unit_tiles<Bias>(p, it);
         if (nt < 0) atomicOr(p.err, kErrBadTable);
         if (nt <= 0) continue;
         if (q_iter > 0 && !(ok = mbar_wait_inline(&bar_q_empty, (q_iter - 1) & 1, wc))) break;
@@ -298,10 +408,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                           it.q_start);
         }
         ++q_iter;
-        Walker wk;
-        wk.init(p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.kbuf_shift, p.seg_filter);
-        int src, row, key, n;
-        while (ok && wk.next(src, row, key, n)) {
+        Walk wk;
+        int src, row, key, n, off = 0;
+        if constexpr (kWindow)
+          wk.init(p.segs, it.seg_begin, it.seg_count, q_last, it.lo, p.kv_hi, p.kbuf_shift, it.slots);
+        else
+          wk.init(p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.kbuf_shift, p.seg_filter);
+        auto next = [&] {
+          if constexpr (kWindow) return wk.next(src, row, key, n, off);
+          else return wk.next(src, row, key, n);
+        };
+        while (ok && next()) {
           for (int kv = 0; kv < 2; ++kv) {
             const int s = kv_cnt % C::kStages;
             if (kv_cnt >= (uint32_t)C::kStages &&
@@ -313,9 +430,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(sKV + s * C::kTileBytes, tm, &bar_kv_full[s], 0, it.g, row);
             } else {
               mbar_arrive_expect_tx(&bar_kv_full[s], C::kTileBytes);
+              uint8_t* dst = sKV + s * C::kTileBytes;
+              if constexpr (kWindow) {
+                if (off > 0) {  // the sinks' rows, then the window's
+                  const bool rcv = it.sink_row >= 0;
+                  const CUtensorMap* ts = kv == 0 ? (rcv ? &bp.kb_sinks : &bp.k_sinks) : (rcv ? &bp.vb_sinks : &bp.v_sinks);
+                  for (int pn = 0; pn < C::kPanels; ++pn)
+                    tma_load_3d(dst + pn * 16384, ts, &bar_kv_full[s], pn * 64, it.g, rcv ? it.sink_row : it.doc);
+                  tm = kv == 0 ? (src ? &bp.kb_rest : &bp.k_rest) : (src ? &bp.vb_rest : &bp.v_rest);
+                  dst += off * 128;
+                }
+              }
               for (int pn = 0; pn < C::kPanels; ++pn)
-                tma_load_3d(sKV + s * C::kTileBytes + pn * 16384, tm, &bar_kv_full[s], pn * 64, it.g,
-                            row);
+                tma_load_3d(dst + pn * 16384, tm, &bar_kv_full[s], pn * 64, it.g, row);
             }
             ++issued[s];
             ++kv_cnt;
@@ -366,9 +493,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = ring.get<true>(k, w, wc))) break;
         ring.release(k);
         if (w >= n_work) break;
-        const WorkItem it = decode<ODD>(p, w);
+        const WorkItem it = decode<ODD>(p, bp, w);
         const int q_last = it.q_start + it.q_rows - 1;
-        const int nt = it.bad ? -1 : count_key_tiles(p, p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.seg_filter);
+        const int nt = unit_tiles<Bias>(p, it);
         if (nt <= 0) continue;
         if (!(ok = mbar_wait_inline(&bar_q_full, q_iter & 1, wc))) break;
         tc_fence_after();
@@ -440,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) ring.release(k);
       if (w >= n_work) break;
-      const WorkItem it = decode<ODD>(p, w);
+      const WorkItem it = decode<ODD>(p, bp, w);
       const int q_last = it.q_start + it.q_rows - 1;
-      const int nt = it.bad ? -1 : count_key_tiles(p, p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.seg_filter);
+      const int nt = unit_tiles<Bias>(p, it);
       if (nt < 0) continue;  // checked build: a unit with out-of-range table entries stores nothing
       const int q = it.q_start + r;
       bool row_valid = r < it.q_rows;
@@ -454,11 +581,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       float run_bias = 0.f;
       if constexpr (kBias) bias_row = bp.bias + (size_t)(i ? it.h1 : it.h0) * bp.n;
       if (nt > 0) {
-        Walker wk;
-        wk.init(p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.kbuf_shift, p.seg_filter);
-        int src, row, key, n;
+        Walk wk;
+        int src, row, key, n, off = 0;
+        if constexpr (kWindow)
+          wk.init(p.segs, it.seg_begin, it.seg_count, q_last, it.lo, p.kv_hi, p.kbuf_shift, it.slots);
+        else
+          wk.init(p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.kbuf_shift, p.seg_filter);
         for (int t = 0; t < nt; ++t) {
-          wk.next(src, row, key, n);
+          if constexpr (kWindow) wk.next(src, row, key, n, off);
+          else wk.next(src, row, key, n);
           // Bias of the tile: one bucket for all the warp's distances, or the
           // window of them. Set up before S is waited for, so its latency is
           // hidden.
@@ -501,7 +632,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               add = run_bias;
             }
           }
-          if (key + 127 > it.q_start || n < 128) {
+          if constexpr (kWindow) {
+            // Columns [off + first, off + last) hold keys of the row's window,
+            // [s_first, s_last) sinks before it.
+            if (n < 128 || key + 127 > it.q_start || key < q_last - bp.window + 1) {
+              const int first = max(q - bp.window + 1 - key, 0), last = min(n, q - key + 1);
+              uint32_t seen[4] = {0, 0, 0, 0};
+              set_bits(seen, off + first, off + last);
+              if (off > 0)
+                set_bits(seen, max(p.kv_lo - it.doc, 0), min(min(bp.sinks, p.kv_hi - it.doc), q - bp.window + 1 - it.doc));
+#pragma unroll
+              for (int c = 0; c < 128; ++c)
+                if (!(seen[c >> 5] & (1u << (c & 31)))) s[c] = -INFINITY;
+            }
+          } else if (key + 127 > it.q_start || n < 128) {
             const int lim = min(n, q - key + 1);  // keys [key, key+lim) are visible to row q
 #pragma unroll
             for (int c = 0; c < 128; ++c)
@@ -521,7 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                      scale_log2;
           if constexpr (kBias) mx += add;
           const float m_new = fmaxf(m_run, mx);
+          // A row of a window may see no key of its first tiles: nothing to scale yet.
           const bool rescale = m_new > m_run + kRescaleThreshold;
+          const bool scale_o = kWindow ? rescale && m_run != -INFINITY : rescale;
           float alpha = 1.f;
           if (rescale) {
             alpha = ex2(m_run - m_new);
@@ -552,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 4; ++j) f2_split(rs2[j], rs[2 * j], rs[2 * j + 1]);
           const float rowsum = ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
           // P_i(t-1) V has completed (see above), so O_i can be rescaled now.
-          if (t > 0 && __any_sync(0xffffffffu, rescale)) {
+          if (t > 0 && __any_sync(0xffffffffu, scale_o)) {
             if (lane == 0 && p.rescale_count) atomicAdd(p.rescale_count, 1);
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -677,6 +823,12 @@ static int launch_fwd_impl(const FwdLaunch& a, const Bias& bias, cudaStream_t st
 
 template <bool ODD>
 static int launch_fwd_any(const FwdLaunch& a, cudaStream_t st) {
+  if (a.has_window) {
+    if (a.has_bias || a.qk8 || a.p.seg_filter >= 0) return FCP_ERR_UNSUPPORTED;
+    if (a.d == 128) return launch_fwd_impl<128, false, ODD>(a, a.window, st);
+    if (a.d == 64) return launch_fwd_impl<64, false, ODD>(a, a.window, st);
+    return FCP_ERR_UNSUPPORTED;
+  }
   if (a.has_bias) {
     if (a.qk8) return FCP_ERR_UNSUPPORTED;
     if (a.d == 128) return launch_fwd_impl<128, false, ODD>(a, a.bias, st);

@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kPreThreads) preprocess_kernel(const PreLaunch
   for (int k = blockIdx.x; k < p.n_pieces; k += gridDim.x) {
     const int32_t* piece = p.pieces + 8 * k;
     const int start = __ldg(piece + 2), end = __ldg(piece + 3);
-    const int64_t tile_end = start + ((int64_t)end - start + 127) / 128 * 128;
+    const int64_t tile_end = p.any_tiles ? (int64_t)end + 127 : start + ((int64_t)end - start + 127) / 128 * 128;
     const int stop = (int)min(tile_end, (int64_t)(k + 1 < p.n_pieces ? __ldg(piece + 8 + 2) : p.T));
     if constexpr (kDeviceChecks) {
       if (start < 0 || end <= start || end > p.T || stop > p.T) {

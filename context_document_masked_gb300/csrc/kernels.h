@@ -63,7 +63,19 @@ struct BiasParams {
   int32_t n;
   int32_t starts[kMaxBuckets];
 };
-struct NoBias {};          // kernels without a bias take this in its place
+struct NoBias {};          // kernels without a bias or a window take this in its place
+
+// The mask of a windowed plan (fcp_plan_window): kernels for one take this in
+// the bias's place. The sinks that a tile's queries see outside their windows lie
+// in the first `slots` rows of one key tile (`slots` a multiple of 8, 0 for a plan
+// without sinks), the tile's window keys behind them: boxes of `slots` and of
+// 128 - slots rows.
+struct WindowParams {
+  CUtensorMap k_sinks, v_sinks, kb_sinks, vb_sinks;  // as tm_k, tm_v, tm_kb, tm_vb
+  CUtensorMap k_rest, v_rest, kb_rest, vb_rest;
+  CUtensorMap dk_sinks, dv_sinks, dk_rest, dv_rest;  // backward: as tm_dk, tm_dv
+  int32_t window, sinks, slots;
+};
 
 struct FwdLaunch {
   CUtensorMap tm_q, tm_k, tm_v, tm_kb, tm_vb;
@@ -73,6 +85,8 @@ struct FwdLaunch {
   bool qk8;                // Q, K, received K as e4m3 (boxes of 128 bytes x 1 x 128)
   bool has_bias;
   BiasParams bias;
+  bool has_window;         // the plan is windowed (without a bias or e4m3)
+  WindowParams window;
 };
 
 // Sizes of a backward's operands, found by its preprocess: each row of dO is
@@ -116,6 +130,8 @@ struct BwdLaunch {
   int num_sms;
   bool has_bias;
   BiasParams bias;
+  bool has_window;
+  WindowParams window;
 };
 
 int launch_attn_fwd(const FwdLaunch& a, cudaStream_t st);
@@ -133,8 +149,9 @@ int64_t wait_limit_ns();
 // follows in the same stream.
 // n_rows_table: entries of `rows` (the checked build bounds the chunk indices).
 // pieces: the shard's n_pieces entries of the piece table, ascending, whose last
-// tiles' rows past the pieces are set to zero in the copies; none (0) for a
-// call over all shards, which writes every row.
+// tiles' rows past the pieces are set to zero in the copies (with `any_tiles`,
+// where tiles begin anywhere, 127 rows); none (0) for a call over all shards,
+// which writes every row.
 struct PreLaunch {
   const void* out;
   bool out_f32;
@@ -149,6 +166,7 @@ struct PreLaunch {
   BwdRange* range;
   const int32_t* pieces;
   int32_t n_pieces;
+  bool any_tiles;
   int num_sms;
   int* err;
   int* zero_word;

@@ -21,6 +21,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <limits>
+#include <memory>
 
 namespace fcp {
 
@@ -42,6 +43,18 @@ static void perdoc_pieces(int32_t doc, int64_t L, int64_t o, int32_t N,
 static int64_t sum_work(const std::vector<Piece>& ps, const std::vector<int32_t>& off) {
   int64_t w = 0;
   for (const Piece& p : ps) w += piece_work(p.start - off[p.doc], p.end - p.start);
+  return w;
+}
+
+// Pairs of a window: a query at position p of its document sees
+// min(p + 1, window) keys of the window and min(max(p + 1 - window, 0), sinks)
+// sinks outside it. ramp(n, cap) = sum over p < n of min(p + 1, cap).
+static int64_t sum_window_work(const std::vector<Piece>& ps, const std::vector<int32_t>& off, int64_t window,
+                               int64_t sinks) {
+  auto ramp = [](int64_t n, int64_t cap) { return n <= cap ? n * (n + 1) / 2 : cap * (cap + 1) / 2 + (n - cap) * cap; };
+  auto upto = [&](int64_t n) { return ramp(n, window) + (n > window ? ramp(n - window, sinks) : 0); };
+  int64_t w = 0;
+  for (const Piece& p : ps) w += upto(p.end - off[p.doc]) - upto(p.start - off[p.doc]);
   return w;
 }
 
@@ -71,6 +84,69 @@ static int64_t sum_tokens(const std::vector<Piece>& ps) {
   return t;
 }
 
+// kv_need: per document touched, [doc start, max piece end); kv_remote: that
+// minus the shard's own pieces of the document.
+void Plan::causal_needs(Shard& sh) const {
+  for (size_t a = 0; a < sh.pieces.size();) {
+    int32_t doc = sh.pieces[a].doc;
+    int32_t e = sh.pieces[a].end;
+    size_t b = a + 1;
+    while (b < sh.pieces.size() && sh.pieces[b].doc == doc) e = std::max(e, sh.pieces[b++].end);
+    sh.kv_need.push_back(fcp_range{doc, off[doc], e});
+    int32_t t = off[doc];
+    for (size_t c = a; c < b; ++c) {
+      if (sh.pieces[c].start > t) sh.kv_remote.push_back(fcp_range{doc, t, sh.pieces[c].start});
+      t = std::max(t, sh.pieces[c].end);
+    }
+    if (t < e) sh.kv_remote.push_back(fcp_range{doc, t, e});
+    a = b;
+  }
+}
+
+// The same under a window: each piece needs [start - window + 1, end) of its
+// document and the sinks that its queries see outside their windows. The
+// kernels load a document's sinks as one run, so a shard that holds some of
+// the sinks it needs but not all receives all of them.
+void Plan::window_needs(Shard& sh) const {
+  for (size_t a = 0, b; a < sh.pieces.size(); a = b) {
+    const int32_t doc = sh.pieces[a].doc, ds = off[doc];
+    int32_t sink_end = ds, held = 0;
+    std::vector<std::pair<int32_t, int32_t>> need;
+    for (b = a; b < sh.pieces.size() && sh.pieces[b].doc == doc; ++b) {
+      const Piece& p = sh.pieces[b];
+      need.push_back({std::max(ds, p.start - window + 1), p.end});
+      if (sees_sinks(p.end - 1, ds)) sink_end = std::max(sink_end, sinks_end(p.end - 1, ds));
+    }
+    if (sink_end > ds) need.push_back({ds, sink_end});
+    std::sort(need.begin(), need.end());
+    size_t n = 0;
+    for (const auto& r : need)
+      if (n && r.first <= need[n - 1].second)
+        need[n - 1].second = std::max(need[n - 1].second, r.second);
+      else
+        need[n++] = r;
+    need.resize(n);
+    for (size_t c = a; c < b; ++c)
+      held += std::max(0, std::min(sh.pieces[c].end, sink_end) - std::max(sh.pieces[c].start, ds));
+    int32_t received = ds;  // keys before it are done
+    if (held > 0 && held < sink_end - ds) {
+      sh.kv_remote.push_back(fcp_range{doc, ds, sink_end});
+      received = sink_end;
+    }
+    for (const auto& r : need) {
+      sh.kv_need.push_back(fcp_range{doc, r.first, r.second});
+      int32_t t = std::max(r.first, received);
+      for (size_t c = a; c < b && t < r.second; ++c) {
+        const Piece& p = sh.pieces[c];
+        if (p.end <= t) continue;
+        if (p.start > t) sh.kv_remote.push_back(fcp_range{doc, t, std::min(p.start, r.second)});
+        t = p.end;
+      }
+      if (t < r.second) sh.kv_remote.push_back(fcp_range{doc, t, r.second});
+    }
+  }
+}
+
 void Plan::finish(std::vector<std::vector<Piece>>& wp) {
   const int32_t n = (int32_t)D.size();
   shards.assign(N, Shard{});
@@ -85,24 +161,12 @@ void Plan::finish(std::vector<std::vector<Piece>>& wp) {
       else
         sh.pieces.push_back(p);
     }
-    // kv_need: per document touched, [doc start, max piece end).
-    for (size_t a = 0; a < sh.pieces.size();) {
-      int32_t doc = sh.pieces[a].doc;
-      int32_t e = sh.pieces[a].end;
-      size_t b = a + 1;
-      while (b < sh.pieces.size() && sh.pieces[b].doc == doc) e = std::max(e, sh.pieces[b++].end);
-      sh.kv_need.push_back(fcp_range{doc, off[doc], e});
-      // kv_remote: the needed range minus this shard's own pieces of the doc.
-      int32_t t = off[doc];
-      for (size_t c = a; c < b; ++c) {
-        if (sh.pieces[c].start > t) sh.kv_remote.push_back(fcp_range{doc, t, sh.pieces[c].start});
-        t = std::max(t, sh.pieces[c].end);
-      }
-      if (t < e) sh.kv_remote.push_back(fcp_range{doc, t, e});
-      a = b;
-    }
+    if (window > 0)
+      window_needs(sh);
+    else
+      causal_needs(sh);
     sh.tokens = sum_tokens(sh.pieces);
-    sh.W = sum_work(sh.pieces, off);
+    sh.W = window > 0 ? sum_window_work(sh.pieces, off, window, sinks) : sum_work(sh.pieces, off);
     sh.remote_rows = 0;
     for (const fcp_range& r : sh.kv_remote) sh.remote_rows += r.end - r.start;
   }
@@ -285,6 +349,27 @@ int make_plan(const int32_t* doclens, int32_t n_docs, int32_t cp, int32_t policy
   if (st != FCP_OK) { delete p; return st; }
   p->build_work_tables();
   *out = p;
+  return FCP_OK;
+}
+
+int make_window_plan(const Plan& of, int32_t window, int32_t sinks, fcp_plan_t** out) {
+  if (window < 1 || sinks < 0) return FCP_ERR_INVALID_ARG;
+  if (sinks > FCP_MAX_SINKS || of.T > (int64_t(1) << 30)) return FCP_ERR_UNSUPPORTED;
+  std::unique_ptr<fcp_plan_t> p(new fcp_plan_t());
+  p->N = of.N;
+  p->T = of.T;
+  p->D = of.D;
+  p->off = of.off;
+  p->per_doc = of.per_doc;
+  p->pd_order = of.pd_order;
+  p->iterations = of.iterations;
+  p->window = (int32_t)std::min<int64_t>(window, of.T);  // no distance is longer
+  p->sinks = sinks;
+  std::vector<std::vector<Piece>> pieces;
+  for (const Shard& s : of.shards) pieces.push_back(s.pieces);
+  p->finish(pieces);
+  p->build_work_tables();
+  *out = p.release();
   return FCP_OK;
 }
 

@@ -13,6 +13,10 @@ constexpr int kTileN = 128;   // keys per tile
 constexpr int kCopyRows = 32; // rows per gather task
 constexpr int kRowChunk = 128;
 
+// Key rows of a tile that a windowed plan's sinks take: whole groups of eight,
+// the rows after which the 128-byte swizzle begins again.
+inline int32_t sink_slots(int32_t sinks) { return (sinks + 7) / 8 * 8; }
+
 struct Piece {
   int32_t doc, start, end;
 };
@@ -30,14 +34,17 @@ struct Shard {
 
 // Device table ids (index into fcp_dev_plan::tables / counts).
 enum Table {
-  TB_PIECES = 0,   // 8 ints: shard, doc, start, end, doc_start, seg_begin, seg_count, pad
+  TB_PIECES = 0,   // 8 ints: shard, doc, start, end, doc_start, seg_begin, seg_count, row of the
+                   // document's sinks in kbuf/vbuf (windowed plans; -1: own rows from doc_start on)
   TB_SEGS,         // 4 ints: src (0 own K/V, 1 kbuf/vbuf), src_row, key_start, len
   TB_FTILES,       // 4 ints: piece, q_start, q_rows, cost   (grouped by shard)
   TB_FORDER,       // all-shards longest-first order of TB_FTILES
   TB_FSHARD,       // N+1 offsets into TB_FTILES
   TB_BTILES,       // kBwdTileInts ints: key_start, key_rows, src, src_row, then two query
                    // ranges (first tile start, piece end, tile count; the first may be
-                   // empty), piece, seg
+                   // empty), piece, seg. In windowed plans the first range is always
+                   // empty and its fields hold the document start (-1: the unit has no
+                   // sinks) and the sinks' row as in TB_PIECES
   TB_BORDER,
   TB_BSHARD,
   TB_COPY,         // 4 ints: src_row, dst_row, nrows, shard (grouped by shard)
@@ -61,6 +68,7 @@ struct Plan {
   double imbalance = 1.0;
   int64_t eq4 = 0, eq5 = 0, eq2dev = 0, total_remote = 0;
   int32_t iterations = 1;
+  int32_t window = 0, sinks = 0;     // window > 0: the mask of fcp_plan_window
   std::vector<int32_t> dev;          // serialized device tables
   int32_t tab_off[TB_COUNT] = {0};
   int32_t tab_cnt[TB_COUNT] = {0};
@@ -69,6 +77,14 @@ struct Plan {
   int build_perdoc();
   int build_algorithm1(double R, bool tiles);
   void finish(std::vector<std::vector<Piece>>& wp);
+  void causal_needs(Shard& sh) const;
+  void window_needs(Shard& sh) const;
+  // Whether queries up to `last` of a document see sinks outside their window,
+  // and the end of those they see.
+  bool sees_sinks(int32_t last, int32_t doc_start) const { return sinks > 0 && last - window >= doc_start; }
+  int32_t sinks_end(int32_t last, int32_t doc_start) const {
+    return doc_start + sinks < last - window + 1 ? doc_start + sinks : last - window + 1;
+  }
   void build_work_tables();
 };
 
@@ -79,6 +95,9 @@ struct fcp_plan : fcp::Plan {};
 namespace fcp {
 int make_plan(const int32_t* doclens, int32_t n_docs, int32_t cp, int32_t policy, double R,
               fcp_plan_t** out);
+
+// The plan of the same shards under a window (fcp_plan_window).
+int make_window_plan(const Plan& of, int32_t window, int32_t sinks, fcp_plan_t** out);
 
 // FCP_OK if `dp` describes its host plan exactly (table offsets, counts, sizes,
 // a 16-byte aligned base) and -1 <= shard < the plan's shard count;

@@ -60,6 +60,48 @@ int64_t count_masked_tiles(const std::vector<Seg>& segs, int32_t seg_begin, int3
   return n;
 }
 
+// Windowed plans. A query tile's keys are those of its rows' windows,
+// [q0 - window + 1, q_last], and where a row sees sinks outside its window the
+// first key tile begins with `slots` rows for them.
+struct WindowTiles {
+  int64_t tiles = 0, masked = 0;
+};
+WindowTiles window_key_tiles(const std::vector<Seg>& segs, int32_t seg_begin, int32_t seg_count, int32_t q0, int32_t q_last,
+                             int32_t window, int32_t slots) {
+  WindowTiles w;
+  const int32_t lo = q0 - window + 1;
+  int32_t taken = slots;  // rows of the tile that are not window keys
+  for (int32_t s = seg_begin; s < seg_begin + seg_count; ++s) {
+    const Seg& g = segs[s];
+    const int32_t end = std::min(g.key_start + g.len, q_last + 1);
+    for (int32_t k = std::max(g.key_start, lo); k < end;) {
+      const int32_t n = std::min(kTileN - taken, end - k);
+      ++w.tiles;
+      if (n < kTileN || k + kTileN - 1 > q0 || k < q_last - window + 1) ++w.masked;
+      taken = 0;
+      k += n;
+    }
+  }
+  return w;
+}
+
+// Rows of a tile against a window: `rows` of one side meet rows + window - 1 of
+// the other, in tiles of 128, beside `slots` sinks. Of the row counts that fill k
+// tiles, up to `most`, the one with the least cost a row: k tiles and `ends`, a
+// unit's beginning and end in tiles.
+int32_t rows_for_window(int32_t window, int32_t slots, int32_t most, double ends) {
+  int32_t best = most;
+  double cost = 1e30;
+  for (int64_t k = (window + slots + 127) / 128;; ++k) {
+    const int32_t rows = (int32_t)std::min<int64_t>(most, 128 * k - slots - window + 1);
+    if (rows > 0 && (k + ends) / rows < cost) {
+      cost = (k + ends) / rows;
+      best = rows;
+    }
+    if (rows == most) return best;
+  }
+}
+
 void append(std::vector<int32_t>& dev, int32_t* off, int32_t* cnt, int tb,
             const std::vector<int32_t>& data, int32_t n_entries) {
   while (dev.size() % 4) dev.push_back(0);  // 16-byte alignment of every table
@@ -78,6 +120,13 @@ void Plan::build_work_tables() {
   std::vector<int32_t> fpiece, bpiece;
   struct PieceInfo { int32_t id, doc, start, end, seg_begin, seg_count; };
   int32_t piece_id = 0;
+  // Under a window: rows of query tiles and of key tiles, with sinks and without.
+  // A forward unit's ends cost about 1.5 key tiles, a backward one's three steps.
+  const int32_t slots = sink_slots(sinks);
+  const int32_t q_plain = window > 0 ? rows_for_window(window, 0, kTileM, 1.5) : kTileM;
+  const int32_t q_sinks = window > 0 ? rows_for_window(window, slots, kTileM, 1.5) : kTileM;
+  const int32_t k_plain = window > 0 ? rows_for_window(window, 0, kTileN, 3) : kTileN;
+  const int32_t k_sinks = window > 0 ? rows_for_window(window, 0, kTileN - slots, 3) : kTileN;
   for (int32_t j = 0; j < N; ++j) {
     const Shard& sh = shards[j];
     fshard[j] = (int32_t)(ftiles.size() / 4);
@@ -100,9 +149,9 @@ void Plan::build_work_tables() {
     for (const Piece& p : sh.pieces) {
       const int32_t ds = off[p.doc];
       const int32_t seg_begin = (int32_t)segs.size();
-      // Walk [ds, p.end): own pieces of this doc and remote ranges of this doc
-      // are disjoint and together cover the needed range.
-      int32_t t = ds;
+      // Walk [ds, p.end) (or the window's part of it): own pieces of this doc
+      // and remote ranges of this doc together cover the needed range.
+      int32_t t = window > 0 ? std::max(ds, p.start - window + 1) : ds;
       while (t < p.end) {
         bool found = false;
         for (const Piece& o : sh.pieces) {
@@ -119,6 +168,7 @@ void Plan::build_work_tables() {
           const fcp_range& rr = sh.kv_remote[r];
           if (rr.doc == p.doc && rr.start <= t && t < rr.end) {
             int32_t e = std::min(rr.end, p.end);
+            if (t < p.start) e = std::min(e, p.start);  // (received sinks may run into the piece)
             segs.push_back(Seg{1, (int32_t)(rpos[r] + (t - rr.start)), t, e - t});
             t = e;
             found = true;
@@ -128,8 +178,30 @@ void Plan::build_work_tables() {
         if (!found) break;  // unreachable for a consistent plan
       }
       const int32_t seg_count = (int32_t)segs.size() - seg_begin;
-      pieces.insert(pieces.end(), {j, p.doc, p.start, p.end, ds, seg_begin, seg_count, 0});
+      // Where the document's sinks are: received as one run, or all held here.
+      int32_t sink_row = 0;
+      if (sees_sinks(p.end - 1, ds)) {
+        sink_row = -1;
+        for (size_t r = 0; r < sh.kv_remote.size(); ++r)
+          if (sh.kv_remote[r].doc == p.doc && sh.kv_remote[r].start == ds) sink_row = (int32_t)rpos[r];
+      }
+      pieces.insert(pieces.end(), {j, p.doc, p.start, p.end, ds, seg_begin, seg_count, sink_row});
       // Forward query tiles.
+      if (window > 0) {
+        for (int32_t q0 = p.start, qr; q0 < p.end; q0 += qr) {
+          const bool far = sees_sinks(q0 + kTileM - 1, ds);
+          qr = q0 + kTileM - 1 - window < ds ? kTileM : far ? q_sinks : q_plain;  // near the document's start no window cuts
+          qr = std::min(qr, p.end - q0);
+          const int32_t last = q0 + qr - 1;
+          const WindowTiles w = window_key_tiles(segs, seg_begin, seg_count, q0, last, window, sees_sinks(last, ds) ? slots : 0);
+          ftiles.insert(ftiles.end(), {piece_id, q0, qr, (int32_t)std::min<int64_t>(w.tiles, 1 << 30)});
+          fcost.push_back(w.tiles);
+          fpiece.push_back(piece_id);
+          shards[j].fwd_tiles += w.tiles;
+          shards[j].fwd_qtiles += 1;
+          shards[j].fwd_masked += w.masked;
+        }
+      } else
       for (int32_t q0 = p.start; q0 < p.end; q0 += kTileM) {
         int32_t qr = std::min(kTileM, p.end - q0);
         int64_t c = count_key_tiles(segs, seg_begin, seg_count, q0 + qr - 1);
@@ -155,7 +227,32 @@ void Plan::build_work_tables() {
       *q0 = pc.start + qt_first * kTileM;
       *n = (pc.end - pc.start + kTileM - 1) / kTileM - qt_first;
     };
-    for (size_t i = 0; i < pinfo.size(); ++i) {
+    // Under a window a key tile's queries end a window after its last key, and
+    // the pieces' walks begin at their own windows, so every piece has units of
+    // its own. The sinks ride in the key tiles that hold the piece's own rows:
+    // each query meets them in the one tile that holds its own key.
+    for (size_t i = 0; window > 0 && i < pinfo.size(); ++i) {
+      const PieceInfo& pc = pinfo[i];
+      const int32_t ds = off[pc.doc];
+      for (int32_t s = pc.seg_begin; s < pc.seg_begin + pc.seg_count; ++s) {
+        const Seg& g = segs[s];
+        for (int32_t k0 = 0, kr; k0 < g.len; k0 += kr) {
+          const int32_t key = g.key_start + k0;
+          const bool own = key >= pc.start;  // (a segment is before the piece or inside it)
+          kr = std::min(own && sees_sinks(key + kTileN - 1, ds) ? k_sinks : k_plain, g.len - k0);
+          const bool with_sinks = own && sees_sinks(key + kr - 1, ds);
+          const int32_t qb0 = std::max(key, pc.start), q_end = std::min(pc.end, key + kr - 1 + window);
+          const int32_t nb = (q_end - qb0 + kTileM - 1) / kTileM;
+          btiles.insert(btiles.end(), {key, kr, g.src, g.src_row + k0, with_sinks ? ds : -1,
+                                       with_sinks ? pieces[8 * pc.id + 7] : -1, 0, qb0, q_end, nb, pc.id, s});
+          bcost.push_back(nb);
+          bpiece.push_back(pc.id);
+          shards[j].bwd_tiles += nb;
+          shards[j].bwd_ktiles += 1;
+        }
+      }
+    }
+    for (size_t i = 0; window == 0 && i < pinfo.size(); ++i) {
       const PieceInfo& pc = pinfo[i];
       int n_same = 0, partner = -1;
       for (size_t o = 0; o < pinfo.size(); ++o)

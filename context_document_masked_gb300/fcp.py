@@ -32,8 +32,10 @@ EXPORTED = (
     "fcp_attn_fwd_qk8", "fcp_quant_e4m3", "fcp_plan_device_image", "fcp_plan_bind",
     "fcp_debug_rescale_events", "fcp_round_bf16", "fcp_merge_ring", "fcp_qk_norm_rope",
     "fcp_qk_norm_rope_bwd", "fcp_rel_buckets", "fcp_attn_fwd_bias", "fcp_attn_bwd_bias",
+    "fcp_plan_window",
 )
 MAX_BUCKETS = 128
+MAX_SINKS = 64
 
 torch = None
 _BF16, _F32, _BF16_F32, _U8, _I32 = range(5)  # places in _DTYPES
@@ -108,6 +110,7 @@ def _load():
     sig = {
         "fcp_strerror": (C.c_char_p, [C.c_int]),
         "fcp_plan": (C.c_int, [C.POINTER(C.c_int32), i32, i32, i32, f64, C.POINTER(vp)]),
+        "fcp_plan_window": (C.c_int, [vp, i32, i32, C.POINTER(vp)]),
         "fcp_plan_free": (None, [vp]),
         "fcp_plan_shard": (C.c_int, [vp, i32, C.POINTER(ShardView)]),
         "fcp_plan_query_indices": (C.c_int, [vp, i32, C.POINTER(C.c_int32), i64, C.POINTER(i64)]),
@@ -181,6 +184,18 @@ class Plan:
         self.doclens = d
         self.cp = cp
         self.policy = policy
+        self.window = self.sinks = 0  # no window
+
+    def windowed(self, window: int, sinks: int = 0) -> "Plan":
+        """fcp_plan_window: the plan of the same shards for attention in which a
+        token sees the last `window` tokens of its document, itself among them,
+        and the document's first `sinks`."""
+        p = object.__new__(Plan)
+        p._ptr = C.c_void_p()
+        _check(_lib.fcp_plan_window(self._ptr, window, sinks, C.byref(p._ptr)), "fcp_plan_window")
+        p.doclens, p.cp, p.policy = self.doclens, self.cp, self.policy
+        p.window, p.sinks = window, sinks
+        return p
 
     def __del__(self):
         if getattr(self, "_ptr", None) and self._ptr.value:

@@ -23,9 +23,14 @@ def _on_stream(stream):
 
 class CPAttention:
     def __init__(self, doclens, cp: int, policy: str, hq: int, hkv: int, d: int,
-                 device="cuda", target_imbalance: float = 1.05, scale: float = 0.0):
+                 device="cuda", target_imbalance: float = 1.05, scale: float = 0.0, window: int = 0, sinks: int = 0):
+        """window > 0: gather(), forward() and backward() are those of a sliding
+        window (a token sees the last `window` tokens of its document, itself
+        among them, and the document's first `sinks`). Sessions of one packed
+        sequence that differ in their windows have the same shards."""
         self.device = torch.device(device)
-        self.plan = fcp.Plan(doclens, cp, policy, target_imbalance)
+        self.window, self.sinks = window, sinks
+        self.plan = self._make_plan(doclens, cp, policy, target_imbalance)
         self.T = int(sum(int(x) for x in doclens))
         self.hq, self.hkv, self.d, self.cp = hq, hkv, d, cp
         self.scale = scale
@@ -39,15 +44,21 @@ class CPAttention:
         ws_bytes = fcp.workspace_bytes(self.dims, self.plan)
         self.ws = torch.zeros(ws_bytes // 4, dtype=torch.int32, device=self.device)
 
+    def _make_plan(self, doclens, cp, policy, target_imbalance):
+        if not self.window and self.sinks:
+            raise ValueError("sinks are those of a window: window > 0")
+        plan = fcp.Plan(doclens, cp, policy, target_imbalance)
+        return plan.windowed(self.window, self.sinks) if self.window else plan
+
     def set_plan(self, doclens, target_imbalance: float = 1.05, stream=None):
-        """A new plan for the next packed sequence (same T, CP size, policy and
-        shapes), uploaded into this session's plan buffer on `stream`; the
+        """A new plan for the next packed sequence (same T, CP size, policy,
+        shapes and window), uploaded into this session's plan buffer on `stream`; the
         received-key buffers and the workspace are kept when they are large
         enough and replaced otherwise, in that stream's order. The previous plan's tables must no longer
         be in use by queued work on other streams."""
         if int(sum(int(x) for x in doclens)) != self.T:
             raise ValueError("set_plan: the token count differs from the session's")
-        plan = fcp.Plan(doclens, self.cp, self.plan.policy, target_imbalance)
+        plan = self._make_plan(doclens, self.cp, self.plan.policy, target_imbalance)
         nbytes = plan.device_bytes()
         with _on_stream(stream):
             if self.plan_buf.numel() * 4 < nbytes:

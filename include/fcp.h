@@ -138,6 +138,30 @@ int fcp_plan(const int32_t* doclens, int32_t n_docs, int32_t cp, int32_t policy,
 
 void fcp_plan_free(fcp_plan_t* plan);
 
+/*
+ * fcp_plan_window -- the plan of the same shards for a layer whose attention
+ * is cut to a sliding window: query i of a document that starts at o sees key
+ * j <= i if i - j < window or j - o < sinks (its last `window` tokens, itself
+ * among them, and the document's first `sinks`). The shards' pieces are those
+ * of `plan`, so layers with a window and without, or with different ones, work
+ * on one sharding; needed and received keys, pairs, imbalance, tiles and work
+ * tables are the window's (a shard receives a window's keys before each of its
+ * pieces and the documents' sinks, however long the documents are). A shard that
+ * holds some but not all of the sinks it needs receives all of them.
+ *   window   >= 1; at a document's length and above nothing is cut.
+ *   sinks    0 .. FCP_MAX_SINKS.
+ *   out      receives a new plan, to be freed with fcp_plan_free; `plan` may be
+ *            freed before it.
+ * fcp_gather_kv, fcp_attn_fwd, fcp_attn_bwd, the head norm and rotation and the
+ * residual norm take it like any other plan; fcp_attn_fwd_qk8, _ring, _noalloc
+ * and _bias and fcp_attn_bwd_bias return FCP_ERR_UNSUPPORTED for it. eq4_tokens
+ * and eq5_tokens stay those of whole prefixes, as the paper defines them.
+ * Errors: FCP_ERR_INVALID_ARG (null, window < 1, sinks < 0), FCP_ERR_UNSUPPORTED
+ * (sinks > FCP_MAX_SINKS, T > 2^30), FCP_ERR_CAPACITY (no host memory).
+ */
+#define FCP_MAX_SINKS 64
+int fcp_plan_window(const fcp_plan_t* plan, int32_t window, int32_t sinks, fcp_plan_t** out);
+
 /* Shard j's pieces, needed and remote KV ranges ([FlashCP] §3.2). */
 int fcp_plan_shard(const fcp_plan_t* plan, int32_t shard, fcp_shard_view* out);
 
