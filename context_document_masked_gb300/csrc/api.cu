@@ -978,6 +978,139 @@ int fcp_qk_norm_rope_bwd(const float* dq, const float* dk, const float* dv, cons
   return fcp::launch_norm_rope(a, static_cast<cudaStream_t>(stream));
 }
 
+// The options and weights of a residual norm, and the launch's rows.
+static int res_norm_params(fcp::ResNormParams* p, const fcp_res_norm* rn, const void* y, const void* gate, const void* w_post,
+                           const void* w_pre, const fcp_dev_plan* plan, int32_t shard, int32_t n) {
+  if (int st = check_dev_plan(plan, shard)) return st;
+  if (n < 8 || n > 16384 || n % 8) return FCP_ERR_UNSUPPORTED;
+  if (!rn) return FCP_ERR_INVALID_ARG;
+  auto flag = [](int32_t v) { return v == 0 || v == 1; };
+  auto finite = [](float v) { return std::fabs(v) <= 3.4e38f; };
+  if (!flag(rn->post_norm) || !flag(rn->pre_norm) || !flag(rn->add_dw) || !flag(rn->gate_fn) || !flag(rn->res_dtype) ||
+      !flag(rn->w_dtype))
+    return FCP_ERR_INVALID_ARG;
+  if (!(rn->eps >= 0.f) || !finite(rn->eps) || !finite(rn->res_scale) || !finite(rn->branch_scale)) return FCP_ERR_INVALID_ARG;
+  if (!y && (gate || w_post)) return FCP_ERR_INVALID_ARG;
+  if (!rn->pre_norm && w_pre) return FCP_ERR_INVALID_ARG;
+  if (!aligned16(w_post) || !aligned16(w_pre)) return FCP_ERR_INVALID_ARG;
+  std::memset(p, 0, sizeof(*p));
+  const Plan* host = plan->host;
+  p->T = plan->T;
+  p->n = n;
+  p->places = plan->T;
+  if (shard >= 0) {
+    const int32_t r0 = host_at(host, fcp::TB_RSHARD, shard), r1 = host_at(host, fcp::TB_RSHARD, shard + 1);
+    static_assert(fcp::kResNormChunk >= fcp::kRowChunk, "a chunk's rows");
+    p->chunks = table(plan, fcp::TB_ROWS) + 2 * (int64_t)r0;
+    p->places = (int64_t)(r1 - r0) * fcp::kResNormChunk;
+  }
+  p->post_norm = rn->post_norm;
+  p->gate_fn = rn->gate_fn;
+  p->res_f32 = rn->res_dtype == FCP_OUT_F32;
+  p->w_f32 = rn->w_dtype == FCP_OUT_F32;
+  p->add_dw = rn->add_dw;
+  p->eps = rn->eps;
+  p->res_scale = rn->res_scale;
+  p->branch_scale = rn->branch_scale;
+  p->y = y;
+  p->gate = gate;
+  p->w_post = w_post;
+  p->w_pre = w_pre;
+  return FCP_OK;
+}
+
+// One operand's rows of n values of `size` bytes.
+struct Rows {
+  const void* at;
+  int64_t stride, size;
+  bool ok(const fcp::ResNormParams& p) const {
+    return at && aligned16(at) && stride % 8 == 0 && stride >= p.n && stride <= INT64_MAX / 16 / p.T;
+  }
+  RowSpan span(const fcp::ResNormParams& p) const { return {(uintptr_t)at, stride * size, p.n * size}; }
+  bool same(const Rows& o) const { return at == o.at && stride * size == o.stride * o.size; }
+};
+
+// No output meets another operand, but for out[i] on in[i] itself.
+static bool rows_apart(const fcp::ResNormParams& p, const Rows* out, int n_out, const Rows* in, int n_in) {
+  for (int o = 0; o < n_out; ++o) {
+    if (!out[o].at) continue;
+    for (int i = 0; i < n_in; ++i)
+      if (in[i].at && !(i == o && out[o].same(in[i])) && spans_meet(out[o].span(p), in[i].span(p), p.T)) return false;
+    for (int i = 0; i < o; ++i)
+      if (out[i].at && spans_meet(out[o].span(p), out[i].span(p), p.T)) return false;
+  }
+  return true;
+}
+
+int fcp_residual_norm(const void* x, int64_t x_stride, const void* y, int64_t y_stride, const void* gate,
+                      int64_t gate_stride, const void* w_post, const void* w_pre, const fcp_res_norm* rn,
+                      const fcp_dev_plan* plan, int32_t shard, int32_t n, void* x_out, int64_t x_out_stride, void* h,
+                      int64_t h_stride, void* stream) {
+  fcp::ResNormParams p;
+  if (int st = res_norm_params(&p, rn, y, gate, w_post, w_pre, plan, shard, n)) return st;
+  const int64_t res = p.res_f32 ? 4 : 2;
+  const Rows in[4] = {{x, x_stride, res}, {nullptr, 0, 0}, {y, y_stride, 2}, {gate, gate_stride, 2}};  // h is in no one's place
+  const Rows out[2] = {{x_out, x_out_stride, res}, {h, h_stride, 2}};
+  if (!in[0].ok(p) || (y && !in[2].ok(p)) || (gate && !in[3].ok(p))) return FCP_ERR_INVALID_ARG;
+  if (!x_out && (y || rn->res_scale != 1.f || !h)) return FCP_ERR_INVALID_ARG;
+  if ((x_out && !out[0].ok(p)) || !h != !rn->pre_norm || (h && !out[1].ok(p))) return FCP_ERR_INVALID_ARG;
+  if (!rows_apart(p, out, 2, in, 4)) return FCP_ERR_INVALID_ARG;
+  p.x = x;
+  p.x_row = x_stride * res;
+  p.y_row = y_stride * 2;
+  p.gate_row = gate_stride * 2;
+  p.x_out = x_out;
+  p.x_out_row = x_out_stride * res;
+  p.h = h;
+  p.h_row = h_stride * 2;
+  return fcp::launch_res_norm(p, static_cast<cudaStream_t>(stream));
+}
+
+int64_t fcp_residual_norm_ws_bytes(int32_t n) { return n < 8 || n > 16384 || n % 8 ? 0 : fcp::res_norm_ws_bytes(n); }
+
+int fcp_residual_norm_bwd(const void* dh, int64_t dh_stride, const void* dx_out, int64_t dx_out_stride, const void* x_out,
+                          int64_t x_out_stride, const void* y, int64_t y_stride, const void* gate, int64_t gate_stride,
+                          const void* w_post, const void* w_pre, const fcp_res_norm* rn, const fcp_dev_plan* plan,
+                          int32_t shard, int32_t n, void* dx, int64_t dx_stride, void* dy, int64_t dy_stride, void* dgate,
+                          int64_t dgate_stride, float* dw_post, float* dw_pre, void* ws, int64_t ws_bytes, void* stream) {
+  fcp::ResNormParams p;
+  if (int st = res_norm_params(&p, rn, y, gate, w_post, w_pre, plan, shard, n)) return st;
+  const int64_t res = p.res_f32 ? 4 : 2;
+  const Rows in[5] = {{dx_out, dx_out_stride, res}, {y, y_stride, 2}, {gate, gate_stride, 2}, {dh, dh_stride, 2}, {x_out, x_out_stride, res}};
+  const Rows out[3] = {{dx, dx_stride, res}, {dy, dy_stride, 2}, {dgate, dgate_stride, 2}};
+  if (!dh != !rn->pre_norm || (dh && (!in[3].ok(p) || !in[4].ok(p)))) return FCP_ERR_INVALID_ARG;
+  if ((!dh && !dx_out) || (dx_out && !in[0].ok(p))) return FCP_ERR_INVALID_ARG;
+  if ((y && !in[1].ok(p)) || (gate && !in[2].ok(p))) return FCP_ERR_INVALID_ARG;
+  if (!out[0].ok(p) || !dy != !y || (dy && !out[1].ok(p)) || !dgate != !gate || (dgate && !out[2].ok(p)))
+    return FCP_ERR_INVALID_ARG;
+  if ((dw_post && !y) || (dw_pre && !dh)) return FCP_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(dw_post) & 3) || (reinterpret_cast<uintptr_t>(dw_pre) & 3)) return FCP_ERR_INVALID_ARG;
+  if (dw_post && dw_pre && ranges_meet(dw_post, dw_pre, n)) return FCP_ERR_INVALID_ARG;
+  if (!rows_apart(p, out, 3, in, dh ? 5 : 3)) return FCP_ERR_INVALID_ARG;
+  if (dw_post || dw_pre) {
+    if (!ws || !aligned16(ws)) return FCP_ERR_INVALID_ARG;
+    if (ws_bytes < fcp::res_norm_ws_bytes(n)) return FCP_ERR_CAPACITY;
+  }
+  p.x = x_out;
+  p.x_row = x_out_stride * res;
+  p.y_row = y_stride * 2;
+  p.gate_row = gate_stride * 2;
+  p.dh = dh;
+  p.dh_row = dh_stride * 2;
+  p.dx_out = dx_out;
+  p.dx_out_row = dx_out_stride * res;
+  p.dx = dx;
+  p.dx_row = dx_stride * res;
+  p.dy = dy;
+  p.dy_row = dy_stride * 2;
+  p.dgate = dgate;
+  p.dgate_row = dgate_stride * 2;
+  p.dw_post = dw_post;
+  p.dw_pre = dw_pre;
+  p.partial = static_cast<float*>(ws);
+  return fcp::launch_res_norm(p, static_cast<cudaStream_t>(stream));
+}
+
 int fcp_get_device_status(void* ws, void* stream) {
   if (!ws) return FCP_ERR_INVALID_ARG;
   int word = 0;

@@ -66,6 +66,12 @@
 // in BiasSteps::load another 0.4 to 0.8). Slower: the sums
 // in the compute warps, by matrix instructions (no faster, for their set-up),
 // in a table for each CTA.
+//
+// Under a window (a separate instantiation, for windowed plans) a unit's queries
+// end a window after its last key. The sinks outside a query's window ride in
+// the first rows of the key tile that holds the query's own key, so no unit has
+// all of a document's queries and no step is for the sinks alone; their dK and
+// dV leave every such unit in a box of their own.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -256,4 +256,30 @@ struct NormRopeLaunch {
 
 int launch_norm_rope(const NormRopeLaunch& a, cudaStream_t st);
 
+// The residual stream between two blocks, and its gradient (residual_norm.cu).
+// *_row: bytes between rows. Null pointers: no block output, no gate, ones for
+// weights, no norm before the next block (h and dh), no gradient of the residual
+// after the block (dx_out); dx is null in the forward.
+constexpr int kResNormMaxCtas = 1216;
+constexpr int kResNormChunk = 128;   // rows of a chunk at most (plan.h, TB_ROWS)
+struct ResNormParams {
+  const int32_t* chunks;   // TB_ROWS entries of a shard; null: all tokens
+  int64_t places;          // tokens, or kResNormChunk for each chunk
+  int32_t T, n, groups;    // (groups: set by the launch)
+  int32_t post_norm, gate_fn, res_f32, w_f32, add_dw;
+  float eps, res_scale, branch_scale;
+  const void *x, *y, *gate, *w_post, *w_pre;  // x: before the block; in the backward after it
+  int64_t x_row, y_row, gate_row;
+  void *x_out, *h;
+  int64_t x_out_row, h_row;
+  const void *dh, *dx_out;
+  int64_t dh_row, dx_out_row;
+  void *dx, *dy, *dgate;
+  int64_t dx_row, dy_row, dgate_row;
+  float *dw_post, *dw_pre;
+  float* partial;          // [res_norm_ws_bytes(n)]
+};
+int64_t res_norm_ws_bytes(int n);
+int launch_res_norm(const ResNormParams& p, cudaStream_t st);
+
 }  // namespace fcp

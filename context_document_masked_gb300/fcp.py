@@ -32,7 +32,7 @@ EXPORTED = (
     "fcp_attn_fwd_qk8", "fcp_quant_e4m3", "fcp_plan_device_image", "fcp_plan_bind",
     "fcp_debug_rescale_events", "fcp_round_bf16", "fcp_merge_ring", "fcp_qk_norm_rope",
     "fcp_qk_norm_rope_bwd", "fcp_rel_buckets", "fcp_attn_fwd_bias", "fcp_attn_bwd_bias",
-    "fcp_plan_window",
+    "fcp_plan_window", "fcp_residual_norm", "fcp_residual_norm_bwd", "fcp_residual_norm_ws_bytes",
 )
 MAX_BUCKETS = 128
 MAX_SINKS = 64
@@ -97,6 +97,12 @@ class NormRope(C.Structure):
                 ("w_dtype", C.c_int32), ("add_dw", C.c_int32)]
 
 
+class ResNorm(C.Structure):
+    _fields_ = [("post_norm", C.c_int32), ("pre_norm", C.c_int32), ("gate_fn", C.c_int32), ("eps", C.c_float),
+                ("res_scale", C.c_float), ("branch_scale", C.c_float), ("res_dtype", C.c_int32), ("w_dtype", C.c_int32),
+                ("add_dw", C.c_int32)]
+
+
 class RelBias(C.Structure):
     _fields_ = [("bias", C.c_void_p), ("starts", C.POINTER(C.c_int32)), ("n_buckets", C.c_int32),
                 ("zero_grads", C.c_int32)]
@@ -150,6 +156,11 @@ def _load():
         "fcp_qk_norm_rope_bwd": (C.c_int, [vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, C.POINTER(NormRope),
                                            C.POINTER(DevPlan), i32, Dims, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64,
                                            vp]),
+        "fcp_residual_norm": (C.c_int, [vp, i64, vp, i64, vp, i64, vp, vp, C.POINTER(ResNorm), C.POINTER(DevPlan), i32, i32,
+                                        vp, i64, vp, i64, vp]),
+        "fcp_residual_norm_ws_bytes": (i64, [i32]),
+        "fcp_residual_norm_bwd": (C.c_int, [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, C.POINTER(ResNorm),
+                                            C.POINTER(DevPlan), i32, i32, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -689,6 +700,102 @@ def qk_norm_rope_bwd(dq, dk, dv, q_in, k_in, dplan: DevicePlan, shard: int, dq_i
                                          Dims(T, hq, hkv, d, 0.0), _ptr(dq_in), sdq, _ptr(dk_in), sdk, _ptr(dv_in), sdv,
                                          _ptr(dwq), _ptr(dwk), _ptr(ws), ws.numel() * ws.element_size(),
                                          _stream(stream)), "fcp_qk_norm_rope_bwd")
+
+
+# ------------------------------------- residual stream between two blocks
+
+GATES = {"plain": 0, "sigmoid": 1}
+
+
+def _matrix(t, name, dtype, T, n):
+    """The stride of a [T][n] tensor whose rows are contiguous and `stride`
+    elements apart (a slice of a wider tensor); 0 for None."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != (T, n):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(T, n)}")
+    stride, of_value = t.stride()
+    if of_value != 1 and n > 1:
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+    if T == 1:
+        stride = max(n, (n + 7) // 8 * 8)
+    if stride % 8 or stride < n:
+        raise ValueError(f"{name}: row stride {stride}, expected a multiple of 8 of at least {n}")
+    return stride
+
+
+def _res_norm_opts(x, dplan, w_post, w_pre, post_norm, pre_norm, gate_fn, eps, res_scale, branch_scale, add_dw=0):
+    if torch is None:
+        _import_torch()
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _DTYPES[_BF16_F32]:
+        raise ValueError("the residual: expected a bf16 or fp32 tensor [T][n]")
+    T, n = x.shape
+    if T != dplan.c.T:
+        raise ValueError(f"the residual: {T} rows, the plan has {dplan.c.T} tokens")
+    for t, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if t is not None:
+            _t(t, name, _BF16_F32, (n,))
+    if w_post is not None and w_pre is not None and w_post.dtype != w_pre.dtype:
+        raise ValueError(f"w_post and w_pre: dtypes {w_post.dtype} and {w_pre.dtype}, expected one for both")
+    if gate_fn not in GATES:
+        raise ValueError(f"gate_fn: {gate_fn!r}, expected one of {sorted(GATES)}")
+    w = w_post if w_post is not None else w_pre
+    return T, n, x.dtype, ResNorm(int(post_norm), int(pre_norm), GATES[gate_fn], eps, res_scale, branch_scale,
+                                  OUT_F32 if x.dtype == torch.float32 else OUT_BF16,
+                                  OUT_BF16 if w is not None and w.dtype == torch.bfloat16 else OUT_F32, int(add_dw))
+
+
+def residual_norm(x, y, gate, dplan: DevicePlan, shard: int, x_out, h, w_post=None, w_pre=None, post_norm: bool = True,
+                  gate_fn: str = "sigmoid", res_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6,
+                  stream=None):
+    """fcp_residual_norm: x_out (the type of x, bf16 or fp32) = res_scale x + branch_scale
+    g(gate) norm(y) w_post and h (bf16; None: no norm) = norm(x_out) w_pre. y, gate (bf16), x_out
+    and the weights may be None; tensors [T][n], slices of wider ones among them."""
+    T, n, res, rn = _res_norm_opts(x, dplan, w_post, w_pre, post_norm, h is not None, gate_fn, eps, res_scale, branch_scale)
+    b16 = torch.bfloat16
+    strides = [_matrix(t, name, dt, T, n) for t, name, dt in ((x, "x", res), (y, "y", b16), (gate, "gate", b16),
+                                                              (x_out, "x_out", res), (h, "h", b16))]
+    with _on(x, y, gate, x_out, h, w_post, w_pre, dplan.buf):
+        _check(_lib.fcp_residual_norm(_ptr(x), strides[0], _ptr(y), strides[1], _ptr(gate), strides[2], _ptr(w_post),
+                                      _ptr(w_pre), C.byref(rn), C.byref(dplan.c), shard, n, _ptr(x_out), strides[3], _ptr(h),
+                                      strides[4], _stream(stream)), "fcp_residual_norm")
+
+
+def residual_norm_ws_bytes(n: int) -> int:
+    return int(_lib.fcp_residual_norm_ws_bytes(n))
+
+
+def residual_norm_bwd(dh, dx_out, x_out, y, gate, dplan: DevicePlan, shard: int, dx, dy, dgate, dw_post, dw_pre, ws,
+                      w_post=None, w_pre=None, post_norm: bool = True, gate_fn: str = "sigmoid", res_scale: float = 1.0,
+                      branch_scale: float = 1.0, eps: float = 1e-6, add_dw: bool = False, stream=None):
+    """fcp_residual_norm_bwd: from dh (bf16; None: no norm before the next block) and dx_out (the type
+    of the residual, or None) the gradients dx, dy and dgate, and dw_post and dw_pre (fp32 [n] or
+    None), written or with add_dw added to. ws: residual_norm_ws_bytes(n) bytes, or None
+    without weights' gradients."""
+    T, n, res, rn = _res_norm_opts(dx, dplan, w_post, w_pre, post_norm, dh is not None, gate_fn, eps, res_scale,
+                                   branch_scale, add_dw)
+    b16 = torch.bfloat16
+    strides = [_matrix(t, name, dt, T, n)
+               for t, name, dt in ((dh, "dh", b16), (dx_out, "dx_out", res), (x_out, "x_out", res), (y, "y", b16),
+                                   (gate, "gate", b16), (dx, "dx", res), (dy, "dy", b16), (dgate, "dgate", b16))]
+    for t, name in ((dw_post, "dw_post"), (dw_pre, "dw_pre")):
+        if t is not None:
+            _t(t, name, _F32, (n,))
+    if ws is not None:
+        _t(ws, "ws")
+    with _on(dx, dh, dx_out, x_out, y, gate, dy, dgate, dw_post, dw_pre, ws, w_post, w_pre, dplan.buf):
+        _check(_lib.fcp_residual_norm_bwd(_ptr(dh), strides[0], _ptr(dx_out), strides[1], _ptr(x_out), strides[2], _ptr(y),
+                                          strides[3], _ptr(gate), strides[4], _ptr(w_post), _ptr(w_pre), C.byref(rn),
+                                          C.byref(dplan.c), shard, n, _ptr(dx), strides[5], _ptr(dy), strides[6],
+                                          _ptr(dgate), strides[7], _ptr(dw_post), _ptr(dw_pre), _ptr(ws),
+                                          0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+               "fcp_residual_norm_bwd")
 
 
 def device_status(ws, stream=None) -> int:

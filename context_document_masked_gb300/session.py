@@ -209,5 +209,51 @@ class CPAttention:
                              stream=stream)
         return dq_in, dk_in, dv_in, dwq, dwk
 
+    def residual_norm(self, x, y=None, gate=None, w_post=None, w_pre=None, post_norm: bool = True, pre_norm: bool = True,
+                      gate_fn: str = "sigmoid", res_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6,
+                      shard: int = -1, x_out=None, h=None, stream=None):
+        """The residual stream after a block and the next block's input, (x_out, h): the block's output
+        y normed (post_norm), gated, scaled and added to the residual x, and that normed again (pre_norm;
+        else h is None). x [T][n] bf16 or fp32, y and gate bf16; without y only the norm (x_out is then
+        x itself where res_scale is 1 and it is not given)."""
+        with _on_stream(stream):
+            if x_out is None and (y is not None or res_scale != 1.0 or not pre_norm):
+                x_out = torch.empty(x.shape, dtype=x.dtype, device=self.device)
+            if h is None and pre_norm:
+                h = torch.empty(x.shape, dtype=torch.bfloat16, device=self.device)
+        fcp.residual_norm(x, y, gate, self.dplan, shard, x_out, h, w_post=w_post, w_pre=w_pre, post_norm=post_norm,
+                          gate_fn=gate_fn, res_scale=res_scale, branch_scale=branch_scale, eps=eps, stream=stream)
+        return x if x_out is None else x_out, h
+
+    def residual_norm_backward(self, dh, dx_out, x_out, y=None, gate=None, w_post=None, w_pre=None, post_norm: bool = True,
+                               gate_fn: str = "sigmoid", res_scale: float = 1.0, branch_scale: float = 1.0,
+                               eps: float = 1e-6, shard: int = -1, dx=None, dy=None, dgate=None, dw_post=None, dw_pre=None,
+                               zero_grads: bool = False, stream=None):
+        """Gradient of residual_norm, (dx, dy, dgate, dw_post, dw_pre), from dh (None: no norm before the
+        next block) and dx_out, the gradient along the residual (None: none). The fp32 gradients of the
+        weights are added to dw_post and dw_pre where they are given (zero_grads: written there). Its
+        workspace is made in the order of the call's stream."""
+        like = x_out if x_out is not None else dx_out
+        n = like.shape[1]
+        with _on_stream(stream):
+            def rows(t, dtype):
+                return torch.empty(t.shape, dtype=dtype, device=self.device)
+            dx = rows(like, like.dtype) if dx is None else dx
+            dy = rows(y, y.dtype) if dy is None and y is not None else dy
+            dgate = rows(gate, gate.dtype) if dgate is None and gate is not None else dgate
+            add = not zero_grads and (dw_post is not None or dw_pre is not None)  # to the given ones: new ones start at zero
+            make = torch.zeros if add else torch.empty
+            if dw_post is None and w_post is not None:
+                dw_post = make(n, dtype=torch.float32, device=self.device)
+            if dw_pre is None and w_pre is not None:
+                dw_pre = make(n, dtype=torch.float32, device=self.device)
+            ws = None
+            if dw_post is not None or dw_pre is not None:
+                ws = torch.empty(fcp.residual_norm_ws_bytes(n) // 4, dtype=torch.float32, device=self.device)
+        fcp.residual_norm_bwd(dh, dx_out, x_out, y, gate, self.dplan, shard, dx, dy, dgate, dw_post, dw_pre, ws,
+                              w_post=w_post, w_pre=w_pre, post_norm=post_norm, gate_fn=gate_fn, res_scale=res_scale,
+                              branch_scale=branch_scale, eps=eps, add_dw=add, stream=stream)
+        return dx, dy, dgate, dw_post, dw_pre
+
     def device_status(self) -> int:
         return fcp.device_status(self.ws)

@@ -543,6 +543,79 @@ int fcp_qk_norm_rope_bwd(const float* dq, const float* dk, const float* dv, cons
                          int64_t dq_stride, void* dk_in, int64_t dk_stride, void* dv_in, int64_t dv_stride, float* dwq,
                          float* dwk, void* ws, int64_t ws_bytes, void* stream);
 
+/* Options of the residual norm. */
+enum { FCP_GATE_PLAIN = 0, FCP_GATE_SIGMOID = 1 };
+typedef struct {
+  int32_t post_norm;    /* 1: RMS norm of the block's output; 0: as it is (w_post then scales it) */
+  int32_t pre_norm;     /* 1: RMS norm before the next block; 0: none (h, dh, w_pre, dw_pre NULL)  */
+  int32_t gate_fn;      /* FCP_GATE_*: the gate's value is taken as it is, or through the sigmoid  */
+  float eps;            /* added to the mean squares, >= 0                                         */
+  float res_scale;      /* of the residual before the block                                        */
+  float branch_scale;   /* of the block's output                                                   */
+  int32_t res_dtype;    /* FCP_OUT_BF16 or FCP_OUT_F32: x, x_out and their gradients               */
+  int32_t w_dtype;      /* of w_post and w_pre                                                     */
+  int32_t add_dw;       /* gradient: 1 adds to dw_post and dw_pre, 0 writes them                   */
+} fcp_res_norm;
+
+/*
+ * fcp_residual_norm -- the residual stream between two blocks of a layer (an
+ * attention and a feed-forward, say): the norm behind a block, its gate, the
+ * scaled sum with the residual and the norm before the next block, one pass. For
+ * every token of the shard (of all shards for shard == -1), rows of n values:
+ *   u     = y / sqrt(mean(y^2) + eps) * w_post     (post_norm = 0: y * w_post)
+ *   x_out = res_scale x + branch_scale g(gate) u   (no gate: g = 1)
+ *   h     = x_out / sqrt(mean(x_out^2) + eps) * w_pre
+ * in fp32; x_out and h are rounded once, h from x_out before its rounding.
+ *   x, x_out  rows of type res_dtype; y, gate, h bf16. Row t at t * stride
+ *             elements: strides multiples of 8 and at least n (slices of wider
+ *             tensors, for instance). Written only at the shard's rows. x_out
+ *             may be x itself (same stride); no other overlap of an output.
+ *   y         NULL: no block before (gate and w_post NULL too); then x_out may
+ *             be NULL where res_scale is 1.
+ *   gate, w_post, w_pre  may be NULL (no gate, weights of ones); weights [n].
+ *   n         a multiple of 8, 8 .. 16384.
+ * Errors, before any launch: FCP_ERR_INVALID_ARG (also an overlap),
+ * FCP_ERR_UNSUPPORTED (n). As fcp_qk_norm_rope, the call has no workspace: the
+ * checked build skips rows of a table entry out of range without a report.
+ */
+int fcp_residual_norm(const void* x, int64_t x_stride, const void* y, int64_t y_stride, const void* gate,
+                      int64_t gate_stride, const void* w_post, const void* w_pre, const fcp_res_norm* rn,
+                      const fcp_dev_plan* plan, int32_t shard, int32_t n, void* x_out, int64_t x_out_stride, void* h,
+                      int64_t h_stride, void* stream);
+
+/* Workspace of fcp_residual_norm_bwd for rows of n values, in bytes (0 for an n
+ * that it does not take). It may hold anything. */
+int64_t fcp_residual_norm_ws_bytes(int32_t n);
+
+/*
+ * fcp_residual_norm_bwd -- gradient of fcp_residual_norm. With D the gradient of
+ * x_out (dx_out and what comes through h):
+ *   k = dh w_pre, r = 1 / sqrt(mean(x_out^2) + eps):  D = dx_out + r (k - x_out r^2 mean(k x_out)),
+ *   dx = res_scale D,  dgate = branch_scale D u g'(gate),
+ *   e = branch_scale D g(gate) w_post, r_y = 1 / sqrt(mean(y^2) + eps):
+ *   dy = r_y (e - y r_y^2 mean(e y))               (post_norm = 0: e),
+ *   dw_pre = sum of dh x_out r,  dw_post = sum of branch_scale D g(gate) y r_y,
+ * the sums over the shard's tokens.
+ *   dh        bf16 (NULL for pre_norm = 0); dx_out of type res_dtype, or NULL:
+ *             no gradient along the residual; one of both at least.
+ *   x_out     the forward's, as stored (may be NULL for pre_norm = 0); y, gate,
+ *             w_post, w_pre as in the forward.
+ *   dx        type res_dtype; may be dx_out itself (same stride). dy, dgate bf16
+ *             (NULL where y, gate are); dy may be y, dgate the gate (same
+ *             strides). No other overlap of an output. Strides as above.
+ *   dw_post, dw_pre  fp32 [n] or NULL, written (add_dw = 0) or accumulated;
+ *             summed in a fixed order: equal inputs give equal bits.
+ *             dw_post needs y, dw_pre needs pre_norm.
+ *   ws        fcp_residual_norm_ws_bytes(n) bytes, 16-byte aligned (needed for
+ *             dw_post or dw_pre); calls that may run at once need one each.
+ * Errors as fcp_residual_norm; FCP_ERR_CAPACITY if the workspace is too small.
+ */
+int fcp_residual_norm_bwd(const void* dh, int64_t dh_stride, const void* dx_out, int64_t dx_out_stride, const void* x_out,
+                          int64_t x_out_stride, const void* y, int64_t y_stride, const void* gate, int64_t gate_stride,
+                          const void* w_post, const void* w_pre, const fcp_res_norm* rn, const fcp_dev_plan* plan,
+                          int32_t shard, int32_t n, void* dx, int64_t dx_stride, void* dy, int64_t dy_stride, void* dgate,
+                          int64_t dgate_stride, float* dw_post, float* dw_pre, void* ws, int64_t ws_bytes, void* stream);
+
 /* Size of the device array that fcp_attn_fwd_noalloc uses as its scratch. */
 #define FCP_NOALLOC_SCRATCH_BYTES (64u * 1024u * 1024u)
 
