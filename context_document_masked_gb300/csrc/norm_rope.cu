@@ -53,20 +53,6 @@ constexpr int kE = 8;  // values of a head in a lane
 // take (a few spilled ones cost the gradient a quarter of its speed).
 constexpr int kFwdPasses = 4, kFwdCtas = 4, kBwdPasses = 4, kBwdCtas = 2;
 
-// Bf16 pairs as fp32 pairs, and back.
-__device__ __forceinline__ uint64_t unpack2(uint32_t v) {
-  return f2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t pack2(uint64_t x) {
-  float lo, hi;
-  f2_split(x, lo, hi);
-  return pack_bf16(lo, hi);
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float f2_sum(uint64_t a, uint64_t b) {
   float lo, hi;
   f2_split(f2_add(a, b), lo, hi);

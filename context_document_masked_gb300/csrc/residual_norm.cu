@@ -34,78 +34,173 @@ namespace {
 constexpr int kV = 8;  // values of a group: 16 bytes of bf16
 constexpr int kMaxWarps = 32;
 
-// Groups a thread holds, and threads a row: one group up to 2048 values, two
+// Groups a thread holds, and threads a row: one group up to 1024 values, two
 // above (16384 values: 1024 threads).
-__host__ __device__ constexpr int groups_of(int n) { return n <= 2048 ? 1 : 2; }
+__host__ __device__ constexpr int groups_of(int n) { return n <= 1024 ? 1 : 2; }
 __host__ __device__ constexpr int threads_of(int n) { return (n / kV + 32 * groups_of(n) - 1) / (32 * groups_of(n)) * 32; }
 int most_ctas(int n) { return std::min(kResNormMaxCtas, 152 * 1024 / threads_of(n)); }
 
-__device__ __forceinline__ void load8(const void* row, bool f32, int i, float (&v)[kV]) {
-  if (f32) {
-    const float4 a = reinterpret_cast<const float4*>(row)[2 * i], b = reinterpret_cast<const float4*>(row)[2 * i + 1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 a = reinterpret_cast<const uint4*>(row)[i];
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// The arithmetic runs on pairs of values (f32x2): with one value an instruction
+// its issue bound the kernels, not memory. A group is four pairs.
+struct Pairs {
+  uint64_t v[4];
+};
+__device__ __forceinline__ uint64_t both(float x) { return f2(x, x); }
+
+// A group as it lies in memory: what a row's loads in flight take of the
+// registers, and pairs of fp32 from there.
+template <bool F32>
+struct Raw {
+  uint4 v[F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* row, int i) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[2 * j] = __uint_as_float(w[j] << 16), v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    for (int j = 0; j < (F32 ? 2 : 1); ++j) v[j] = __ldcs(reinterpret_cast<const uint4*>(row) + (F32 ? 2 * i + j : i));
+  }
+  // The same from a thread's place in shared memory (words `step` apart).
+  __device__ __forceinline__ void take(const uint4* place, int step) {
+#pragma unroll
+    for (int j = 0; j < (F32 ? 2 : 1); ++j) v[j] = place[j * step];
+  }
+  static __device__ __forceinline__ void fetch(uint4* place, int step, const void* row, int i) {
+#pragma unroll
+    for (int j = 0; j < (F32 ? 2 : 1); ++j)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(place + j * step)),
+                   "l"(reinterpret_cast<const uint4*>(row) + (F32 ? 2 * i + j : i))
+                   : "memory");
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < (F32 ? 2 : 1); ++j) v[j] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ uint64_t pair(int j) const {
+    if constexpr (F32) {
+      const uint4 q = v[j >> 1];
+      return j & 1 ? f2(__uint_as_float(q.z), __uint_as_float(q.w)) : f2(__uint_as_float(q.x), __uint_as_float(q.y));
+    } else {
+      return unpack2(j == 0 ? v[0].x : j == 1 ? v[0].y : j == 2 ? v[0].z : v[0].w);
+    }
+  }
+};
+template <bool F32>
+__device__ __forceinline__ void store8(void* row, int i, const Pairs& x) {
+  if constexpr (F32) {
+    float a[kV];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f2_split(x.v[j], a[2 * j], a[2 * j + 1]);
+    __stcs(reinterpret_cast<float4*>(row) + 2 * i, make_float4(a[0], a[1], a[2], a[3]));
+    __stcs(reinterpret_cast<float4*>(row) + 2 * i + 1, make_float4(a[4], a[5], a[6], a[7]));
+  } else {
+    __stcs(reinterpret_cast<uint4*>(row) + i, make_uint4(pack2(x.v[0]), pack2(x.v[1]), pack2(x.v[2]), pack2(x.v[3])));
   }
 }
-__device__ __forceinline__ void store8(void* row, bool f32, int i, const float (&v)[kV]) {
-  if (f32) {
-    reinterpret_cast<float4*>(row)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(row)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    reinterpret_cast<uint4*>(row)[i] =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  }
-}
-// Weights of group i; ones without.
-__device__ __forceinline__ void load_w(const void* w, bool f32, int i, float (&v)[kV]) {
-  if (w) {
-    load8(w, f32, i, v);
-  } else {
+// Weights of group i (in L1 after a CTA's first row); ones without.
+__device__ __forceinline__ Pairs load_w(const void* w, bool f32, int i) {
+  Pairs r;
+  if (!w) {
 #pragma unroll
-    for (int e = 0; e < kV; ++e) v[e] = 1.f;
+    for (int j = 0; j < 4; ++j) r.v[j] = both(1.f);
+  } else if (f32) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(w) + 2 * i), b = __ldg(reinterpret_cast<const float4*>(w) + 2 * i + 1);
+    r.v[0] = f2(a.x, a.y), r.v[1] = f2(a.z, a.w), r.v[2] = f2(b.x, b.y), r.v[3] = f2(b.z, b.w);
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(w) + i);
+    r.v[0] = unpack2(a.x), r.v[1] = unpack2(a.y), r.v[2] = unpack2(a.z), r.v[3] = unpack2(a.w);
   }
+  return r;
+}
+__device__ __forceinline__ float sum_of(uint64_t a) {
+  float lo, hi;
+  f2_split(a, lo, hi);
+  return lo + hi;
 }
 
-// Sums of K values over the CTA's threads (every thread gets them). `sh` is not
-// read any more when the next call's values arrive in the other half.
-template <int K>
-__device__ __forceinline__ void row_sums(float (&v)[K], float (*sh)[kMaxWarps], int& half) {
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int m = 16; m; m >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], m);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return;
-  float(*s)[kMaxWarps] = sh + 4 * half;
-  half ^= 1;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int k = 0; k < K; ++k) s[k][threadIdx.x >> 5] = v[k];
+// Sums of one, or of four values at once, over the CTA's threads (every thread
+// gets them). Four: after two exchanges a lane holds one of the values, so they
+// take 6 shuffles, not 20. A half is not read any more when the call after the next
+// one's values arrive there.
+struct Sums {
+  float4 four[2][kMaxWarps];
+  float one[2][kMaxWarps];  // (zeros in the places of warps that there are not)
+};
+__device__ __forceinline__ void init(Sums& sh) {
+  for (int i = threadIdx.x; i < 2 * kMaxWarps; i += blockDim.x) sh.one[i / kMaxWarps][i % kMaxWarps] = 0.f;
   __syncthreads();
+}
+__device__ __forceinline__ float shuffled(float v, int m) { return v + __shfl_xor_sync(0xffffffffu, v, m); }
+__device__ __forceinline__ float row_sum(float v, Sums& sh, int& half) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    float t = 0.f;
-    for (int w = 0; w < warps; ++w) t += s[k][w];
-    v[k] = t;
+  for (int m = 16; m; m >>= 1) v = shuffled(v, m);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  float* s = sh.one[half];
+  half ^= 1;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int w = 0; w < warps; w += 4) {
+    const float4 a = *reinterpret_cast<const float4*>(s + w);
+    v += (a.x + a.y) + (a.z + a.w);
   }
+  return v;
+}
+__device__ __forceinline__ float4 row_sums(float4 v, Sums& sh, int& half) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1, second = lane & 2;
+  // Even lanes keep the sums of x and y, odd ones those of z and w; then one each.
+  const float a = (odd ? v.z : v.x) + __shfl_xor_sync(0xffffffffu, odd ? v.x : v.z, 1);
+  const float b = (odd ? v.w : v.y) + __shfl_xor_sync(0xffffffffu, odd ? v.y : v.w, 1);
+  float t = (second ? b : a) + __shfl_xor_sync(0xffffffffu, second ? a : b, 2);
+#pragma unroll
+  for (int m = 4; m < 32; m <<= 1) t = shuffled(t, m);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1)  // lane 0 holds x's sum, 1 z's, 2 y's, 3 w's
+    return make_float4(__shfl_sync(0xffffffffu, t, 0), __shfl_sync(0xffffffffu, t, 2), __shfl_sync(0xffffffffu, t, 1),
+                       __shfl_sync(0xffffffffu, t, 3));
+  float4* s = sh.four[half];
+  half ^= 1;
+  if (lane < 4) reinterpret_cast<float*>(s + (threadIdx.x >> 5))[(lane >> 1) | (lane & 1) << 1] = t;
+  __syncthreads();
+  float4 r = s[0];
+  for (int w = 1; w < warps; ++w) {
+    const float4 o = s[w];
+    r = make_float4(r.x + o.x, r.y + o.y, r.z + o.z, r.w + o.w);
+  }
+  return r;
 }
 
-// g(z) and g'(z); the sigmoid and its derivative without a loss of bits at
-// either end (e = exp(-|z|) is at most 1).
-__device__ __forceinline__ void gate_of(int fn, float z, float& g, float& dg) {
-  if (fn == FCP_GATE_SIGMOID) {
-    const float e = __expf(-fabsf(z)), d = __fdividef(1.f, 1.f + e);
-    g = z >= 0.f ? d : e * d;
-    dg = e * d * d;
-  } else {
-    g = z;
-    dg = 1.f;
-  }
+// g(z) and g'(z) = g (1 - g) for the sigmoid, as e g g, which keeps its bits where
+// g is near 1; e is cut below infinity, where it would meet g = 0. (min.NaN: a
+// NaN stays one.)
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
+__device__ __forceinline__ uint64_t gate_of(int fn, uint64_t z) {
+  if (fn != FCP_GATE_SIGMOID) return z;
+  float a, b;
+  f2_split(f2_mul(z, both(-1.4426950408889634f)), a, b);
+  return f2(rcp(1.f + ex2(a)), rcp(1.f + ex2(b)));
+}
+__device__ __forceinline__ void gate_of(int fn, uint64_t z, uint64_t& g, uint64_t& dg) {
+  if (fn != FCP_GATE_SIGMOID) {
+    g = z;
+    dg = both(1.f);
+    return;
+  }
+  float a, b;
+  f2_split(f2_mul(z, both(-1.4426950408889634f)), a, b);
+  asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(a));  // 126
+  asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(b));
+  const uint64_t e = f2(ex2(a), ex2(b));
+  f2_split(f2_add(e, both(1.f)), a, b);
+  g = f2(rcp(a), rcp(b));
+  dg = f2_mul(f2_mul(e, g), g);
+}
+
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Row k of the launch: a token, or -1 for a place past a chunk's end. Chunks are
 // runs of at most kResNormChunk rows of a shard; none for all tokens in order.
@@ -119,6 +214,19 @@ __device__ __forceinline__ int64_t row_at(const ResNormParams& p, int64_t k) {
   return r < n ? first + r : -1;
 }
 
+// The first place from k on, in steps of the grid, that holds a token: the
+// token, or -1 at the end.
+__device__ __forceinline__ int64_t next_row(const ResNormParams& p, int64_t& k) {
+  for (; k < p.places; k += gridDim.x) {
+    const int64_t t = row_at(p, k);
+    if (t >= 0) {
+      k += gridDim.x;
+      return t;
+    }
+  }
+  return -1;
+}
+
 __device__ __forceinline__ const char* at(const void* base, int64_t row_bytes, int64_t t) {
   return static_cast<const char*>(base) + row_bytes * t;
 }
@@ -126,162 +234,240 @@ __device__ __forceinline__ char* at(void* base, int64_t row_bytes, int64_t t) {
   return static_cast<char*>(base) + row_bytes * t;
 }
 
-template <int G>
-__global__ void __launch_bounds__(1024) res_norm_kernel(const ResNormParams p) {
-  __shared__ float sh[8][kMaxWarps];
-  int half = 0;
+// A thread's groups of one row, c of them, `kWords` words of 16 bytes each, in a
+// stage of the ring in shared memory; the words of neighbouring threads are
+// neighbours. Only the thread itself reads what it fetched.
+constexpr int kFwdWords[2] = {3, 4}, kBwdWords[2] = {5, 7};  // bf16, fp32 residual
+
+template <int G, int THREADS, int CTAS, bool F32, bool RING>
+__global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormParams p) {
+  extern __shared__ uint4 ring[];
+  __shared__ __align__(16) Sums sh;
+  init(sh);
+  constexpr int kWords = kFwdWords[F32];
+  const int step = blockDim.x;
+  int half = 0, stage = 0;
   const float inv_n = 1.f / p.n;
-  for (int64_t k = blockIdx.x; k < p.places; k += gridDim.x) {
-    const int64_t t = row_at(p, k);
-    if (t < 0) continue;
-    float x[G][kV], y[G][kV];
-    float sum[1] = {0.f};
+  int64_t k = blockIdx.x;
+  auto place = [&](int st, int c) { return ring + (st * G + c) * kWords * step + threadIdx.x; };
+  auto fetch = [&](int st, int64_t t) {
+    if constexpr (RING) {
+#pragma unroll
+      for (int c = 0; c < G; ++c) {
+        const int i = threadIdx.x + c * step;
+        if (t < 0 || i >= p.groups) continue;
+        uint4* at_c = place(st, c);
+        if (p.y) Raw<false>::fetch(at_c, step, at(p.y, p.y_row, t), i);
+        if (p.gate) Raw<false>::fetch(at_c + step, step, at(p.gate, p.gate_row, t), i);
+        Raw<F32>::fetch(at_c + 2 * step, step, at(p.x, p.x_row, t), i);
+      }
+      async_commit();
+    }
+  };
+  int64_t t = next_row(p, k);
+  fetch(0, t);
+  for (int64_t next; t >= 0; t = next, stage ^= 1) {
+    next = next_row(p, k);
+    fetch(stage ^ 1, next);
+    Raw<F32> xr[G];
+    Raw<false> yr[G], zr[G];
+    if constexpr (RING) async_wait<1>();
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * blockDim.x;
-#pragma unroll
-      for (int e = 0; e < kV; ++e) x[c][e] = y[c][e] = 0.f;
-      if (i < p.groups) {
-        load8(at(p.x, p.x_row, t), p.res_f32, i, x[c]);
-        if (p.y) load8(at(p.y, p.y_row, t), false, i, y[c]);
+      const int i = threadIdx.x + c * step;
+      xr[c].zero(), yr[c].zero(), zr[c].zero();
+      if (i >= p.groups) continue;
+      if constexpr (RING) {
+        const uint4* at_c = place(stage, c);
+        if (p.y) yr[c].take(at_c, step);
+        if (p.gate) zr[c].take(at_c + step, step);
+        xr[c].take(at_c + 2 * step, step);
+      } else {
+        if (p.y) yr[c].load(at(p.y, p.y_row, t), i);
+        xr[c].load(at(p.x, p.x_row, t), i);
+        if (p.gate) zr[c].load(at(p.gate, p.gate_row, t), i);
       }
-#pragma unroll
-      for (int e = 0; e < kV; ++e) sum[0] += y[c][e] * y[c][e];
     }
     float ry = 1.f;
     if (p.y && p.post_norm) {
-      row_sums(sum, sh, half);
-      ry = rsqrtf(sum[0] * inv_n + p.eps);
+      uint64_t s2 = 0;
+#pragma unroll
+      for (int c = 0; c < G; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s2 = f2_fma(yr[c].pair(j), yr[c].pair(j), s2);
+      ry = rsqrtf(row_sum(sum_of(s2), sh, half) * inv_n + p.eps);
     }
-    sum[0] = 0.f;
+    const uint64_t a2 = both(p.res_scale), b2 = both(p.branch_scale * ry);
+    uint64_t s2 = 0;
+    Pairs x[G];
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * blockDim.x;
+      const int i = threadIdx.x + c * step;
       if (i >= p.groups) continue;
-      float w[kV], z[kV];
-      load_w(p.w_post, p.w_f32, i, w);
-      if (p.gate) load8(at(p.gate, p.gate_row, t), false, i, z);
+      if (p.y) {
+        const Pairs w = load_w(p.w_post, p.w_f32, i);
 #pragma unroll
-      for (int e = 0; e < kV; ++e) {
-        float g = 1.f, dg;
-        if (p.gate) gate_of(p.gate_fn, z[e], g, dg);
-        x[c][e] = p.res_scale * x[c][e] + (p.y ? p.branch_scale * g * (y[c][e] * ry * w[e]) : 0.f);
-        sum[0] += x[c][e] * x[c][e];
+        for (int j = 0; j < 4; ++j) {
+          uint64_t u = f2_mul(f2_mul(yr[c].pair(j), b2), w.v[j]);
+          if (p.gate) u = f2_mul(u, gate_of(p.gate_fn, zr[c].pair(j)));
+          x[c].v[j] = f2_fma(xr[c].pair(j), a2, u);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[c].v[j] = f2_mul(xr[c].pair(j), a2);
       }
-      if (p.x_out) store8(at(p.x_out, p.x_out_row, t), p.res_f32, i, x[c]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s2 = f2_fma(x[c].v[j], x[c].v[j], s2);
+      if (p.x_out) store8<F32>(at(p.x_out, p.x_out_row, t), i, x[c]);
     }
     if (!p.h) continue;
-    row_sums(sum, sh, half);
-    const float r = rsqrtf(sum[0] * inv_n + p.eps);
+    const uint64_t r2 = both(rsqrtf(row_sum(sum_of(s2), sh, half) * inv_n + p.eps));
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * blockDim.x;
+      const int i = threadIdx.x + c * step;
       if (i >= p.groups) continue;
-      float w[kV];
-      load_w(p.w_pre, p.w_f32, i, w);
+      Pairs w = load_w(p.w_pre, p.w_f32, i);
 #pragma unroll
-      for (int e = 0; e < kV; ++e) w[e] *= x[c][e] * r;
-      store8(at(p.h, p.h_row, t), false, i, w);
+      for (int j = 0; j < 4; ++j) w.v[j] = f2_mul(f2_mul(x[c].v[j], r2), w.v[j]);
+      store8<false>(at(p.h, p.h_row, t), i, w);
     }
   }
 }
 
-template <int G>
-__global__ void __launch_bounds__(1024) res_norm_bwd_kernel(const ResNormParams p) {
-  __shared__ float sh[8][kMaxWarps];
-  int half = 0;
+template <int G, int THREADS, int CTAS, bool F32, bool RING>
+__global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNormParams p) {
+  extern __shared__ uint4 ring[];
+  __shared__ __align__(16) Sums sh;
+  init(sh);
+  constexpr int kWords = kBwdWords[F32], kRes = F32 ? 2 : 1;
+  const int step = blockDim.x;
+  int half = 0, half4 = 0, stage = 0;
   const float inv_n = 1.f / p.n;
-  float acc_pre[G][kV], acc_post[G][kV];
+  Pairs acc_pre[G], acc_post[G];
 #pragma unroll
   for (int c = 0; c < G; ++c)
 #pragma unroll
-    for (int e = 0; e < kV; ++e) acc_pre[c][e] = acc_post[c][e] = 0.f;
-  for (int64_t k = blockIdx.x; k < p.places; k += gridDim.x) {
-    const int64_t t = row_at(p, k);
-    if (t < 0) continue;
-    float x[G][kV], dh[G][kV], y[G][kV];
-    float sum[3] = {0.f, 0.f, 0.f};  // X^2, k X, y^2
+    for (int j = 0; j < 4; ++j) acc_pre[c].v[j] = acc_post[c].v[j] = 0;
+  int64_t k = blockIdx.x;
+  auto place = [&](int st, int c) { return ring + (st * G + c) * kWords * step + threadIdx.x; };
+  auto fetch = [&](int st, int64_t t) {
+    if constexpr (RING) {
+#pragma unroll
+      for (int c = 0; c < G; ++c) {
+        const int i = threadIdx.x + c * step;
+        if (t < 0 || i >= p.groups) continue;
+        uint4* at_c = place(st, c);
+        if (p.dh) {
+          Raw<false>::fetch(at_c, step, at(p.dh, p.dh_row, t), i);
+          Raw<F32>::fetch(at_c + 3 * step, step, at(p.x, p.x_row, t), i);
+        }
+        if (p.y) Raw<false>::fetch(at_c + step, step, at(p.y, p.y_row, t), i);
+        if (p.gate) Raw<false>::fetch(at_c + 2 * step, step, at(p.gate, p.gate_row, t), i);
+        if (p.dx_out) Raw<F32>::fetch(at_c + (3 + kRes) * step, step, at(p.dx_out, p.dx_out_row, t), i);
+      }
+      async_commit();
+    }
+  };
+  int64_t t = next_row(p, k);
+  fetch(0, t);
+  for (int64_t next; t >= 0; t = next, stage ^= 1) {
+    next = next_row(p, k);
+    fetch(stage ^ 1, next);
+    Raw<F32> xr[G], dr[G];
+    Raw<false> hr[G], yr[G], zr[G];
+    if constexpr (RING) async_wait<1>();
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * blockDim.x;
-#pragma unroll
-      for (int e = 0; e < kV; ++e) x[c][e] = dh[c][e] = y[c][e] = 0.f;
-      if (i < p.groups) {
-        float w[kV];
+      const int i = threadIdx.x + c * step;
+      xr[c].zero(), hr[c].zero(), yr[c].zero(), dr[c].zero(), zr[c].zero();
+      if (i >= p.groups) continue;
+      if constexpr (RING) {
+        const uint4* at_c = place(stage, c);
         if (p.dh) {
-          load8(at(p.x, p.x_row, t), p.res_f32, i, x[c]);
-          load8(at(p.dh, p.dh_row, t), false, i, dh[c]);
-          load_w(p.w_pre, p.w_f32, i, w);
-#pragma unroll
-          for (int e = 0; e < kV; ++e) {
-            sum[0] += x[c][e] * x[c][e];
-            sum[1] += dh[c][e] * w[e] * x[c][e];
-          }
+          hr[c].take(at_c, step);
+          xr[c].take(at_c + 3 * step, step);
         }
-        if (p.y) load8(at(p.y, p.y_row, t), false, i, y[c]);
-#pragma unroll
-        for (int e = 0; e < kV; ++e) sum[2] += y[c][e] * y[c][e];
+        if (p.y) yr[c].take(at_c + step, step);
+      } else {
+        if (p.dh) {
+          xr[c].load(at(p.x, p.x_row, t), i);
+          hr[c].load(at(p.dh, p.dh_row, t), i);
+        }
+        if (p.y) yr[c].load(at(p.y, p.y_row, t), i);
+        if (p.dx_out) dr[c].load(at(p.dx_out, p.dx_out_row, t), i);
+        if (p.gate) zr[c].load(at(p.gate, p.gate_row, t), i);
       }
     }
-    row_sums(sum, sh, half);
-    const float r = p.dh ? rsqrtf(sum[0] * inv_n + p.eps) : 0.f;
-    const float m = r * (r * r * (sum[1] * inv_n));
-    const float ry = p.post_norm && p.y ? rsqrtf(sum[2] * inv_n + p.eps) : 1.f;
-    float ey[1] = {0.f};
-    // dh becomes e.
+    uint64_t xx = 0, kx = 0, yy = 0;
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * blockDim.x;
+      const int i = threadIdx.x + c * step;
+      const Pairs w = i < p.groups ? load_w(p.w_pre, p.w_f32, i) : load_w(nullptr, false, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t x = xr[c].pair(j), y = yr[c].pair(j);
+        xx = f2_fma(x, x, xx);
+        kx = f2_fma(f2_mul(hr[c].pair(j), x), w.v[j], kx);
+        yy = f2_fma(y, y, yy);
+      }
+    }
+    const float4 sums = row_sums(make_float4(sum_of(xx), sum_of(kx), sum_of(yy), 0.f), sh, half4);
+    const float r = p.dh ? rsqrtf(sums.x * inv_n + p.eps) : 0.f;
+    const float ry = p.post_norm && p.y ? rsqrtf(sums.z * inv_n + p.eps) : 1.f;
+    const uint64_t r2 = both(r), nm2 = both(-r * (r * r * (sums.y * inv_n))), ry2 = both(ry);
+    uint64_t ey = 0;
+    Pairs ee[G];  // e
+#pragma unroll
+    for (int c = 0; c < G; ++c) {
+      const int i = threadIdx.x + c * step;
       if (i >= p.groups) continue;
-      float w[kV], d[kV], z[kV], dz[kV];
-      load_w(p.w_pre, p.w_f32, i, w);
-#pragma unroll
-      for (int e = 0; e < kV; ++e) d[e] = 0.f;
-      if (p.dx_out) load8(at(p.dx_out, p.dx_out_row, t), p.res_f32, i, d);
-#pragma unroll
-      for (int e = 0; e < kV; ++e) {
-        acc_pre[c][e] += dh[c][e] * x[c][e] * r;
-        d[e] += r * (dh[c][e] * w[e]) - x[c][e] * m;
-        z[e] = p.res_scale * d[e];
+      Pairs w = load_w(p.w_pre, p.w_f32, i), out;
+      if constexpr (RING) {  // what the sums did not need stayed in shared memory till now
+        const uint4* at_c = place(stage, c);
+        if (p.gate) zr[c].take(at_c + 2 * step, step);
+        if (p.dx_out) dr[c].take(at_c + (3 + kRes) * step, step);
       }
-      store8(at(p.dx, p.dx_row, t), p.res_f32, i, z);
+      Pairs d;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t x = xr[c].pair(j), h = hr[c].pair(j);
+        acc_pre[c].v[j] = f2_fma(f2_mul(h, x), r2, acc_pre[c].v[j]);
+        d.v[j] = f2_fma(x, nm2, f2_fma(f2_mul(h, w.v[j]), r2, dr[c].pair(j)));
+        out.v[j] = f2_mul(d.v[j], both(p.res_scale));
+      }
+      store8<F32>(at(p.dx, p.dx_row, t), i, out);
       if (!p.y) continue;
-      load_w(p.w_post, p.w_f32, i, w);
-      if (p.gate) load8(at(p.gate, p.gate_row, t), false, i, z);
+      w = load_w(p.w_post, p.w_f32, i);
 #pragma unroll
-      for (int e = 0; e < kV; ++e) {
-        float g = 1.f, dg = 0.f;
-        if (p.gate) gate_of(p.gate_fn, z[e], g, dg);
-        const float cd = p.branch_scale * d[e], u = y[c][e] * ry;
-        dz[e] = cd * (u * w[e]) * dg;
-        acc_post[c][e] += cd * g * u;
-        dh[c][e] = cd * g * w[e];
-        ey[0] += dh[c][e] * y[c][e];
+      for (int j = 0; j < 4; ++j) {
+        uint64_t g = both(1.f), dg = 0;
+        if (p.gate) gate_of(p.gate_fn, zr[c].pair(j), g, dg);
+        const uint64_t y = yr[c].pair(j), cd = f2_mul(d.v[j], both(p.branch_scale)), cu = f2_mul(cd, f2_mul(y, ry2));
+        out.v[j] = f2_mul(f2_mul(cu, w.v[j]), dg);
+        acc_post[c].v[j] = f2_fma(cu, g, acc_post[c].v[j]);
+        ee[c].v[j] = f2_mul(f2_mul(cd, w.v[j]), g);
+        ey = f2_fma(ee[c].v[j], y, ey);
       }
-      if (p.gate) store8(at(p.dgate, p.dgate_row, t), false, i, dz);
+      if (p.gate) store8<false>(at(p.dgate, p.dgate_row, t), i, out);
     }
     if (!p.y) continue;
-    float my = 0.f;
-    if (p.post_norm) {
-      row_sums(ey, sh, half);
-      my = ry * (ry * ry * (ey[0] * inv_n));
-    }
+    const float my = p.post_norm ? ry * (ry * ry * (row_sum(sum_of(ey), sh, half) * inv_n)) : 0.f;
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * blockDim.x;
+      const int i = threadIdx.x + c * step;
       if (i >= p.groups) continue;
 #pragma unroll
-      for (int e = 0; e < kV; ++e) y[c][e] = ry * dh[c][e] - y[c][e] * my;
-      store8(at(p.dy, p.dy_row, t), false, i, y[c]);
+      for (int j = 0; j < 4; ++j) ee[c].v[j] = f2_fma(yr[c].pair(j), both(-my), f2_mul(ee[c].v[j], ry2));
+      store8<false>(at(p.dy, p.dy_row, t), i, ee[c]);
     }
   }
   float* part = p.partial + (size_t)blockIdx.x * 2 * p.n;
 #pragma unroll
   for (int c = 0; c < G; ++c) {
-    const int i = threadIdx.x + c * blockDim.x;
+    const int i = threadIdx.x + c * step;
     if (i >= p.groups) continue;
-    if (p.dw_post) store8(part, true, i, acc_post[c]);
-    if (p.dw_pre) store8(part + p.n, true, i, acc_pre[c]);
+    if (p.dw_post) store8<true>(part, i, acc_post[c]);
+    if (p.dw_pre) store8<true>(part + p.n, i, acc_pre[c]);
   }
 }
 
@@ -314,14 +500,45 @@ __global__ void __launch_bounds__(32 * kSumWarps) res_norm_dw_kernel(const float
 
 int64_t res_norm_ws_bytes(int n) { return (int64_t)most_ctas(n) * 2 * n * sizeof(float); }
 
+// A ring of two rows in shared memory where CTAS CTAs of an SM have the room.
+constexpr int kRingBytes = 220 * 1024;
+template <class Kernel>
+static bool go(Kernel ring, Kernel direct, int words, int ctas, int groups, const ResNormParams& p, int grid, int threads,
+               cudaStream_t st) {
+  const int bytes = 2 * groups * words * threads * 16;
+  if (bytes > kRingBytes / ctas) {
+    direct<<<grid, threads, 0, st>>>(p);
+    return true;
+  }
+  if (bytes > 40 * 1024 && cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  ring<<<grid, threads, bytes, st>>>(p);
+  return true;
+}
+template <int G, int THREADS, int FWD_CTAS, int BWD_CTAS>
+static bool go(const ResNormParams& p, int grid, int threads, cudaStream_t st) {
+  const int f = p.res_f32;
+  if (p.dx)
+    return f ? go(res_norm_bwd_kernel<G, THREADS, BWD_CTAS, true, true>, res_norm_bwd_kernel<G, THREADS, BWD_CTAS, true, false>,
+                  kBwdWords[f], BWD_CTAS, G, p, grid, threads, st)
+             : go(res_norm_bwd_kernel<G, THREADS, BWD_CTAS, false, true>, res_norm_bwd_kernel<G, THREADS, BWD_CTAS, false, false>,
+                  kBwdWords[f], BWD_CTAS, G, p, grid, threads, st);
+  return f ? go(res_norm_kernel<G, THREADS, FWD_CTAS, true, true>, res_norm_kernel<G, THREADS, FWD_CTAS, true, false>,
+                kFwdWords[f], FWD_CTAS, G, p, grid, threads, st)
+           : go(res_norm_kernel<G, THREADS, FWD_CTAS, false, true>, res_norm_kernel<G, THREADS, FWD_CTAS, false, false>,
+                kFwdWords[f], FWD_CTAS, G, p, grid, threads, st);
+}
+
 int launch_res_norm(const ResNormParams& a, cudaStream_t st) {
   ResNormParams p = a;
   p.groups = p.n / kV;
   const int threads = threads_of(p.n), grid = (int)std::min<int64_t>(p.places, most_ctas(p.n));
   if (grid > 0) {
-    const bool two = groups_of(p.n) == 2;
-    if (p.dx) two ? res_norm_bwd_kernel<2><<<grid, threads, 0, st>>>(p) : res_norm_bwd_kernel<1><<<grid, threads, 0, st>>>(p);
-    else two ? res_norm_kernel<2><<<grid, threads, 0, st>>>(p) : res_norm_kernel<1><<<grid, threads, 0, st>>>(p);
+    const bool ok = groups_of(p.n) == 1 ? go<1, 256, 4, 3>(p, grid, threads, st)
+                    : threads <= 256    ? go<2, 256, 4, 2>(p, grid, threads, st)
+                    : threads <= 512    ? go<2, 512, 2, 1>(p, grid, threads, st)
+                                        : go<2, 1024, 1, 1>(p, grid, threads, st);
+    if (!ok) return FCP_ERR_CUDA;
   }
   // (A shard without tokens: no rows, whose sum is written as zero.)
   if (p.dx && (p.dw_post || p.dw_pre))

@@ -409,6 +409,21 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// Bf16 pairs as fp32 pairs, and back.
+__device__ __forceinline__ uint64_t unpack2(uint32_t v) {
+  return f2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t x) {
+  float lo, hi;
+  f2_split(x, lo, hi);
+  return pack_bf16(lo, hi);
+}
+
 // (An atomicAdd through a pointer of unknown space brings code for shared
 // memory with it.)
 __device__ __forceinline__ void red_add(float* at, float v) {
