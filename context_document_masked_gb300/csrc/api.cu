@@ -997,6 +997,7 @@ static int res_norm_params(fcp::ResNormParams* p, const fcp_res_norm* rn, const 
   const Plan* host = plan->host;
   p->T = plan->T;
   p->n = n;
+  p->num_sms = num_sms();
   p->places = plan->T;
   if (shard >= 0) {
     const int32_t r0 = host_at(host, fcp::TB_RSHARD, shard), r1 = host_at(host, fcp::TB_RSHARD, shard + 1);

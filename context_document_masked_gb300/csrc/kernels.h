@@ -278,6 +278,7 @@ struct ResNormParams {
   int64_t dx_row, dy_row, dgate_row;
   float *dw_post, *dw_pre;
   float* partial;          // [res_norm_ws_bytes(n)]
+  int num_sms;
 };
 int64_t res_norm_ws_bytes(int n);
 int launch_res_norm(const ResNormParams& p, cudaStream_t st);

@@ -21,6 +21,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
+#include <type_traits>
 
 #include "kernels.h"
 #include "sm103.cuh"
@@ -34,11 +36,17 @@ namespace {
 constexpr int kV = 8;  // values of a group: 16 bytes of bf16
 constexpr int kMaxWarps = 32;
 
-// Groups a thread holds, and threads a row: one group up to 1024 values, two
-// above (16384 values: 1024 threads).
-__host__ __device__ constexpr int groups_of(int n) { return n <= 1024 ? 1 : 2; }
-__host__ __device__ constexpr int threads_of(int n) { return (n / kV + 32 * groups_of(n) - 1) / (32 * groups_of(n)) * 32; }
-int most_ctas(int n) { return std::min(kResNormMaxCtas, 152 * 1024 / threads_of(n)); }
+// Groups a thread holds. The forward: one up to 1024 values, two above (16384
+// values: 1024 threads). The gradient, whose instructions a row and thread count
+// for more: up to four.
+__host__ __device__ constexpr int groups_of(int n, bool bwd) {
+  return n <= 1024 ? 1 : bwd && n > 8192 ? 4 : 2;
+}
+__host__ __device__ constexpr int threads_of(int n, bool bwd) {
+  return (n / kV + 32 * groups_of(n, bwd) - 1) / (32 * groups_of(n, bwd)) * 32;
+}
+// CTAs of the gradient at most (each writes a row of the weights' sums).
+int most_ctas(int n) { return std::min(kResNormMaxCtas, 152 * 512 / threads_of(n, true)); }
 
 // The arithmetic runs on pairs of values (f32x2): with one value an instruction
 // its issue bound the kernels, not memory. A group is four pairs.
@@ -56,17 +64,42 @@ struct Raw {
 #pragma unroll
     for (int j = 0; j < (F32 ? 2 : 1); ++j) v[j] = __ldcs(reinterpret_cast<const uint4*>(row) + (F32 ? 2 * i + j : i));
   }
-  // The same from a thread's place in shared memory (words `step` apart).
-  __device__ __forceinline__ void take(const uint4* place, int step) {
-#pragma unroll
-    for (int j = 0; j < (F32 ? 2 : 1); ++j) v[j] = place[j * step];
+  // The same by way of shared memory, `place` this thread's word among its
+  // neighbours' (fp32: of two such runs of words). The two words of an fp32
+  // group are fetched by two lanes of the warp, so that a warp's fetch covers whole
+  // lines; i: the group, n: groups of a row.
+  static __device__ __forceinline__ void fetch(uint4* place, const void* row, int i, int n) {
+    const uint4* src = reinterpret_cast<const uint4*>(row) + i;
+    if constexpr (F32) {
+      const int lane = threadIdx.x & 31, block = (int)threadIdx.x - lane;
+      src += i - lane;  // word 2 (i - lane) + lane
+      place += block;   // words 2 block + lane and 32 on
+      if (2 * i - lane < 2 * n) copy(place, src);
+      if (2 * i - lane + 32 < 2 * n) copy(place + 32, src + 32);
+    } else if (i < n) {
+      copy(place, src);
+    }
   }
-  static __device__ __forceinline__ void fetch(uint4* place, int step, const void* row, int i) {
-#pragma unroll
-    for (int j = 0; j < (F32 ? 2 : 1); ++j)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(place + j * step)),
-                   "l"(reinterpret_cast<const uint4*>(row) + (F32 ? 2 * i + j : i))
-                   : "memory");
+  __device__ __forceinline__ void take(const uint4* place) {
+    if constexpr (F32) {
+      place += threadIdx.x;
+      v[0] = place[0];
+      v[1] = place[1];
+    } else {
+      v[0] = place[0];
+    }
+  }
+  // Zeros in the place of a group past the row's end, which no fetch covers: such
+  // threads compute with them and only do not store.
+  static __device__ __forceinline__ void clear(uint4* place) {
+    if constexpr (F32) {
+      place += threadIdx.x;
+      place[1] = make_uint4(0, 0, 0, 0);
+    }
+    place[0] = make_uint4(0, 0, 0, 0);
+  }
+  static __device__ __forceinline__ void copy(uint4* to, const uint4* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -94,12 +127,13 @@ __device__ __forceinline__ void store8(void* row, int i, const Pairs& x) {
   }
 }
 // Weights of group i (in L1 after a CTA's first row); ones without.
+template <bool THERE = false>
 __device__ __forceinline__ Pairs load_w(const void* w, bool f32, int i) {
   Pairs r;
-  if (!w) {
+  if (!THERE && !w) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) r.v[j] = both(1.f);
-  } else if (f32) {
+  } else if (THERE || f32) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(w) + 2 * i), b = __ldg(reinterpret_cast<const float4*>(w) + 2 * i + 1);
     r.v[0] = f2(a.x, a.y), r.v[1] = f2(a.z, a.w), r.v[2] = f2(b.x, b.y), r.v[3] = f2(b.z, b.w);
   } else {
@@ -176,26 +210,29 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ uint64_t gate_of(int fn, uint64_t z) {
-  if (fn != FCP_GATE_SIGMOID) return z;
+enum Gate { kNoGate, kPlainGate, kSigmoidGate };
+template <Gate GATE>
+__device__ __forceinline__ uint64_t gate_of(uint64_t z) {
+  if constexpr (GATE != kSigmoidGate) return z;
   float a, b;
   f2_split(f2_mul(z, both(-1.4426950408889634f)), a, b);
   return f2(rcp(1.f + ex2(a)), rcp(1.f + ex2(b)));
 }
-__device__ __forceinline__ void gate_of(int fn, uint64_t z, uint64_t& g, uint64_t& dg) {
-  if (fn != FCP_GATE_SIGMOID) {
+template <Gate GATE>
+__device__ __forceinline__ void gate_of(uint64_t z, uint64_t& g, uint64_t& dg) {
+  if constexpr (GATE != kSigmoidGate) {
     g = z;
     dg = both(1.f);
-    return;
+  } else {
+    float a, b;
+    f2_split(f2_mul(z, both(-1.4426950408889634f)), a, b);
+    asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(a));  // 126
+    asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(b));
+    const uint64_t e = f2(ex2(a), ex2(b));
+    f2_split(f2_add(e, both(1.f)), a, b);
+    g = f2(rcp(a), rcp(b));
+    dg = f2_mul(f2_mul(e, g), g);
   }
-  float a, b;
-  f2_split(f2_mul(z, both(-1.4426950408889634f)), a, b);
-  asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(a));  // 126
-  asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(b));
-  const uint64_t e = f2(ex2(a), ex2(b));
-  f2_split(f2_add(e, both(1.f)), a, b);
-  g = f2(rcp(a), rcp(b));
-  dg = f2_mul(f2_mul(e, g), g);
 }
 
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -236,10 +273,10 @@ __device__ __forceinline__ char* at(void* base, int64_t row_bytes, int64_t t) {
 
 // A thread's groups of one row, c of them, `kWords` words of 16 bytes each, in a
 // stage of the ring in shared memory; the words of neighbouring threads are
-// neighbours. Only the thread itself reads what it fetched.
+// neighbours. Only a warp's own lanes read what it fetched.
 constexpr int kFwdWords[2] = {3, 4}, kBwdWords[2] = {5, 7};  // bf16, fp32 residual
 
-template <int G, int THREADS, int CTAS, bool F32, bool RING>
+template <int G, int THREADS, int CTAS, bool RING, bool F32, Gate GATE>
 __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormParams p) {
   extern __shared__ uint4 ring[];
   __shared__ __align__(16) Sums sh;
@@ -255,37 +292,47 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormPa
 #pragma unroll
       for (int c = 0; c < G; ++c) {
         const int i = threadIdx.x + c * step;
-        if (t < 0 || i >= p.groups) continue;
+        if (t < 0) continue;
         uint4* at_c = place(st, c);
-        if (p.y) Raw<false>::fetch(at_c, step, at(p.y, p.y_row, t), i);
-        if (p.gate) Raw<false>::fetch(at_c + step, step, at(p.gate, p.gate_row, t), i);
-        Raw<F32>::fetch(at_c + 2 * step, step, at(p.x, p.x_row, t), i);
+        if (p.y) Raw<false>::fetch(at_c, at(p.y, p.y_row, t), i, p.groups);
+        if constexpr (GATE != kNoGate) Raw<false>::fetch(at_c + step, at(p.gate, p.gate_row, t), i, p.groups);
+        Raw<F32>::fetch(at_c + 2 * step, at(p.x, p.x_row, t), i, p.groups);
       }
       async_commit();
     }
   };
+  if constexpr (RING) {
+    for (int c = 0; c < G; ++c)
+      for (int st = 0; st < 2 && threadIdx.x + c * step >= p.groups; ++st) {
+        Raw<false>::clear(place(st, c));
+        Raw<false>::clear(place(st, c) + step);
+        Raw<F32>::clear(place(st, c) + 2 * step);
+      }
+  }
   int64_t t = next_row(p, k);
   fetch(0, t);
   for (int64_t next; t >= 0; t = next, stage ^= 1) {
     next = next_row(p, k);
+    if constexpr (RING && F32) __syncwarp();  // the lanes have read the last row
     fetch(stage ^ 1, next);
     Raw<F32> xr[G];
     Raw<false> yr[G], zr[G];
     if constexpr (RING) async_wait<1>();
+    if constexpr (RING && F32) __syncwarp();
 #pragma unroll
     for (int c = 0; c < G; ++c) {
       const int i = threadIdx.x + c * step;
       xr[c].zero(), yr[c].zero(), zr[c].zero();
-      if (i >= p.groups) continue;
+      if (!RING && i >= p.groups) continue;
       if constexpr (RING) {
         const uint4* at_c = place(stage, c);
-        if (p.y) yr[c].take(at_c, step);
-        if (p.gate) zr[c].take(at_c + step, step);
-        xr[c].take(at_c + 2 * step, step);
+        if (p.y) yr[c].take(at_c);
+        if constexpr (GATE != kNoGate) zr[c].take(at_c + step);
+        xr[c].take(at_c + 2 * step);
       } else {
         if (p.y) yr[c].load(at(p.y, p.y_row, t), i);
         xr[c].load(at(p.x, p.x_row, t), i);
-        if (p.gate) zr[c].load(at(p.gate, p.gate_row, t), i);
+        if constexpr (GATE != kNoGate) zr[c].load(at(p.gate, p.gate_row, t), i);
       }
     }
     float ry = 1.f;
@@ -303,13 +350,13 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormPa
 #pragma unroll
     for (int c = 0; c < G; ++c) {
       const int i = threadIdx.x + c * step;
-      if (i >= p.groups) continue;
+      const bool there = i < p.groups;
       if (p.y) {
-        const Pairs w = load_w(p.w_post, p.w_f32, i);
+        const Pairs w = load_w(p.w_post, p.w_f32, there ? i : 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           uint64_t u = f2_mul(f2_mul(yr[c].pair(j), b2), w.v[j]);
-          if (p.gate) u = f2_mul(u, gate_of(p.gate_fn, zr[c].pair(j)));
+          if constexpr (GATE != kNoGate) u = f2_mul(u, gate_of<GATE>(zr[c].pair(j)));
           x[c].v[j] = f2_fma(xr[c].pair(j), a2, u);
         }
       } else {
@@ -318,23 +365,25 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormPa
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2 = f2_fma(x[c].v[j], x[c].v[j], s2);
-      if (p.x_out) store8<F32>(at(p.x_out, p.x_out_row, t), i, x[c]);
+      if (p.x_out && there) store8<F32>(at(p.x_out, p.x_out_row, t), i, x[c]);
     }
     if (!p.h) continue;
     const uint64_t r2 = both(rsqrtf(row_sum(sum_of(s2), sh, half) * inv_n + p.eps));
 #pragma unroll
     for (int c = 0; c < G; ++c) {
       const int i = threadIdx.x + c * step;
-      if (i >= p.groups) continue;
-      Pairs w = load_w(p.w_pre, p.w_f32, i);
+      const bool there = i < p.groups;
+      Pairs w = load_w(p.w_pre, p.w_f32, there ? i : 0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) w.v[j] = f2_mul(f2_mul(x[c].v[j], r2), w.v[j]);
-      store8<false>(at(p.h, p.h_row, t), i, w);
+      if (there) store8<false>(at(p.h, p.h_row, t), i, w);
     }
   }
 }
 
-template <int G, int THREADS, int CTAS, bool F32, bool RING>
+// FULL: every operand but the gate is there and the weights are fp32, as in nearly
+// every call of a stack of layers: no branch for each group and operand.
+template <int G, int THREADS, int CTAS, bool RING, bool F32, Gate GATE, bool FULL>
 __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNormParams p) {
   extern __shared__ uint4 ring[];
   __shared__ __align__(16) Sums sh;
@@ -355,54 +404,63 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNo
 #pragma unroll
       for (int c = 0; c < G; ++c) {
         const int i = threadIdx.x + c * step;
-        if (t < 0 || i >= p.groups) continue;
+        if (t < 0) continue;
         uint4* at_c = place(st, c);
-        if (p.dh) {
-          Raw<false>::fetch(at_c, step, at(p.dh, p.dh_row, t), i);
-          Raw<F32>::fetch(at_c + 3 * step, step, at(p.x, p.x_row, t), i);
+        if (FULL || p.dh) {
+          Raw<false>::fetch(at_c, at(p.dh, p.dh_row, t), i, p.groups);
+          Raw<F32>::fetch(at_c + 3 * step, at(p.x, p.x_row, t), i, p.groups);
         }
-        if (p.y) Raw<false>::fetch(at_c + step, step, at(p.y, p.y_row, t), i);
-        if (p.gate) Raw<false>::fetch(at_c + 2 * step, step, at(p.gate, p.gate_row, t), i);
-        if (p.dx_out) Raw<F32>::fetch(at_c + (3 + kRes) * step, step, at(p.dx_out, p.dx_out_row, t), i);
+        if (FULL || p.y) Raw<false>::fetch(at_c + step, at(p.y, p.y_row, t), i, p.groups);
+        if constexpr (GATE != kNoGate) Raw<false>::fetch(at_c + 2 * step, at(p.gate, p.gate_row, t), i, p.groups);
+        if (FULL || p.dx_out) Raw<F32>::fetch(at_c + (3 + kRes) * step, at(p.dx_out, p.dx_out_row, t), i, p.groups);
       }
       async_commit();
     }
   };
+  if constexpr (RING) {
+    for (int c = 0; c < G; ++c)
+      for (int st = 0; st < 2 && threadIdx.x + c * step >= p.groups; ++st) {
+        for (int a = 0; a < 3; ++a) Raw<false>::clear(place(st, c) + a * step);
+        for (int a = 0; a < 2; ++a) Raw<F32>::clear(place(st, c) + (3 + a * kRes) * step);
+      }
+  }
   int64_t t = next_row(p, k);
   fetch(0, t);
   for (int64_t next; t >= 0; t = next, stage ^= 1) {
     next = next_row(p, k);
+    if constexpr (RING && F32) __syncwarp();  // the lanes have read the last row
     fetch(stage ^ 1, next);
     Raw<F32> xr[G], dr[G];
     Raw<false> hr[G], yr[G], zr[G];
     if constexpr (RING) async_wait<1>();
+    if constexpr (RING && F32) __syncwarp();
 #pragma unroll
     for (int c = 0; c < G; ++c) {
       const int i = threadIdx.x + c * step;
       xr[c].zero(), hr[c].zero(), yr[c].zero(), dr[c].zero(), zr[c].zero();
-      if (i >= p.groups) continue;
+      if (!RING && i >= p.groups) continue;
       if constexpr (RING) {
         const uint4* at_c = place(stage, c);
-        if (p.dh) {
-          hr[c].take(at_c, step);
-          xr[c].take(at_c + 3 * step, step);
+        if (FULL || p.dh) {
+          hr[c].take(at_c);
+          xr[c].take(at_c + 3 * step);
         }
-        if (p.y) yr[c].take(at_c + step, step);
+        if (FULL || p.y) yr[c].take(at_c + step);
       } else {
-        if (p.dh) {
+        if (FULL || p.dh) {
           xr[c].load(at(p.x, p.x_row, t), i);
           hr[c].load(at(p.dh, p.dh_row, t), i);
         }
-        if (p.y) yr[c].load(at(p.y, p.y_row, t), i);
-        if (p.dx_out) dr[c].load(at(p.dx_out, p.dx_out_row, t), i);
-        if (p.gate) zr[c].load(at(p.gate, p.gate_row, t), i);
+        if (FULL || p.y) yr[c].load(at(p.y, p.y_row, t), i);
+        if (FULL || p.dx_out) dr[c].load(at(p.dx_out, p.dx_out_row, t), i);
+        if constexpr (GATE != kNoGate) zr[c].load(at(p.gate, p.gate_row, t), i);
       }
     }
     uint64_t xx = 0, kx = 0, yy = 0;
 #pragma unroll
     for (int c = 0; c < G; ++c) {
       const int i = threadIdx.x + c * step;
-      const Pairs w = i < p.groups ? load_w(p.w_pre, p.w_f32, i) : load_w(nullptr, false, 0);
+      const Pairs w = load_w<FULL>(p.w_pre, p.w_f32, i < p.groups ? i : 0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint64_t x = xr[c].pair(j), y = yr[c].pair(j);
@@ -412,20 +470,20 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNo
       }
     }
     const float4 sums = row_sums(make_float4(sum_of(xx), sum_of(kx), sum_of(yy), 0.f), sh, half4);
-    const float r = p.dh ? rsqrtf(sums.x * inv_n + p.eps) : 0.f;
-    const float ry = p.post_norm && p.y ? rsqrtf(sums.z * inv_n + p.eps) : 1.f;
+    const float r = FULL || p.dh ? rsqrtf(sums.x * inv_n + p.eps) : 0.f;
+    const float ry = p.post_norm ? rsqrtf(sums.z * inv_n + p.eps) : 1.f;
     const uint64_t r2 = both(r), nm2 = both(-r * (r * r * (sums.y * inv_n))), ry2 = both(ry);
     uint64_t ey = 0;
     Pairs ee[G];  // e
 #pragma unroll
     for (int c = 0; c < G; ++c) {
       const int i = threadIdx.x + c * step;
-      if (i >= p.groups) continue;
-      Pairs w = load_w(p.w_pre, p.w_f32, i), out;
+      const bool there = i < p.groups;
+      Pairs w = load_w<FULL>(p.w_pre, p.w_f32, there ? i : 0), out;
       if constexpr (RING) {  // what the sums did not need stayed in shared memory till now
         const uint4* at_c = place(stage, c);
-        if (p.gate) zr[c].take(at_c + 2 * step, step);
-        if (p.dx_out) dr[c].take(at_c + (3 + kRes) * step, step);
+        if constexpr (GATE != kNoGate) zr[c].take(at_c + 2 * step);
+        if (FULL || p.dx_out) dr[c].take(at_c + (3 + kRes) * step);
       }
       Pairs d;
 #pragma unroll
@@ -435,30 +493,30 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNo
         d.v[j] = f2_fma(x, nm2, f2_fma(f2_mul(h, w.v[j]), r2, dr[c].pair(j)));
         out.v[j] = f2_mul(d.v[j], both(p.res_scale));
       }
-      store8<F32>(at(p.dx, p.dx_row, t), i, out);
-      if (!p.y) continue;
-      w = load_w(p.w_post, p.w_f32, i);
+      if (there) store8<F32>(at(p.dx, p.dx_row, t), i, out);
+      if (!FULL && !p.y) continue;
+      w = load_w<FULL>(p.w_post, p.w_f32, there ? i : 0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint64_t g = both(1.f), dg = 0;
-        if (p.gate) gate_of(p.gate_fn, zr[c].pair(j), g, dg);
+        if constexpr (GATE != kNoGate) gate_of<GATE>(zr[c].pair(j), g, dg);
         const uint64_t y = yr[c].pair(j), cd = f2_mul(d.v[j], both(p.branch_scale)), cu = f2_mul(cd, f2_mul(y, ry2));
-        out.v[j] = f2_mul(f2_mul(cu, w.v[j]), dg);
+        if constexpr (GATE != kNoGate) out.v[j] = f2_mul(f2_mul(cu, w.v[j]), dg);
         acc_post[c].v[j] = f2_fma(cu, g, acc_post[c].v[j]);
         ee[c].v[j] = f2_mul(f2_mul(cd, w.v[j]), g);
         ey = f2_fma(ee[c].v[j], y, ey);
       }
-      if (p.gate) store8<false>(at(p.dgate, p.dgate_row, t), i, out);
+      if constexpr (GATE != kNoGate)
+        if (there) store8<false>(at(p.dgate, p.dgate_row, t), i, out);
     }
-    if (!p.y) continue;
+    if (!FULL && !p.y) continue;
     const float my = p.post_norm ? ry * (ry * ry * (row_sum(sum_of(ey), sh, half) * inv_n)) : 0.f;
 #pragma unroll
     for (int c = 0; c < G; ++c) {
       const int i = threadIdx.x + c * step;
-      if (i >= p.groups) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) ee[c].v[j] = f2_fma(yr[c].pair(j), both(-my), f2_mul(ee[c].v[j], ry2));
-      store8<false>(at(p.dy, p.dy_row, t), i, ee[c]);
+      if (i < p.groups) store8<false>(at(p.dy, p.dy_row, t), i, ee[c]);
     }
   }
   float* part = p.partial + (size_t)blockIdx.x * 2 * p.n;
@@ -500,45 +558,59 @@ __global__ void __launch_bounds__(32 * kSumWarps) res_norm_dw_kernel(const float
 
 int64_t res_norm_ws_bytes(int n) { return (int64_t)most_ctas(n) * 2 * n * sizeof(float); }
 
-// A ring of two rows in shared memory where CTAS CTAs of an SM have the room.
-constexpr int kRingBytes = 220 * 1024;
+// Starts the kernel; its CTAs, or 0 for an error.
 template <class Kernel>
-static bool go(Kernel ring, Kernel direct, int words, int ctas, int groups, const ResNormParams& p, int grid, int threads,
-               cudaStream_t st) {
-  const int bytes = 2 * groups * words * threads * 16;
-  if (bytes > kRingBytes / ctas) {
-    direct<<<grid, threads, 0, st>>>(p);
-    return true;
-  }
-  if (bytes > 40 * 1024 && cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return false;
-  ring<<<grid, threads, bytes, st>>>(p);
-  return true;
+static int start(Kernel kernel, int bytes, int ctas, int most, int threads, const ResNormParams& p, cudaStream_t st) {
+  if (bytes > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return 0;
+  // As many CTAs as are resident at once: by registers, by shared memory, and 32 an SM.
+  const int fit = std::max(1, std::min({ctas, 227 * 1024 / (bytes + 2048), 32}));
+  const int grid = (int)std::min({p.places, (int64_t)fit * p.num_sms, (int64_t)most});
+  kernel<<<grid, threads, bytes, st>>>(p);
+  return grid;
 }
-template <int G, int THREADS, int FWD_CTAS, int BWD_CTAS>
-static bool go(const ResNormParams& p, int grid, int threads, cudaStream_t st) {
-  const int f = p.res_f32;
-  if (p.dx)
-    return f ? go(res_norm_bwd_kernel<G, THREADS, BWD_CTAS, true, true>, res_norm_bwd_kernel<G, THREADS, BWD_CTAS, true, false>,
-                  kBwdWords[f], BWD_CTAS, G, p, grid, threads, st)
-             : go(res_norm_bwd_kernel<G, THREADS, BWD_CTAS, false, true>, res_norm_bwd_kernel<G, THREADS, BWD_CTAS, false, false>,
-                  kBwdWords[f], BWD_CTAS, G, p, grid, threads, st);
-  return f ? go(res_norm_kernel<G, THREADS, FWD_CTAS, true, true>, res_norm_kernel<G, THREADS, FWD_CTAS, true, false>,
-                kFwdWords[f], FWD_CTAS, G, p, grid, threads, st)
-           : go(res_norm_kernel<G, THREADS, FWD_CTAS, false, true>, res_norm_kernel<G, THREADS, FWD_CTAS, false, false>,
-                kFwdWords[f], FWD_CTAS, G, p, grid, threads, st);
+// Rows that do not fit the shared memory twice come straight from memory (RING
+// false): more than 8192 values.
+template <int G, int THREADS, int CTAS, bool RING, bool F32, Gate GATE, bool BWD>
+static int start(const ResNormParams& p, cudaStream_t st) {
+  const int threads = threads_of(p.n, BWD), ctas = CTAS * THREADS / threads;
+  const int bytes = RING ? 2 * G * (BWD ? kBwdWords : kFwdWords)[F32] * threads * 16 : 0;
+  if constexpr (BWD) {
+    const bool full = p.dh && p.y && p.dx_out && p.w_pre && p.w_post && p.w_f32;
+    if constexpr (!RING) return start(res_norm_bwd_kernel<G, THREADS, CTAS, RING, F32, GATE, false>, bytes, ctas, most_ctas(p.n), threads, p, st);
+    else return full ? start(res_norm_bwd_kernel<G, THREADS, CTAS, RING, F32, GATE, true>, bytes, ctas, most_ctas(p.n), threads, p, st)
+                : start(res_norm_bwd_kernel<G, THREADS, CTAS, RING, F32, GATE, false>, bytes, ctas, most_ctas(p.n), threads, p, st);
+  }
+  else return start(res_norm_kernel<G, THREADS, CTAS, RING, F32, GATE>, bytes, ctas, INT_MAX, threads, p, st);
+}
+template <int G, int THREADS, int CTAS, bool RING, bool BWD>
+static int start(const ResNormParams& p, cudaStream_t st) {
+  auto gated = [&](auto f32) {
+    constexpr bool kF32 = decltype(f32)::value;
+    if (!p.gate) return start<G, THREADS, CTAS, RING, kF32, kNoGate, BWD>(p, st);
+    return p.gate_fn == FCP_GATE_SIGMOID ? start<G, THREADS, CTAS, RING, kF32, kSigmoidGate, BWD>(p, st)
+                                         : start<G, THREADS, CTAS, RING, kF32, kPlainGate, BWD>(p, st);
+  };
+  return p.res_f32 ? gated(std::true_type()) : gated(std::false_type());
 }
 
 int launch_res_norm(const ResNormParams& a, cudaStream_t st) {
   ResNormParams p = a;
   p.groups = p.n / kV;
-  const int threads = threads_of(p.n), grid = (int)std::min<int64_t>(p.places, most_ctas(p.n));
-  if (grid > 0) {
-    const bool ok = groups_of(p.n) == 1 ? go<1, 256, 4, 3>(p, grid, threads, st)
-                    : threads <= 256    ? go<2, 256, 4, 2>(p, grid, threads, st)
-                    : threads <= 512    ? go<2, 512, 2, 1>(p, grid, threads, st)
-                                        : go<2, 1024, 1, 1>(p, grid, threads, st);
-    if (!ok) return FCP_ERR_CUDA;
+  int grid = 0;
+  if (p.places > 0) {
+    if (p.dx)
+      grid = p.n <= 1024   ? start<1, 128, 5, true, true>(p, st)
+             : p.n <= 2048 ? start<2, 128, 4, true, true>(p, st)
+             : p.n <= 4096 ? start<2, 256, 2, true, true>(p, st)
+             : p.n <= 8192 ? start<2, 512, 1, true, true>(p, st)
+                           : start<4, 512, 1, false, true>(p, st);
+    else
+      grid = p.n <= 1024   ? start<1, 128, 8, true, false>(p, st)
+             : p.n <= 4096 ? start<2, 256, 4, true, false>(p, st)
+             : p.n <= 8192 ? start<2, 512, 2, true, false>(p, st)
+                           : start<2, 1024, 1, false, false>(p, st);
+    if (grid == 0) return FCP_ERR_CUDA;
   }
   // (A shard without tokens: no rows, whose sum is written as zero.)
   if (p.dx && (p.dw_post || p.dw_pre))
