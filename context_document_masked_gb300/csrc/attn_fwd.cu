@@ -209,31 +209,98 @@ __device__ __forceinline__ int count_key_tiles(const FwdParams& p, const int32_t
   return n;
 }
 
-// The tiles that WindowWalker gives; -1 as above.
-__device__ __forceinline__ int count_window_tiles(const FwdParams& p, const int32_t* segs, int seg_begin, int seg_count,
-                                                  int q_last, int lo, int hi, int slots) {
-  int n = 0;
-  for (int s = seg_begin; s < seg_begin + seg_count; ++s) {
-    const int* g = segs + 4 * s;
-    if constexpr (kDeviceChecks) {
-      if (!segment_ok(p, g)) return -1;
-    }
-    const int ks = __ldg(g + 2);
-    const int len = min(min(ks + __ldg(g + 3), hi), q_last + 1) - max(ks, lo);
-    if (len <= 0) continue;
-    // The first tile's sinks take `slots` of its rows.
-    n += len <= 128 - slots ? 1 : (len + slots + 127) / 128;
-    slots = 0;
-  }
-  return n + (slots > 0);
-}
-
 struct WorkItem {
   int q_start, q_rows, seg_begin, seg_count, h0, h1, g;
   bool bad;  // checked build: the unit's table entries are out of range (skip it)
   // Under a window: where the piece's document starts, and its sinks' row in the
   // received ones (-1: at doc in K and V); first key of the tile's windows.
   int doc, sink_row, lo, slots;
+};
+
+// Under a window units are short (a window of 128: two key tiles), and what every
+// role reads of the tables for each, four loads one after another, took longer
+// than a tile. There the producer decodes a unit while the one before it is
+// computed and puts what the others need into shared memory.
+constexpr int kUnitSegs = 6;  // key runs held; a unit of more reads the table
+struct WindowUnit {
+  int q_start, q_rows, h0, h1, nt, doc, slots, lo, seg_begin, n_segs;  // nt: -1 skipped, -2 none left
+  int run[kUnitSegs][2];  // keys [begin, end) of the segments that hold any
+};
+template <int R>
+struct UnitRing {
+  WindowUnit unit[R];
+  uint64_t full[R], empty[R];
+  __device__ void init(uint32_t consumers) {
+    for (int r = 0; r < R; ++r) {
+      mbar_init(&full[r], 1);
+      mbar_init(&empty[r], consumers);
+    }
+  }
+  // The producer's place for unit k, once the consumers are done with the one R before.
+  __device__ __forceinline__ WindowUnit* claim(uint32_t k, const WaitCtl& wc) {
+    return k < (uint32_t)R || mbar_wait(&empty[k % R], ((k / R) - 1) & 1, wc) ? &unit[k % R] : nullptr;
+  }
+  __device__ __forceinline__ void publish(uint32_t k) { mbar_arrive(&full[k % R]); }
+  __device__ __forceinline__ bool wait(uint32_t k, const WaitCtl& wc) { return mbar_wait_inline(&full[k % R], (k / R) & 1, wc); }
+  __device__ __forceinline__ void release(uint32_t k) { mbar_arrive(&empty[k % R]); }
+};
+
+// Fills `u` from a decoded unit; its tiles are those that WindowWalker gives.
+__device__ __forceinline__ void describe(const FwdParams& p, const WorkItem& it, WindowUnit* u) {
+  const int q_last = it.q_start + it.q_rows - 1;
+  int n = 0, segs = 0, slots = it.slots;
+  bool ok = !it.bad;
+  for (int s = it.seg_begin; ok && s < it.seg_begin + it.seg_count; ++s) {
+    const int* g = p.segs + 4 * s;
+    if constexpr (kDeviceChecks) ok = segment_ok(p, g);
+    const int ks = __ldg(g + 2), a = max(ks, it.lo), e = min(min(ks + __ldg(g + 3), p.kv_hi), q_last + 1);
+    if (e <= a) continue;
+    if (segs < kUnitSegs) u->run[segs][0] = a, u->run[segs][1] = e;
+    ++segs;
+    n += (e - a + slots + 127) / 128;  // the first tile's sinks take `slots` of its rows
+    slots = 0;
+  }
+  u->q_start = it.q_start;
+  u->q_rows = it.q_rows;
+  u->h0 = it.h0;
+  u->h1 = it.h1;
+  u->doc = it.doc;
+  u->slots = it.slots;
+  u->lo = it.lo;
+  u->seg_begin = it.seg_begin;
+  u->n_segs = segs > kUnitSegs ? -it.seg_count : segs;
+  u->nt = ok ? n + (slots > 0) : -1;
+}
+
+// The tiles of a unit in shared memory, as WindowWalker gives them.
+struct UnitWalker {
+  int s, pos, end, slots;
+  __device__ __forceinline__ explicit UnitWalker(const WindowUnit& u) : s(0), pos(0), end(0), slots(u.slots) {}
+  __device__ __forceinline__ void next(const FwdParams& p, const WindowUnit& u, int& key, int& n, int& off) {
+    off = slots;
+    slots = 0;
+    const int q_last = u.q_start + u.q_rows - 1;
+    while (pos >= end) {
+      if (s >= (u.n_segs < 0 ? -u.n_segs : u.n_segs)) {
+        key = q_last;
+        n = 0;
+        return;
+      }
+      if (u.n_segs >= 0) {
+        pos = u.run[s][0];
+        end = u.run[s][1];
+      } else {
+        const int* g = p.segs + 4 * (u.seg_begin + s);
+        const int ks = __ldg(g + 2);
+        pos = max(ks, u.lo);
+        end = min(min(ks + __ldg(g + 3), p.kv_hi), q_last + 1);
+      }
+      ++s;
+    }
+    key = pos;
+    n = min(128 - off, end - pos);
+    pos += n;
+  }
 };
 
 // Bits [a, b) of 128 set (none for a >= b; the ends may lie outside).
@@ -306,14 +373,9 @@ __device__ __forceinline__ WorkItem decode(const FwdParams& p, const Bias& bias,
 }
 
 // Key tiles of a unit, -1 for one that is skipped (checked build).
-template <class Bias>
 __device__ __forceinline__ int unit_tiles(const FwdParams& p, const WorkItem& it) {
   const int q_last = it.q_start + it.q_rows - 1;
-  if (it.bad) return -1;
-  if constexpr (std::is_same_v<Bias, WindowParams>)
-    return count_window_tiles(p, p.segs, it.seg_begin, it.seg_count, q_last, it.lo, p.kv_hi, it.slots);
-  else
-    return count_key_tiles(p, p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.seg_filter);
+  return it.bad ? -1 : count_key_tiles(p, p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.seg_filter);
 }
 
 template <int D, bool QK8, bool ODD, class Bias>
@@ -331,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_q_full, bar_q_empty, bar_drain;
   __shared__ __align__(8) uint64_t bar_kv_full[C::kStages], bar_kv_empty[C::kStages];
   __shared__ __align__(8) uint64_t bar_s_full[2], bar_p_ready[2], bar_o_done[2], bar_o_free[2];
-  __shared__ WorkRing<4> ring;
+  __shared__ std::conditional_t<kWindow, UnitRing<4>, WorkRing<4>> ring;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   __shared__ std::conditional_t<kBias, Buckets, NoBias> buckets;
@@ -388,11 +450,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int s = 0; s < C::kStages; ++s) issued[s] = 0;
       bool ok = true;
       uint32_t k = 0;
-      for (int w = blockIdx.x; ok; w = next_work(p.work_counter)) {
-        if (!(ok = ring.put<true>(k++, w, wc)) || w >= n_work) break;
-        const WorkItem it = decode<ODD>(p, bp, w);
+      // Under a window: the next unit, decoded and published as soon as the
+      // loads of the one before are issued (claimed any earlier, a CTA with a long
+      // unit would hold another that an idle one could take).
+      WorkItem ahead;
+      int w_ahead = blockIdx.x, nt_ahead = 0;
+      auto publish_next = [&] {
+        if constexpr (kWindow) {
+          WindowUnit* u = ring.claim(k, wc);
+          if (!(ok = u != nullptr)) return;
+          if (w_ahead >= n_work) {
+            u->nt = -2;
+          } else {
+            ahead = decode<ODD>(p, bp, w_ahead);
+            describe(p, ahead, u);
+          }
+          nt_ahead = u->nt;
+          ring.publish(k++);
+        }
+      };
+      for (int w = blockIdx.x; ok;) {
+        WorkItem it;
+        int nt;
+        if constexpr (kWindow) {
+          if (k > 0) w_ahead = next_work(p.work_counter);
+          publish_next();
+          if (!ok || nt_ahead == -2) break;
+          it = ahead;
+          nt = nt_ahead;
+        } else {
+          if (k > 0) w = next_work(p.work_counter);
+          if (!(ok = ring.template put<true>(k++, w, wc)) || w >= n_work) break;
+          it = decode<ODD>(p, bp, w);
+          nt = unit_tiles(p, it);
+        }
         const int q_last = it.q_start + it.q_rows - 1;
-        const int nt = unit_tiles<Bias>(p, it);
         if (nt < 0) atomicOr(p.err, kErrBadTable);
         if (nt <= 0) continue;
         if (q_iter > 0 && !(ok = mbar_wait_inline(&bar_q_empty, (q_iter - 1) & 1, wc))) break;
@@ -489,13 +581,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                      smem_desc_sw128(va + kk * 2048, 16384, 1024), idesc_o, (acc || kk > 0));
       };
       for (uint32_t k = 0; ok; ++k) {
-        int w;
-        if (!(ok = ring.get<true>(k, w, wc))) break;
-        ring.release(k);
-        if (w >= n_work) break;
-        const WorkItem it = decode<ODD>(p, bp, w);
-        const int q_last = it.q_start + it.q_rows - 1;
-        const int nt = unit_tiles<Bias>(p, it);
+        int nt;
+        if constexpr (kWindow) {
+          if (!(ok = ring.wait(k, wc))) break;
+          nt = ring.unit[k % 4].nt;
+          ring.release(k);
+          if (nt == -2) break;
+        } else {
+          int w;
+          if (!(ok = ring.template get<true>(k, w, wc))) break;
+          ring.release(k);
+          if (w >= n_work) break;
+          nt = unit_tiles(p, decode<ODD>(p, bp, w));
+        }
         if (nt <= 0) continue;
         if (!(ok = mbar_wait_inline(&bar_q_full, q_iter & 1, wc))) break;
         tc_fence_after();
@@ -562,15 +660,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float scale_log2 = QK8 ? p.scale_log2 / (p.qk_scale[0] * p.qk_scale[1]) : p.scale_log2;
     for (uint32_t k = 0; ok; ++k) {
       int w = 0;
-      ok = ring.get<true>(k, w, wc);
+      if constexpr (kWindow) ok = ring.wait(k, wc);
+      else ok = ring.template get<true>(k, w, wc);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       __syncwarp();
-      if (lane == 0) ring.release(k);
-      if (w >= n_work) break;
-      const WorkItem it = decode<ODD>(p, bp, w);
+      std::conditional_t<kWindow, WindowUnit, WorkItem> it;
+      int nt;
+      if constexpr (kWindow) {  // released at the unit's end
+        const WindowUnit& u = ring.unit[k % 4];
+        it.q_start = u.q_start, it.q_rows = u.q_rows, it.h0 = u.h0, it.h1 = u.h1, it.doc = u.doc;
+        nt = u.nt;
+        if (nt == -2) break;
+      } else {
+        if (lane == 0) ring.release(k);
+        if (w >= n_work) break;
+        it = decode<ODD>(p, bp, w);
+        nt = unit_tiles(p, it);
+      }
+      auto release_unit = [&] {
+        if constexpr (kWindow) {
+          __syncwarp();
+          if (lane == 0) ring.release(k);
+        }
+      };
       const int q_last = it.q_start + it.q_rows - 1;
-      const int nt = unit_tiles<Bias>(p, it);
-      if (nt < 0) continue;  // checked build: a unit with out-of-range table entries stores nothing
+      if (nt < 0) {  // checked build: a unit with out-of-range table entries stores nothing
+        release_unit();
+        continue;
+      }
       const int q = it.q_start + r;
       bool row_valid = r < it.q_rows;
       int head = it.h0 + i;
@@ -581,14 +698,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       float run_bias = 0.f;
       if constexpr (kBias) bias_row = bp.bias + (size_t)(i ? it.h1 : it.h0) * bp.n;
       if (nt > 0) {
-        Walk wk;
+        std::conditional_t<kWindow, UnitWalker, Walker> wk = [&] {
+          if constexpr (kWindow) return UnitWalker(ring.unit[k % 4]);
+          else return Walker();
+        }();
         int src, row, key, n, off = 0;
-        if constexpr (kWindow)
-          wk.init(p.segs, it.seg_begin, it.seg_count, q_last, it.lo, p.kv_hi, p.kbuf_shift, it.slots);
-        else
+        if constexpr (!kWindow)
           wk.init(p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.kbuf_shift, p.seg_filter);
         for (int t = 0; t < nt; ++t) {
-          if constexpr (kWindow) wk.next(src, row, key, n, off);
+          if constexpr (kWindow) wk.next(p, ring.unit[k % 4], key, n, off);
           else wk.next(src, row, key, n);
           // Bias of the tile: one bucket for all the warp's distances, or the
           // window of them. Set up before S is waited for, so its latency is
@@ -779,6 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&bar_o_free[i]);
       }
+      release_unit();
     }
   }
 
