@@ -496,12 +496,9 @@ static int attn_fwd_impl(const void* q, const void* k, const void* v, const void
       sq = fcp::launch_quant_e4m3_with(kbuf, wsb + wl.kb8, rrows * dims.hkv * dims.d, amax + 1, num_sms(), cs);
     if (sq) return sq;
   }
-  int st2 = fcp::launch_convert_f16(v, v16, (int64_t)dims.T * dims.hkv * dims.d, static_cast<int*>(ws),
-                                    counter, num_sms(), cs);
-  if (st2 == FCP_OK && rrows > 0)
-    st2 = fcp::launch_convert_f16(vbuf, vb16, rrows * dims.hkv * dims.d, static_cast<int*>(ws), nullptr,
-                                  num_sms(), cs);
-  if (st2) return st2;
+  if (int st2 = fcp::launch_convert_f16(v, v16, (int64_t)dims.T * dims.hkv * dims.d, vbuf, vb16,
+                                        rrows * dims.hkv * dims.d, static_cast<int*>(ws), counter, num_sms(), cs))
+    return st2;
 
   fcp::FwdLaunch a;
   std::memset(&a, 0, sizeof(a));

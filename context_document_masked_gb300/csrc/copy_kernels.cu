@@ -388,23 +388,25 @@ __global__ void __launch_bounds__(kPreThreads) preprocess_kernel(const PreLaunch
 }
 
 // ------------------------------------------------------- bf16 -> fp16
-// fp16 copy of a bf16 tensor (exact from 2^-17 up, below that off by 2^-25 at
+// fp16 copies of one or two bf16 tensors (exact from 2^-17 up, below that off by 2^-25 at
 // most; error bit 4 when a value exceeds the fp16 range). The forward's P*V product runs on fp16 operands.
 constexpr int kCvtThreads = 256;
 
 __global__ void __launch_bounds__(kCvtThreads)
-    convert_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst, int64_t n, int* err,
-                   int* zero_word) {
+    convert_kernel(const uint4* __restrict__ src, uint4* __restrict__ dst, int64_t n, const uint4* __restrict__ src2,
+                   uint4* __restrict__ dst2, int64_t n2, int* err, int* zero_word) {
   if (zero_word && blockIdx.x == 0 && threadIdx.x == 0) *zero_word = 0;
   bool ovf = false;
-  for (int64_t i = (int64_t)blockIdx.x * kCvtThreads + threadIdx.x; i < n;
-       i += (int64_t)gridDim.x * kCvtThreads) {
-    uint4 x = __ldg(src + i);
+  for (int64_t j = (int64_t)blockIdx.x * kCvtThreads + threadIdx.x; j < n + n2;
+       j += (int64_t)gridDim.x * kCvtThreads) {
+    const bool first = j < n;
+    const int64_t i = first ? j : j - n;
+    uint4 x = __ldg((first ? src : src2) + i);
     x.x = cvt_pair(x.x, ovf);
     x.y = cvt_pair(x.y, ovf);
     x.z = cvt_pair(x.z, ovf);
     x.w = cvt_pair(x.w, ovf);
-    dst[i] = x;
+    (first ? dst : dst2)[i] = x;
   }
   if (ovf) atomicOr(err, 4);
 }
@@ -503,15 +505,16 @@ int launch_quant_e4m3_with(const void* src, void* dst, int64_t n_elems, const un
   return cudaGetLastError() == cudaSuccess ? FCP_OK : FCP_ERR_CUDA;
 }
 
-int launch_convert_f16(const void* src, void* dst, int64_t n_elems, int* err, int* zero_word,
-                       int num_sms, cudaStream_t st) {
-  const int64_t n = n_elems / 8;
-  if (n == 0 && !zero_word) return FCP_OK;
-  int64_t grid = (n + kCvtThreads - 1) / kCvtThreads;
+int launch_convert_f16(const void* src, void* dst, int64_t n_elems, const void* src2, void* dst2, int64_t n_elems2, int* err,
+                       int* zero_word, int num_sms, cudaStream_t st) {
+  const int64_t n = n_elems / 8, n2 = n_elems2 / 8;
+  if (n + n2 == 0 && !zero_word) return FCP_OK;
+  int64_t grid = (n + n2 + kCvtThreads - 1) / kCvtThreads;
   if (grid > (int64_t)num_sms * 16) grid = (int64_t)num_sms * 16;
   if (grid < 1) grid = 1;
   convert_kernel<<<(int)grid, kCvtThreads, 0, st>>>(static_cast<const uint4*>(src),
-                                                    static_cast<uint4*>(dst), n, err, zero_word);
+                                                    static_cast<uint4*>(dst), n, static_cast<const uint4*>(src2),
+                                                    static_cast<uint4*>(dst2), n2, err, zero_word);
   return cudaGetLastError() == cudaSuccess ? FCP_OK : FCP_ERR_CUDA;
 }
 

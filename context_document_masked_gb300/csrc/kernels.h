@@ -173,10 +173,10 @@ struct PreLaunch {
 };
 int launch_bwd_preprocess(const PreLaunch& a, int32_t d, cudaStream_t st);
 
-// fp16 copy of a bf16 array of n_elems (a multiple of 8) elements; *zero_word
-// (if not null) is set to 0, as above.
-int launch_convert_f16(const void* src, void* dst, int64_t n_elems, int* err, int* zero_word,
-                       int num_sms, cudaStream_t st);
+// fp16 copies of a bf16 array of n_elems (a multiple of 8) elements and of a
+// second one of n_elems2 (0: none); *zero_word (if not null) is set to 0, as above.
+int launch_convert_f16(const void* src, void* dst, int64_t n_elems, const void* src2, void* dst2, int64_t n_elems2, int* err,
+                       int* zero_word, int num_sms, cudaStream_t st);
 
 // bf16 copy (round to nearest even) of an fp32 array of n_elems (a multiple
 // of 8) elements.

@@ -129,9 +129,8 @@ extern "C" int fcp_attn_fwd_noalloc(const void* q, const void* k, const void* v,
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (cudaMemsetAsync(err, 0, sizeof(int), cs) != cudaSuccess) return FCP_ERR_CUDA;
   int* counter = reinterpret_cast<int*>(base + 64);  // the forward kernel's work counter
-  st = fcp::launch_convert_f16(v, v16, (int64_t)dims.T * dims.hkv * dims.d, err, counter, num_sms(), cs);
-  if (st == FCP_OK && rrows > 0)
-    st = fcp::launch_convert_f16(vbuf, vb16, rrows * dims.hkv * dims.d, err, nullptr, num_sms(), cs);
+  st = fcp::launch_convert_f16(v, v16, (int64_t)dims.T * dims.hkv * dims.d, vbuf, vb16, rrows * dims.hkv * dims.d, err,
+                               counter, num_sms(), cs);
   if (st) return st;
 
   fcp::FwdLaunch a;

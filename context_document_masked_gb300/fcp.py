@@ -314,7 +314,7 @@ def _stream(stream):
     if stream is None:
         # torch.cuda.current_stream().cuda_stream, without making a Stream object
         # (8 us of a call's 45 on this host).
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -384,8 +384,9 @@ def gather_kv(k, v, dplan: DevicePlan, shard: int, kbuf, vbuf, stream=None):
     _t(k, "k", _BF16, (None, None, None))
     _t(v, "v", _BF16, tuple(k.shape))
     _kbuf(kbuf, vbuf, dplan, shard, k.shape[1], k.shape[2])
-    _check(_lib.fcp_gather_kv(_ptr(k), _ptr(v), C.byref(dplan.c), shard, k.shape[1], k.shape[2],
-                              _ptr(kbuf), _ptr(vbuf), _stream(stream)), "fcp_gather_kv")
+    with _on(k, v, kbuf, vbuf, dplan.buf):
+        _check(_lib.fcp_gather_kv(_ptr(k), _ptr(v), C.byref(dplan.c), shard, k.shape[1], k.shape[2],
+                                  _ptr(kbuf), _ptr(vbuf), _stream(stream)), "fcp_gather_kv")
 
 
 def attn_fwd(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, lse, ws, kv_lo: int = 0,
@@ -396,10 +397,11 @@ def attn_fwd(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, lse, ws, k
     _t(ws, "ws")
     dm = Dims(T, hq, hkv, d, scale)
     out_dtype = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
-    _check(_lib.fcp_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kbuf), _ptr(vbuf), C.byref(dplan.c),
-                             shard, kv_lo, T if kv_hi is None else kv_hi, dm, out_dtype, _ptr(out),
-                             _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "fcp_attn_fwd")
+    with _on(q, k, v, kbuf, vbuf, out, lse, ws, dplan.buf):
+        _check(_lib.fcp_attn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kbuf), _ptr(vbuf), C.byref(dplan.c),
+                                 shard, kv_lo, T if kv_hi is None else kv_hi, dm, out_dtype, _ptr(out),
+                                 _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+               "fcp_attn_fwd")
 
 
 def attn_fwd_qk8(q, k, v, kbuf, vbuf, dplan: DevicePlan, shard: int, out, lse, ws, kv_lo: int = 0,
@@ -510,10 +512,11 @@ def attn_bwd(q, k, v, kbuf, vbuf, out, lse, dout, dplan: DevicePlan, shard: int,
     _t(ws, "ws")
     dm = Dims(T, hq, hkv, d, scale)
     out_dtype = OUT_F32 if out.dtype == torch.float32 else OUT_BF16
-    _check(_lib.fcp_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kbuf), _ptr(vbuf), _ptr(out), out_dtype,
-                             _ptr(lse), _ptr(dout), C.byref(dplan.c), shard, dm, _ptr(dq), _ptr(dk),
-                             _ptr(dv), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "fcp_attn_bwd")
+    with _on(q, k, v, kbuf, vbuf, out, lse, dout, dq, dk, dv, ws, dplan.buf):
+        _check(_lib.fcp_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(kbuf), _ptr(vbuf), _ptr(out), out_dtype,
+                                 _ptr(lse), _ptr(dout), C.byref(dplan.c), shard, dm, _ptr(dq), _ptr(dk),
+                                 _ptr(dv), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+               "fcp_attn_bwd")
 
 
 # ----------------------------------------------- bias by distance buckets
@@ -603,7 +606,7 @@ def _on(first, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != i:
             raise ValueError(f"tensors on {first.device} and {t.device}")
-    return _HERE_CTX if torch.cuda.current_device() == i else torch.cuda.device(i)
+    return _HERE_CTX if torch._C._cuda_getDevice() == i else torch.cuda.device(i)
 
 
 def _rows(t, name, T, heads, d):
@@ -712,6 +715,10 @@ def _matrix(t, name, dtype, T, n):
     elements apart (a slice of a wider tensor); 0 for None."""
     if t is None:
         return 0
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.shape == (T, n):  # what a call nearly always has
+        stride, of_value = t.stride()
+        if of_value == 1 and stride >= n and not stride & 7 and T > 1:
+            return stride
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if not t.is_cuda:
