@@ -554,6 +554,11 @@ static int attn_fwd_impl(const void* q, const void* k, const void* v, const void
       !set_window(&a.window, p, dims, k, v16, rrows > 0 ? kbuf : k, rrows > 0 ? vb16 : v16, rrows > 0 ? rrows : dims.T, true,
                   nullptr, nullptr))
     return FCP_ERR_CUDA;
+  if (a.has_window) {
+    const int32_t d0 = shard < 0 ? 0 : host_at(p, fcp::TB_RSEGS, shard);
+    a.window.doubles = table(plan, fcp::TB_RPIECES) + 4 * (int64_t)d0;
+    a.window.n_doubles = (shard < 0 ? plan->counts[fcp::TB_RPIECES] : host_at(p, fcp::TB_RSEGS, shard + 1)) - d0;
+  }
   return fcp::launch_attn_fwd(a, cs);
 }
 

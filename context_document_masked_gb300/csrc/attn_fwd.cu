@@ -58,6 +58,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "bias.cuh"
@@ -215,6 +216,9 @@ struct WorkItem {
   // Under a window: where the piece's document starts, and its sinks' row in the
   // received ones (-1: at doc in K and V); first key of the tile's windows.
   int doc, sink_row, lo, slots;
+  // Rows of the second slot and where they begin: the first's but for a double
+  // tile, whose second tile is of the same head.
+  int q1, rows1;
 };
 
 // Under a window units are short (a window of 128: two key tiles), and what every
@@ -223,7 +227,7 @@ struct WorkItem {
 // computed and puts what the others need into shared memory.
 constexpr int kUnitSegs = 6;  // key runs held; a unit of more reads the table
 struct WindowUnit {
-  int q_start, q_rows, h0, h1, nt, doc, slots, lo, seg_begin, n_segs;  // nt: -1 skipped, -2 none left
+  int q_start, q_rows, q1, rows1, q_last, h0, h1, nt, doc, slots, lo, seg_begin, n_segs;  // nt: -1 skipped, -2 none left
   int run[kUnitSegs][2];  // keys [begin, end) of the segments that hold any
 };
 template <int R>
@@ -247,7 +251,7 @@ struct UnitRing {
 
 // Fills `u` from a decoded unit; its tiles are those that WindowWalker gives.
 __device__ __forceinline__ void describe(const FwdParams& p, const WorkItem& it, WindowUnit* u) {
-  const int q_last = it.q_start + it.q_rows - 1;
+  const int q_last = max(it.q_start + it.q_rows, it.q1 + it.rows1) - 1;
   int n = 0, segs = 0, slots = it.slots;
   bool ok = !it.bad;
   for (int s = it.seg_begin; ok && s < it.seg_begin + it.seg_count; ++s) {
@@ -262,6 +266,9 @@ __device__ __forceinline__ void describe(const FwdParams& p, const WorkItem& it,
   }
   u->q_start = it.q_start;
   u->q_rows = it.q_rows;
+  u->q1 = it.q1;
+  u->rows1 = it.rows1;
+  u->q_last = q_last;
   u->h0 = it.h0;
   u->h1 = it.h1;
   u->doc = it.doc;
@@ -279,7 +286,7 @@ struct UnitWalker {
   __device__ __forceinline__ void next(const FwdParams& p, const WindowUnit& u, int& key, int& n, int& off) {
     off = slots;
     slots = 0;
-    const int q_last = u.q_start + u.q_rows - 1;
+    const int q_last = u.q_last;
     while (pos >= end) {
       if (s >= (u.n_segs < 0 ? -u.n_segs : u.n_segs)) {
         key = q_last;
@@ -316,26 +323,52 @@ __device__ __forceinline__ void set_bits(uint32_t (&m)[4], int a, int b) {
 // group's last pair holds one head (its second slot repeats the first and
 // stores nothing).
 __host__ __device__ __forceinline__ int head_pairs(int hq, int hkv) { return hkv * ((hq / hkv + 1) / 2); }
+// Under a window such a head has double tiles instead (units of their own, before
+// those of the pairs): a tile's second slot then works on other rows, not for nothing.
+__host__ __device__ __forceinline__ int whole_pairs(int hq, int hkv) { return hkv * (hq / hkv / 2); }
+template <bool ODD, class Bias>
+__host__ __device__ __forceinline__ int unit_count(const FwdParams& p, const Bias& bias) {
+  if constexpr (ODD && std::is_same_v<Bias, WindowParams>)
+    return p.n_items * whole_pairs(p.hq, p.hkv) + bias.n_doubles * p.hkv;
+  else
+    return p.n_items * (ODD ? head_pairs(p.hq, p.hkv) : p.hq / 2);
+}
 
 template <bool ODD, class Bias>
 __device__ __forceinline__ WorkItem decode(const FwdParams& p, const Bias& bias, int w) {
-  const int hp_count = ODD ? head_pairs(p.hq, p.hkv) : p.hq / 2;
-  const WorkSlot ws = work_slot(w, p.n_items, hp_count, p.order_block);
-  const int item = __ldg(p.order + ws.pos);
-  const int hp = ws.head;
+  constexpr bool kDoubles = ODD && std::is_same_v<Bias, WindowParams>;
+  const int hp_count = kDoubles ? whole_pairs(p.hq, p.hkv) : ODD ? head_pairs(p.hq, p.hkv) : p.hq / 2;
+  bool single = false;  // a double tile
+  int at = 0, hp = 0, piece;
+  if constexpr (kDoubles) {
+    if ((single = w < bias.n_doubles * p.hkv)) {  // the longer ones first
+      hp = w / bias.n_doubles;  // the KV head
+      at = w % bias.n_doubles;
+    }
+    w -= bias.n_doubles * p.hkv;
+  }
   WorkItem it;
   it.bad = false;
-  if constexpr (kDeviceChecks) {
-    if (item < 0 || item >= p.n_tiles) {
-      it = WorkItem{0, 0, 0, 0, 0, 0, 0, true, 0, 0, 0, 0};
-      return it;
+  const int* t;
+  if (single) {
+    if constexpr (kDoubles) t = bias.doubles + 4 * at;
+    piece = __ldg(t + 0);
+  } else {
+    const WorkSlot ws = work_slot(w, p.n_items, hp_count, p.order_block);
+    const int item = __ldg(p.order + ws.pos);
+    hp = ws.head;
+    if constexpr (kDeviceChecks) {
+      if (item < 0 || item >= p.n_tiles) {
+        it = WorkItem{0, 0, 0, 0, 0, 0, 0, true, 0, 0, 0, 0, 0, 0};
+        return it;
+      }
     }
+    t = p.tiles + 4 * item;
+    piece = __ldg(t + 0);
   }
-  const int* t = p.tiles + 4 * item;
-  const int piece = __ldg(t + 0);
   if constexpr (kDeviceChecks) {
     if (piece < 0 || piece >= p.n_pieces) {
-      it = WorkItem{0, 0, 0, 0, 0, 0, 0, true, 0, 0, 0, 0};
+      it = WorkItem{0, 0, 0, 0, 0, 0, 0, true, 0, 0, 0, 0, 0, 0};
       return it;
     }
   }
@@ -347,8 +380,11 @@ __device__ __forceinline__ WorkItem decode(const FwdParams& p, const Bias& bias,
     it.bad = it.q_rows < 1 || it.q_rows > 128 || it.q_start < 0 || it.q_start > p.T - it.q_rows ||
              it.seg_begin < 0 || it.seg_count < 0 || it.seg_begin > p.n_segs - it.seg_count;
   }
-  if constexpr (ODD) {
-    const int G = p.hq / p.hkv, per_group = (G + 1) / 2;
+  if (single) {
+    it.g = hp;
+    it.h0 = it.h1 = (hp + 1) * (p.hq / p.hkv) - 1;
+  } else if constexpr (ODD) {
+    const int G = p.hq / p.hkv, per_group = kDoubles ? G / 2 : (G + 1) / 2;
     it.g = hp / per_group;
     it.h0 = it.g * G + 2 * (hp % per_group);
     it.h1 = it.h0 + 1 < (it.g + 1) * G ? it.h0 + 1 : it.h0;
@@ -358,7 +394,15 @@ __device__ __forceinline__ WorkItem decode(const FwdParams& p, const Bias& bias,
     it.g = it.h0 / (p.hq / p.hkv);
   }
   if constexpr (std::is_same_v<Bias, WindowParams>) {
-    const int q_last = it.q_start + it.q_rows - 1;
+    it.q1 = it.q_start;
+    it.rows1 = it.q_rows;
+    if (single) {
+      const int rows = __ldg(t + 3);
+      if (rows > 0) it.q1 += it.q_rows;
+      it.rows1 = rows;
+      if constexpr (kDeviceChecks) it.bad = it.bad || rows < 0 || rows > 128 || it.q1 > p.T - rows;
+    }
+    const int q_last = max(it.q_start + it.q_rows, it.q1 + it.rows1) - 1;
     it.doc = __ldg(p.pieces + 8 * piece + 4);
     it.lo = max(p.kv_lo, it.q_start - bias.window + 1);
     it.slots = q_last - bias.window >= it.doc ? bias.slots : 0;
@@ -437,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
   const WaitCtl wc{&abort_sh, p.err, p.wait_ns};
-  const int n_work = p.n_items * (ODD ? head_pairs(p.hq, p.hkv) : p.hq / 2);
+  const int n_work = unit_count<ODD>(p, bp);
 
   uint8_t* sQ = smem + C::kQOff;
   uint8_t* sKV = smem + C::kKVOff;
@@ -484,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           it = decode<ODD>(p, bp, w);
           nt = unit_tiles(p, it);
         }
-        const int q_last = it.q_start + it.q_rows - 1;
+        const int q_last = (kWindow && ODD ? max(it.q_start + it.q_rows, it.q1 + it.rows1) : it.q_start + it.q_rows) - 1;
         if (nt < 0) atomicOr(p.err, kErrBadTable);
         if (nt <= 0) continue;
         if (q_iter > 0 && !(ok = mbar_wait_inline(&bar_q_empty, (q_iter - 1) & 1, wc))) break;
@@ -497,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; h < 2; ++h)
             for (int pn = 0; pn < C::kPanels; ++pn)
               tma_load_3d(sQ + h * C::kTileBytes + pn * 16384, &tm_q, &bar_q_full, pn * 64, h ? it.h1 : it.h0,
-                          it.q_start);
+                          kWindow && ODD && h ? it.q1 : it.q_start);
         }
         ++q_iter;
         Walk wk;
@@ -668,7 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int nt;
       if constexpr (kWindow) {  // released at the unit's end
         const WindowUnit& u = ring.unit[k % 4];
-        it.q_start = u.q_start, it.q_rows = u.q_rows, it.h0 = u.h0, it.h1 = u.h1, it.doc = u.doc;
+        it.q_start = ODD && i ? u.q1 : u.q_start, it.q_rows = ODD && i ? u.rows1 : u.q_rows;
+        it.h0 = u.h0, it.h1 = u.h1, it.doc = u.doc;
         nt = u.nt;
         if (nt == -2) break;
       } else {
@@ -843,7 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // group's last pair repeats the first head: it runs but stores nothing.
       if constexpr (ODD) {
         head = i ? it.h1 : it.h0;
-        row_valid = row_valid && (i == 0 || it.h1 != it.h0);
+        // (Of a double tile it has rows of its own.)
+        if (!kWindow) row_valid = row_valid && (i == 0 || it.h1 != it.h0);
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const size_t obase = ((size_t)q * p.hq + head) * D;
@@ -923,13 +969,13 @@ static int launch_fwd_impl(const FwdLaunch& a, const Bias& bias, cudaStream_t st
       return FCP_ERR_CUDA;
     attr_set[dev] = true;
   }
-  const int n_work = a.p.n_items * head_pairs(a.p.hq, a.p.hkv);
+  const int n_work = unit_count<ODD>(a.p, bias);
   if (n_work == 0) return FCP_OK;
   const int grid = n_work < a.num_sms ? n_work : a.num_sms;
   // Blocks of query tiles such that one block's head pairs of one KV head
   // fill the grid: the CTAs running together stream the same K/V rows.
   FwdParams p = a.p;
-  const int pairs_per_kv = head_pairs(p.hq, p.hkv) / p.hkv;
+  const int pairs_per_kv = std::max(1, (std::is_same_v<Bias, WindowParams> ? whole_pairs : head_pairs)(p.hq, p.hkv) / p.hkv);
   // Few units go item by item, so that the longest come first (with a bias, 7001
   // tokens of 6 heads, 1.6 units a CTA: 64 us for 73; one document of 16K, 16
   // heads, 6.7: 1.01 ms for 1.03; the 32K workload, 20 or more: the same).

@@ -75,6 +75,8 @@ struct WindowParams {
   CUtensorMap k_rest, v_rest, kb_rest, vb_rest;
   CUtensorMap dk_sinks, dv_sinks, dk_rest, dv_rest;  // backward: as tm_dk, tm_dv
   int32_t window, sinks, slots;
+  const int32_t* doubles;  // forward, odd groups: double query tiles (plan.h, TB_RPIECES)
+  int32_t n_doubles;
 };
 
 struct FwdLaunch {

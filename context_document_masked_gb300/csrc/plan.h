@@ -53,8 +53,12 @@ enum Table {
   TB_RSHARD,
   TB_IDENT,        // 0, 1, 2, ... (indirection for one-shard launches)
   TB_KBASE,        // N+1 kbuf row offsets
-  TB_RPIECES,      // TB_PIECES with seg_begin / seg_count into TB_RSEGS
-  TB_RSEGS,        // 4 ints: ring distance, src_row (= key_start), key_start, len
+  TB_RPIECES,      // TB_PIECES with seg_begin / seg_count into TB_RSEGS. In windowed plans
+                   // (no ring order): double query tiles for one head, 4 ints: piece,
+                   // q_start, rows of the first, rows of the second behind it (0: none),
+                   // grouped by shard
+  TB_RSEGS,        // 4 ints: ring distance, src_row (= key_start), key_start, len. In
+                   // windowed plans N+1 offsets into the double tiles
   TB_COUNT
 };
 

@@ -119,12 +119,16 @@ void Plan::build_work_tables() {
   std::vector<int64_t> fcost, bcost;
   std::vector<int32_t> fpiece, bpiece;
   struct PieceInfo { int32_t id, doc, start, end, seg_begin, seg_count; };
+  std::vector<int32_t> doubles, dshard(N + 1, 0);
+  std::vector<int64_t> dcost;
   int32_t piece_id = 0;
   // Under a window: rows of query tiles and of key tiles, with sinks and without.
   // A forward unit's ends cost about 1.5 key tiles, a backward one's three steps.
   const int32_t slots = sink_slots(sinks);
   const int32_t q_plain = window > 0 ? rows_for_window(window, 0, kTileM, 1.5) : kTileM;
   const int32_t q_sinks = window > 0 ? rows_for_window(window, slots, kTileM, 1.5) : kTileM;
+  const int32_t d_plain = window > 0 ? rows_for_window(window, 0, 2 * kTileM, 1.5) : 0;
+  const int32_t d_sinks = window > 0 ? rows_for_window(window, slots, 2 * kTileM, 1.5) : 0;
   const int32_t k_plain = window > 0 ? rows_for_window(window, 0, kTileN, 3) : kTileN;
   const int32_t k_sinks = window > 0 ? rows_for_window(window, 0, kTileN - slots, 3) : kTileN;
   for (int32_t j = 0; j < N; ++j) {
@@ -133,6 +137,7 @@ void Plan::build_work_tables() {
     bshard[j] = (int32_t)(btiles.size() / kBwdTileInts);
     cshard[j] = (int32_t)(copy.size() / 4);
     rshard[j] = (int32_t)(rows.size() / 2);
+    dshard[j] = (int32_t)(doubles.size() / 4);
     // Position of each remote range inside this shard's kbuf.
     std::vector<int64_t> rpos(sh.kv_remote.size());
     int64_t acc = sh.kbuf_base;
@@ -200,6 +205,16 @@ void Plan::build_work_tables() {
           shards[j].fwd_tiles += w.tiles;
           shards[j].fwd_qtiles += 1;
           shards[j].fwd_masked += w.masked;
+        }
+        // The same rows in double tiles, for the head of a group that has no
+        // partner: its two tiles share their keys as two heads do.
+        for (int32_t q0 = p.start, qr; q0 < p.end; q0 += qr) {
+          const int32_t most = 2 * kTileM;
+          qr = q0 + most - 1 - window < ds ? most : sees_sinks(q0 + most - 1, ds) ? d_sinks : d_plain;
+          qr = std::min(qr, p.end - q0);
+          const int32_t first = qr <= kTileM ? qr : (qr + 1) / 2, last = q0 + qr - 1;
+          doubles.insert(doubles.end(), {piece_id, q0, first, qr - first});
+          dcost.push_back(window_key_tiles(segs, seg_begin, seg_count, q0, last, window, sees_sinks(last, ds) ? slots : 0).tiles);
         }
       } else
       for (int32_t q0 = p.start; q0 < p.end; q0 += kTileM) {
@@ -286,6 +301,15 @@ void Plan::build_work_tables() {
   bshard[N] = (int32_t)(btiles.size() / kBwdTileInts);
   cshard[N] = (int32_t)(copy.size() / 4);
   rshard[N] = (int32_t)(rows.size() / 2);
+  dshard[N] = (int32_t)(doubles.size() / 4);
+  for (int32_t j = 0; j < N; ++j) {  // longest first
+    std::vector<int32_t> idx(dshard[j + 1] - dshard[j]);
+    std::iota(idx.begin(), idx.end(), dshard[j]);
+    std::stable_sort(idx.begin(), idx.end(), [&](int32_t a, int32_t b) { return dcost[a] > dcost[b]; });
+    std::vector<int32_t> sorted;
+    for (int32_t i : idx) sorted.insert(sorted.end(), doubles.begin() + 4 * (size_t)i, doubles.begin() + 4 * (size_t)i + 4);
+    std::copy(sorted.begin(), sorted.end(), doubles.begin() + 4 * (size_t)dshard[j]);
+  }
   // Piece-major, longest-first orders. A piece's rank is the position of its
   // longest tile among all pieces' longest tiles.
   auto ranks = [&](const std::vector<int64_t>& cost, const std::vector<int32_t>& piece) {
@@ -352,7 +376,7 @@ void Plan::build_work_tables() {
     for (const Piece& p : shards[j].pieces) doc_runs[p.doc].push_back({p.start, p.end, j});
   for (auto& v : doc_runs) std::sort(v.begin(), v.end());
   std::vector<int32_t> rpieces, rsegs;
-  for (int32_t j = 0; j < N; ++j) {
+  for (int32_t j = 0; window == 0 && j < N; ++j) {
     for (const Piece& p : shards[j].pieces) {
       std::vector<std::array<int32_t, 3>> runs;  // (distance, start, len)
       for (const auto& r : doc_runs[p.doc]) {
@@ -388,8 +412,13 @@ void Plan::build_work_tables() {
   append(dev, tab_off, tab_cnt, TB_RSHARD, rshard, N + 1);
   append(dev, tab_off, tab_cnt, TB_IDENT, ident, (int32_t)ident.size());
   append(dev, tab_off, tab_cnt, TB_KBASE, kbase, N + 1);
-  append(dev, tab_off, tab_cnt, TB_RPIECES, rpieces, (int32_t)(rpieces.size() / 8));
-  append(dev, tab_off, tab_cnt, TB_RSEGS, rsegs, (int32_t)(rsegs.size() / 4));
+  if (window > 0) {
+    append(dev, tab_off, tab_cnt, TB_RPIECES, doubles, (int32_t)(doubles.size() / 4));
+    append(dev, tab_off, tab_cnt, TB_RSEGS, dshard, N + 1);
+  } else {
+    append(dev, tab_off, tab_cnt, TB_RPIECES, rpieces, (int32_t)(rpieces.size() / 8));
+    append(dev, tab_off, tab_cnt, TB_RSEGS, rsegs, (int32_t)(rsegs.size() / 4));
+  }
   while ((dev.size() * 4) % 256) dev.push_back(0);
 }
 

@@ -169,6 +169,35 @@ def test_tables_cover_the_mask(lib, docs, cp, policy, window, sinks):
     assert sorted(t[FORDER]) == list(range(len(t[FTILES]))) and sorted(t[BORDER]) == list(range(len(t[BTILES])))
 
 
+@pytest.mark.parametrize("docs,cp,policy,window,sinks", CASES)
+def test_double_tiles_cover_the_mask(lib, docs, cp, policy, window, sinks):
+    """The double query tiles (two runs of up to 128 rows of one head), walked as the forward walks them."""
+    p = lib.Plan(docs, cp, policy).windowed(window, sinks)
+    image = p.device_image()
+    t = tables(p, image)
+    dp = lib.DevPlan()
+    assert lib.raw_call("fcp_plan_bind", p._ptr, FAKE, p.device_bytes(), C.byref(dp)) == lib.OK
+    doubles = image[dp.tables[14]:dp.tables[14] + 4 * dp.counts[14]].reshape(-1, 4)
+    shard = image[dp.tables[15]:dp.tables[15] + cp + 1]
+    assert dp.counts[15] == cp + 1 and shard[0] == 0 and shard[-1] == len(doubles)
+    T, slots, W0 = sum(docs), (sinks + 7) // 8 * 8, min(window, sum(docs))
+    seen, queries = np.zeros((T, T), int), np.zeros(T, int)
+    for j in range(cp):
+        for piece, q0, first, second in doubles[shard[j]:shard[j + 1]]:
+            owner, _, start, end, ds, sb, sc, _ = t[PIECES][piece]
+            n = first + second
+            assert owner == j and start <= q0 and q0 + n <= end and 1 <= first <= 128 and 0 <= second <= 128
+            q = np.arange(q0, q0 + n)
+            queries[q] += 1
+            take = slots if q[-1] - W0 >= ds and sinks else 0
+            for s in range(ds, ds + sinks if take else ds):
+                seen[q[s <= q - W0], s] += 1
+            for _, _, ks, ln in t[SEGS][sb:sb + sc]:
+                key = np.arange(max(ks, q0 - W0 + 1), min(ks + ln, q[-1] + 1))
+                seen[np.ix_(q, key)] += (key <= q[:, None]) & (q[:, None] - key < W0)
+    assert (queries == 1).all() and np.array_equal(seen, mask(docs, window, sinks).astype(int))
+
+
 def test_windows_of_a_plan_are_independent(lib):
     base = lib.Plan([1000, 200], 2, "perdoc")
     image = base.device_image()
