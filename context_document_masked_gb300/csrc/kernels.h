@@ -266,7 +266,8 @@ constexpr int kResNormMaxCtas = 1216;
 constexpr int kResNormChunk = 128;   // rows of a chunk at most (plan.h, TB_ROWS)
 struct ResNormParams {
   const int32_t* chunks;   // TB_ROWS entries of a shard; null: all tokens
-  int64_t places;          // tokens, or kResNormChunk for each chunk
+  int64_t units;           // tokens, or of a shard kResNormChunk / unit_rows for each chunk
+  int32_t unit_rows;       // 1 or kResNormChunk
   int32_t T, n, groups;    // (groups: set by the launch)
   int32_t post_norm, gate_fn, res_f32, w_f32, add_dw;
   float eps, res_scale, branch_scale;

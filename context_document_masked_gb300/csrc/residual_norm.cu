@@ -239,30 +239,36 @@ __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_g
 template <int N>
 __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Row k of the launch: a token, or -1 for a place past a chunk's end. Chunks are
-// runs of at most kResNormChunk rows of a shard; none for all tokens in order.
-__device__ __forceinline__ int64_t row_at(const ResNormParams& p, int64_t k) {
-  if (!p.chunks) return k;
-  const int32_t* c = p.chunks + 2 * (k / kResNormChunk);
-  const int r = (int)(k % kResNormChunk), first = __ldg(c), n = __ldg(c + 1);
-  if constexpr (kDeviceChecks) {
-    if (first < 0 || n < 0 || first > p.T - n) return -1;
-  }
-  return r < n ? first + r : -1;
-}
-
-// The first place from k on, in steps of the grid, that holds a token: the
-// token, or -1 at the end.
-__device__ __forceinline__ int64_t next_row(const ResNormParams& p, int64_t& k) {
-  for (; k < p.places; k += gridDim.x) {
-    const int64_t t = row_at(p, k);
-    if (t >= 0) {
-      k += gridDim.x;
-      return t;
+// The tokens of a CTA: units of the launch in steps of the grid. A unit is one
+// token, or of a shard `unit_rows` rows of a chunk (a run of at most kResNormChunk
+// rows): one, as rows have to spread over the SMs, or the whole chunk where chunks
+// are short (documents of a few tokens), whose units would otherwise mostly be empty.
+struct RowWalk {
+  int64_t unit;
+  int row, end;
+  __device__ __forceinline__ RowWalk() : unit(blockIdx.x), row(0), end(0) {}
+  // The next token, or -1.
+  __device__ __forceinline__ int64_t next(const ResNormParams& p) {
+    if (!p.chunks) {
+      const int64_t t = unit;
+      unit += gridDim.x;
+      return t < p.units ? t : -1;
     }
+    while (row >= end) {
+      if (unit >= p.units) return -1;
+      const int per = kResNormChunk / p.unit_rows, sub = (int)(unit % per) * p.unit_rows;
+      const int32_t* c = p.chunks + 2 * (unit / per);
+      const int first = __ldg(c), n = __ldg(c + 1);
+      unit += gridDim.x;
+      if constexpr (kDeviceChecks) {
+        if (first < 0 || n < 0 || first > p.T - n) continue;
+      }
+      row = first + sub;
+      end = first + min(n, sub + p.unit_rows);
+    }
+    return row++;
   }
-  return -1;
-}
+};
 
 __device__ __forceinline__ const char* at(const void* base, int64_t row_bytes, int64_t t) {
   return static_cast<const char*>(base) + row_bytes * t;
@@ -285,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormPa
   const int step = blockDim.x;
   int half = 0, stage = 0;
   const float inv_n = 1.f / p.n;
-  int64_t k = blockIdx.x;
+  RowWalk walk;
   auto place = [&](int st, int c) { return ring + (st * G + c) * kWords * step + threadIdx.x; };
   auto fetch = [&](int st, int64_t t) {
     if constexpr (RING) {
@@ -309,10 +315,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormPa
         Raw<F32>::clear(place(st, c) + 2 * step);
       }
   }
-  int64_t t = next_row(p, k);
+  int64_t t = walk.next(p);
   fetch(0, t);
   for (int64_t next; t >= 0; t = next, stage ^= 1) {
-    next = next_row(p, k);
+    next = walk.next(p);
     if constexpr (RING && F32) __syncwarp();  // the lanes have read the last row
     fetch(stage ^ 1, next);
     Raw<F32> xr[G];
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNo
   for (int c = 0; c < G; ++c)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc_pre[c].v[j] = acc_post[c].v[j] = 0;
-  int64_t k = blockIdx.x;
+  RowWalk walk;
   auto place = [&](int st, int c) { return ring + (st * G + c) * kWords * step + threadIdx.x; };
   auto fetch = [&](int st, int64_t t) {
     if constexpr (RING) {
@@ -424,10 +430,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNo
         for (int a = 0; a < 2; ++a) Raw<F32>::clear(place(st, c) + (3 + a * kRes) * step);
       }
   }
-  int64_t t = next_row(p, k);
+  int64_t t = walk.next(p);
   fetch(0, t);
   for (int64_t next; t >= 0; t = next, stage ^= 1) {
-    next = next_row(p, k);
+    next = walk.next(p);
     if constexpr (RING && F32) __syncwarp();  // the lanes have read the last row
     fetch(stage ^ 1, next);
     Raw<F32> xr[G], dr[G];
@@ -565,7 +571,7 @@ static int start(Kernel kernel, int bytes, int ctas, int most, int threads, cons
     return 0;
   // As many CTAs as are resident at once: by registers, by shared memory, and 32 an SM.
   const int fit = std::max(1, std::min({ctas, 227 * 1024 / (bytes + 2048), 32}));
-  const int grid = (int)std::min({p.places, (int64_t)fit * p.num_sms, (int64_t)most});
+  const int grid = (int)std::min({p.units, (int64_t)fit * p.num_sms, (int64_t)most});
   kernel<<<grid, threads, bytes, st>>>(p);
   return grid;
 }
@@ -598,7 +604,7 @@ int launch_res_norm(const ResNormParams& a, cudaStream_t st) {
   ResNormParams p = a;
   p.groups = p.n / kV;
   int grid = 0;
-  if (p.places > 0) {
+  if (p.units > 0) {
     if (p.dx)
       grid = p.n <= 1024   ? start<1, 128, 5, true, true>(p, st)
              : p.n <= 2048 ? start<2, 128, 4, true, true>(p, st)

@@ -193,6 +193,22 @@ def test_shards(cuda, policy, cp):
         within(y, bwd[k], k)
 
 
+def test_many_short_documents(cuda):
+    """Shards of many runs of a few rows, which are taken run by run."""
+    docs = [1, 2, 5] * 600
+    s, n = session(docs, 2, "wholedoc"), 64
+    T = sum(docs)
+    x = make(T, n, seed=4)
+    fwd, bwd = forward_reference(x, KW), backward_reference(x, KW)
+    outs = {k: torch.full((T, n), torch.nan, dtype=torch.bfloat16, device="cuda") for k in ("x_out", "h", "dx", "dy", "dgate")}
+    dw = {k: torch.zeros(n, device="cuda") for k in ("dw_post", "dw_pre")}
+    for j in range(2):
+        run_forward(s, x, KW, shard=j, x_out=outs["x_out"], h=outs["h"])
+        run_backward(s, x, KW, shard=j, dx=outs["dx"], dy=outs["dy"], dgate=outs["dgate"], **dw)
+    for k, y in (outs | dw).items():
+        within(y, (fwd | bwd)[k], k)
+
+
 def test_a_shard_without_tokens(cuda):
     s = session([3], 4, "perdoc")
     empty = [j for j in range(4) if len(s.plan.query_indices(j)) == 0]
