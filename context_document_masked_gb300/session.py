@@ -246,6 +246,8 @@ class CPAttention:
             dgate = rows(gate, gate.dtype) if dgate is None and gate is not None else dgate
             add = not zero_grads and (dw_post is not None or dw_pre is not None)  # to the given ones: new ones start at zero
             make = torch.zeros if add else torch.empty
+            if dw_post is None and dw_pre is None and w_post is not None and w_pre is not None:
+                dw_post, dw_pre = make(2, n, dtype=torch.float32, device=self.device).unbind(0)
             if dw_post is None and w_post is not None:
                 dw_post = make(n, dtype=torch.float32, device=self.device)
             if dw_pre is None and w_pre is not None:
