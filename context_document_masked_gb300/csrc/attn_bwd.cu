@@ -71,7 +71,14 @@
 // end a window after its last key. The sinks outside a query's window ride in
 // the first rows of the key tile that holds the query's own key, so no unit has
 // all of a document's queries and no step is for the sinks alone; their dK and
-// dV leave every such unit in a box of their own.
+// dV leave every such unit in a box of their own. With the preprocess: 32K packed
+// sequence (32/8 heads, d = 128, 4 sinks), window 1024 1.90 ms, 128 0.91 ms, of which
+// the preprocess 0.35; one document of 64K (16/2 heads), window 2048: 3.45 ms. Bound:
+// the compute warps' P and dS phases (3,600 to 4,000 cycles a step) and the dQ
+// reduce-adds (0.80 ms without them at window 128, 2.71 at 2048). Nothing gained:
+// units decoded by the producer, LSE and D loaded a step ahead, the rows of coming
+// steps brought into L2, a part of the epilogue given to the dQ warps; for d = 64, where
+// there is room, two K/V stages, three of Q, two of dO and a second S (497 -> 542 us).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -52,9 +52,21 @@
 //
 // Under a window (a separate instantiation, for windowed plans), query i sees the
 // keys i - window < j <= i and, of those before, its document's first `sinks`.
-// A query tile walks the keys from its first row's window on; the sinks have the
-// first rows of its first key tile (TMA boxes of their own), and the plan makes
-// the query tiles as long as the key tiles then hold (WindowWalker).
+// - A query tile walks the keys from its first row's window on; the sinks have the
+//   first rows of its first key tile (TMA boxes of their own), so they cost no tile,
+//   and the plan makes the query tiles as long as whole key tiles then hold.
+// - Units are short, and between two of them each role read the tables (four loads
+//   one after another): the producer decodes a unit ahead into shared memory
+//   (WindowUnit). 32K packed sequence (32/8 heads, d = 128), window 128: 323 -> 308 us.
+// - The head of an odd group that has no partner takes two query tiles instead of
+//   one tile twice: 16 heads of 64 without groups, window 256, 297 -> 214 us.
+// 32K packed sequence, 4 sinks: window 1024 661 us, 128 308 us; one document of 64K,
+// window 4096: 3.38 ms, 1.26 PFLOP/s of pairs that are seen. Bound: long windows as
+// without one (the softmax chain against the other head's MMAs); short ones by the
+// chain of a unit, about 12,000 cycles for two key tiles (tensor pipe 25% busy, DRAM
+// 33%). Slower: the softmax by runs of 32 columns, those that nobody sees left out
+// (410 us for 308), or masked run by run (622): branches around parts of the row's
+// 128 registers make it spill.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

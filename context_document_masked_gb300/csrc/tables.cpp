@@ -14,6 +14,10 @@
 //     points), so that tile is one unit whose steps run over both pieces'
 //     query tiles: dK/dV of the tile leave the kernel once, not twice;
 //   - gather runs (<= kCopyRows rows) and preprocess row chunks.
+// A windowed plan's tables hold the window's part: segments from a window before
+// the piece on, query and key tiles of as many rows as fill whole tiles of the other
+// side beside the sinks, units whose queries end a window after their keys, one
+// unit a piece, and double query tiles in the place of the ring tables.
 // Tiles are listed piece by piece (pieces ordered by their longest tile) and,
 // inside a piece, longest first (by the number of tile pairs they cover): the
 // CTAs running at the same time then share one piece's query rows and keys

@@ -156,7 +156,8 @@ class CPAttention:
             if dq is None:
                 dq = torch.empty(self.T, self.hq, self.d, dtype=torch.float32, device=self.device)
             if dk is None and dv is None:  # one fill for both
-                dk, dv = torch.zeros(2, self.T, self.hkv, self.d, dtype=torch.float32, device=self.device).unbind(0)
+                both = torch.zeros(2, self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
+                dk, dv = both[0], both[1]
             else:
                 if dk is None:
                     dk = torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
@@ -246,8 +247,6 @@ class CPAttention:
             dgate = rows(gate, gate.dtype) if dgate is None and gate is not None else dgate
             add = not zero_grads and (dw_post is not None or dw_pre is not None)  # to the given ones: new ones start at zero
             make = torch.zeros if add else torch.empty
-            if dw_post is None and dw_pre is None and w_post is not None and w_pre is not None:
-                dw_post, dw_pre = make(2, n, dtype=torch.float32, device=self.device).unbind(0)
             if dw_post is None and w_post is not None:
                 dw_post = make(n, dtype=torch.float32, device=self.device)
             if dw_pre is None and w_pre is not None:
