@@ -203,7 +203,10 @@ class Plan:
         and the document's first `sinks`."""
         p = object.__new__(Plan)
         p._ptr = C.c_void_p()
-        _check(_lib.fcp_plan_window(self._ptr, window, sinks, C.byref(p._ptr)), "fcp_plan_window")
+        # A length above 32 bits is one that cuts nothing, not its low half.
+        low, high = -1, 2**31 - 1
+        _check(_lib.fcp_plan_window(self._ptr, max(low, min(window, high)), max(low, min(sinks, high)), C.byref(p._ptr)),
+               "fcp_plan_window")
         p.doclens, p.cp, p.policy = self.doclens, self.cp, self.policy
         p.window, p.sinks = window, sinks
         return p

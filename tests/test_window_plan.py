@@ -250,3 +250,13 @@ def test_session_refuses_sinks_without_a_window(lib):
     from context_document_masked_gb300.session import CPAttention
     with pytest.raises(ValueError, match="window"):
         CPAttention([64], 1, "perdoc", 4, 2, 64, device="cpu", sinks=4)
+
+
+def test_lengths_above_32_bits(lib):
+    p = lib.Plan([300, 212], 2, "hybrid")
+    whole = p.windowed(512, 4)
+    for window in (2**31 - 1, 2**31, 2**32 + 1, 2**63):
+        assert p.windowed(window, 4).stats() == whole.stats(), window
+    for window, sinks in ((-2**32 + 8, 0), (-2**31 - 1, 0), (8, 2**32), (8, 2**32 + 4), (8, -2**32)):
+        with pytest.raises(lib.FcpError):
+            p.windowed(window, sinks)
