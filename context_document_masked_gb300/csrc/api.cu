@@ -1038,6 +1038,39 @@ struct Rows {
   bool same(const Rows& o) const { return at == o.at && stride * size == o.stride * o.size; }
 };
 
+// An operand that is one run of bytes: a weight, its gradient, the workspace.
+struct Flat {
+  const void* at;
+  int64_t bytes;
+  bool meets(const Flat& o) const {
+    const uintptr_t a = (uintptr_t)at, b = (uintptr_t)o.at;
+    return at && o.at && a < b + (uintptr_t)o.bytes && b < a + (uintptr_t)bytes;
+  }
+  // Of the rows that end behind its start, whether the first begins before its end.
+  bool meets(const Rows& o, const fcp::ResNormParams& p) const {
+    if (!at || !o.at) return false;
+    const RowSpan r = o.span(p);
+    const int64_t before = (int64_t)((uintptr_t)at - r.at) - r.len;  // rows that begin here or earlier end too soon
+    const int64_t t = before < 0 ? 0 : before / r.stride + 1;
+    return t < p.T && r.at + (uintptr_t)(t * r.stride) < (uintptr_t)at + (uintptr_t)bytes;
+  }
+};
+
+// No output's rows meet a flat operand, and no flat output (the first n_out of
+// them) an input's rows or another flat operand.
+static bool flats_apart(const fcp::ResNormParams& p, const Flat* f, int n_f, int n_flat_out, const Rows* out, int n_out,
+                        const Rows* in, int n_in) {
+  for (int a = 0; a < n_f; ++a) {
+    for (int o = 0; o < n_out; ++o)
+      if (f[a].meets(out[o], p)) return false;
+    for (int i = 0; a < n_flat_out && i < n_in; ++i)
+      if (f[a].meets(in[i], p)) return false;
+    for (int b = 0; a < n_flat_out && b < n_f; ++b)
+      if (b != a && f[a].meets(f[b])) return false;
+  }
+  return true;
+}
+
 // No output meets another operand, but for out[i] on in[i] itself.
 static bool rows_apart(const fcp::ResNormParams& p, const Rows* out, int n_out, const Rows* in, int n_in) {
   for (int o = 0; o < n_out; ++o) {
@@ -1063,6 +1096,9 @@ int fcp_residual_norm(const void* x, int64_t x_stride, const void* y, int64_t y_
   if (!x_out && (y || rn->res_scale != 1.f || !h)) return FCP_ERR_INVALID_ARG;
   if ((x_out && !out[0].ok(p)) || !h != !rn->pre_norm || (h && !out[1].ok(p))) return FCP_ERR_INVALID_ARG;
   if (!rows_apart(p, out, 2, in, 4)) return FCP_ERR_INVALID_ARG;
+  const int64_t w_bytes = (int64_t)n * (p.w_f32 ? 4 : 2);
+  const Flat flat[2] = {{w_post, w_bytes}, {w_pre, w_bytes}};
+  if (!flats_apart(p, flat, 2, 0, out, 2, in, 4)) return FCP_ERR_INVALID_ARG;
   p.x = x;
   p.x_row = x_stride * res;
   p.y_row = y_stride * 2;
@@ -1093,8 +1129,11 @@ int fcp_residual_norm_bwd(const void* dh, int64_t dh_stride, const void* dx_out,
     return FCP_ERR_INVALID_ARG;
   if ((dw_post && !y) || (dw_pre && !dh)) return FCP_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(dw_post) & 3) || (reinterpret_cast<uintptr_t>(dw_pre) & 3)) return FCP_ERR_INVALID_ARG;
-  if (dw_post && dw_pre && ranges_meet(dw_post, dw_pre, n)) return FCP_ERR_INVALID_ARG;
   if (!rows_apart(p, out, 3, in, dh ? 5 : 3)) return FCP_ERR_INVALID_ARG;
+  const int64_t w_bytes = (int64_t)n * (p.w_f32 ? 4 : 2);
+  const Flat flat[5] = {{dw_post, (int64_t)n * 4}, {dw_pre, (int64_t)n * 4},
+                        {dw_post || dw_pre ? ws : nullptr, fcp::res_norm_ws_bytes(n)}, {w_post, w_bytes}, {w_pre, w_bytes}};
+  if (!flats_apart(p, flat, 5, 3, out, 3, in, dh ? 5 : 3)) return FCP_ERR_INVALID_ARG;
   if (dw_post || dw_pre) {
     if (!ws || !aligned16(ws)) return FCP_ERR_INVALID_ARG;
     if (ws_bytes < fcp::res_norm_ws_bytes(n)) return FCP_ERR_CAPACITY;

@@ -133,3 +133,37 @@ def test_widths_of_the_workloads(lib):
     for cfg in range(1, 6):
         w = synth.WORKLOADS[cfg]
         assert lib.residual_norm_ws_bytes(w.Hq * w.d) > 0
+
+
+def test_outputs_on_weights_their_gradients_and_the_workspace(lib, bound):
+    _, dp = bound
+    inv, cap = lib.ERR_INVALID_ARG, lib.ERR_CAPACITY
+    n, T = 64, 64
+    row, ws = 2 * n, lib.residual_norm_ws_bytes(64)
+    for k in ("x_out", "h"):
+        for w in (4, 5):
+            assert forward(lib, dp, **{k: STEP * w}) == inv, (k, w)
+            assert forward(lib, dp, **{k: STEP * w + 4 * n - 16}) == inv, (k, w)
+            assert forward(lib, dp, **{k: STEP * w - (T - 1) * row - 16}) == inv, (k, w)  # its last row
+    for k in ("dx", "dy", "dgate"):
+        for o, size in ((6, 4 * n), (7, 4 * n), (11, 4 * n), (12, 4 * n), (13, ws)):
+            assert backward(lib, dp, **{k: STEP * o + size - 16}) == inv, (k, o)
+            assert backward(lib, dp, **{k: STEP * o - (T - 1) * row - 16}) == inv, (k, o)
+            assert backward(lib, dp, **{k: STEP * o + size}) == cap, (k, o)
+            assert backward(lib, dp, **{k: STEP * o - T * row}) == cap, (k, o)
+    for k, size in (("dw_post", 4 * n), ("dw_pre", 4 * n), ("ws", ws)):
+        for o in (1, 2, 3, 4, 5):
+            assert backward(lib, dp, **{k: STEP * o + T * row - 16}) == inv, (k, o)
+            assert backward(lib, dp, **{k: STEP * o - size + 16}) == inv, (k, o)
+            assert backward(lib, dp, **{k: STEP * o + T * row}) == backward(lib, dp, **{k: STEP * o - size}) == cap, (k, o)
+        for o in (6, 7):
+            assert backward(lib, dp, **{k: STEP * o}) == inv, (k, o)
+    for k in ("dw_post", "dw_pre"):
+        assert backward(lib, dp, **{k: STEP * 13 + ws - 4}) == inv and backward(lib, dp, **{k: STEP * 13 + ws}) == cap
+    # Between the rows of a slice there is room; beside it too.
+    for k, size in (("dw_post", 4 * n), ("dw_pre", 4 * n)):
+        wide = dict(s_dx=4 * n, dx=STEP * 20)
+        assert backward(lib, dp, **wide, **{k: STEP * 20 + 8 * n * 3 + row}) == cap, k
+        assert backward(lib, dp, **wide, **{k: STEP * 20 + 8 * n * 3 + row - 4}) == inv, k
+        assert backward(lib, dp, **wide, **{k: STEP * 20 + 8 * n * 4 - size + 4}) == inv, k
+        assert backward(lib, dp, **wide, **{k: STEP * 20 + 8 * n * (T - 1) + row}) == cap, k
