@@ -238,6 +238,8 @@ class CPAttention:
         weights are added to dw_post and dw_pre where they are given (zero_grads: written there). Its
         workspace is made in the order of the call's stream."""
         like = x_out if x_out is not None else dx_out
+        if like is None:
+            raise ValueError("residual_norm_backward: x_out or dx_out is needed")
         n = like.shape[1]
         with _on_stream(stream):
             def rows(t, dtype):

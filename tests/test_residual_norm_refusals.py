@@ -167,3 +167,10 @@ def test_outputs_on_weights_their_gradients_and_the_workspace(lib, bound):
         assert backward(lib, dp, **wide, **{k: STEP * 20 + 8 * n * 3 + row - 4}) == inv, k
         assert backward(lib, dp, **wide, **{k: STEP * 20 + 8 * n * 4 - size + 4}) == inv, k
         assert backward(lib, dp, **wide, **{k: STEP * 20 + 8 * n * (T - 1) + row}) == cap, k
+
+
+def test_session_backward_needs_a_residual(lib):
+    from context_document_masked_gb300.session import CPAttention
+    s = object.__new__(CPAttention)
+    with pytest.raises(ValueError, match="x_out or dx_out"):
+        s.residual_norm_backward(None, None, None)
