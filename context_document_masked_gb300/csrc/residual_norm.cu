@@ -23,13 +23,21 @@
 // Bound: device memory, each operand read once and each result written once; on the
 // way there instructions and, in the gradient, registers (its sums take 32 of a
 // thread's 128, which leaves 16 warps an SM). 65536 rows of 8192, bf16 residual,
-// sigmoid gate: 874 us, 6.14 TB/s (0.91 of the measured copy rate); gradient of
-// 32768 rows of 4096: 398 us, 5.39 TB/s (0.79). From 1264 and 887: registers that a launch
+// sigmoid gate: 849 us, 6.32 TB/s (0.93 of the measured copy rate); gradient of
+// 32768 rows of 4096: 385 us, 5.58 TB/s (0.82; with an fp32 residual 470 us, 6.28 TB/s). From 1264 and 887: registers that a launch
 // bound of 1024 threads had cut to 64 (1103, 546), the ring (1058, 511), pairs of values an
 // instruction and four sums in six shuffles (952, 504), the gate's form at compile
 // time (898, 464), the operands' presence too, and zeros for groups past a row's end in
-// place of branches (884, 401). Slower in the gradient: four groups a thread (581: eight
+// place of branches (884, 401), shared memory for a CTA's own number of warps (849, 385; fp32 585 to
+// 470, two CTAs an SM). Slower in the gradient: four groups a thread (581: eight
 // warps an SM), one (1162: spills), fp32 pairs kept for raw bf16 (488).
+//
+// Rows of more than 8192 values. Forward: the ring where it fits the shared memory, else the next
+// row is fetched into L2 (16384 rows of 16384: bf16 566 to 505 us, fp32 820 to 626; of 9216 396 to 296, 448
+// to 364). Gradient: a row on two CTAs of a cluster, which exchange their sums by each other's
+// shared memory, where one CTA with four groups a thread and no ring took 1392 us (now 1221), fp32 1806 (1456); at 9216
+// 929 (886), 1066 (953). Its 0.52 to 0.6 of the copy rate: both cluster barriers of a row are
+// waited for by every warp of an SM. Clusters of more and smaller CTAs, two an SM, were slower (1936 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -47,19 +55,17 @@ using namespace dev;
 namespace {
 
 constexpr int kV = 8;  // values of a group: 16 bytes of bf16
-constexpr int kMaxWarps = 32;
 
-// Groups a thread holds. The forward: one up to 1024 values, two above (16384
-// values: 1024 threads). The gradient, whose instructions a row and thread count
-// for more: up to four.
-__host__ __device__ constexpr int groups_of(int n, bool bwd) {
-  return n <= 1024 ? 1 : bwd && n > 8192 ? 4 : 2;
+// A thread holds one group up to 1024 values, two above (the forward's 16384:
+// 1024 threads). The gradient takes a row of more than 8192 values by a cluster of
+// two CTAs, half a row each: its registers do not suffice for 1024 threads.
+constexpr bool paired(int n, bool bwd) { return bwd && n > 8192; }
+constexpr int threads_of(int n, bool bwd) {
+  const int groups = paired(n, bwd) ? (n / kV + 1) / 2 : n / kV, per = n <= 1024 ? 32 : 64;
+  return (groups + per - 1) / per * 32;
 }
-__host__ __device__ constexpr int threads_of(int n, bool bwd) {
-  return (n / kV + 32 * groups_of(n, bwd) - 1) / (32 * groups_of(n, bwd)) * 32;
-}
-// CTAs of the gradient at most (each writes a row of the weights' sums).
-int most_ctas(int n) { return std::min(kResNormMaxCtas, 152 * 512 / threads_of(n, true)); }
+// CTAs, or pairs of them, of the gradient at most (each writes a row of the weights' sums).
+int most_sums(int n) { return std::min(kResNormMaxCtas, 152 * 512 / threads_of(n, true) / (paired(n, true) ? 2 : 1)); }
 
 // The arithmetic runs on pairs of values (f32x2): with one value an instruction
 // its issue bound the kernels, not memory. A group is four pairs.
@@ -111,6 +117,11 @@ struct Raw {
     }
     place[0] = make_uint4(0, 0, 0, 0);
   }
+  // Into L2 by one lane a line.
+  static __device__ __forceinline__ void ahead(const void* row, int i) {
+    const char* line = static_cast<const char*>(row) + (F32 ? 32 : 16) * (int64_t)i;
+    if (!(threadIdx.x & (F32 ? 3 : 7))) asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+  }
   static __device__ __forceinline__ void copy(uint4* to, const uint4* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
   }
@@ -161,28 +172,60 @@ __device__ __forceinline__ float sum_of(uint64_t a) {
   return lo + hi;
 }
 
-// Sums of one, or of four values at once, over the CTA's threads (every thread
-// gets them). Four: after two exchanges a lane holds one of the values, so they
-// take 6 shuffles, not 20. A half is not read any more when the call after the next
-// one's values arrive there.
-struct Sums {
-  float4 four[2][kMaxWarps];
-  float one[2][kMaxWarps];  // (zeros in the places of warps that there are not)
+// Sums of one, or of four values at once, over the threads of the CTA or of the
+// pair of CTAs (every thread gets them). Four: after two exchanges a lane holds
+// one of the values, so they take 6 shuffles, not 20. A half is not read any more
+// when the call after the next one's values arrive there. In whole lines of 128
+// bytes, so that the ring behind them starts on one (else 4 to 6% slower), and for
+// the CTA's own number of warps: only then two CTAs with rings of 4096 values and
+// an fp32 residual fit an SM (585 to 470 us).
+template <int WARPS>
+struct alignas(128) Sums {
+  float4 four[2][WARPS];
+  float one[2][WARPS];  // (zeros in the places of warps that there are not)
 };
-__device__ __forceinline__ void init(Sums& sh) {
-  for (int i = threadIdx.x; i < 2 * kMaxWarps; i += blockDim.x) sh.one[i / kMaxWarps][i % kMaxWarps] = 0.f;
+template <int WARPS>
+__device__ __forceinline__ void init(Sums<WARPS>& sh) {
+  for (int i = threadIdx.x; i < 2 * WARPS; i += blockDim.x) sh.one[i / WARPS][i % WARPS] = 0.f;
   __syncthreads();
 }
+// A pair's warps write into both CTAs' shared memory, so each CTA reads its own.
+__device__ __forceinline__ uint32_t pair_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+template <bool PAIR>
+__device__ __forceinline__ void put(float* to, float v) {
+  *to = v;
+  if constexpr (PAIR) {
+    uint32_t other;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(other) : "r"(smem_u32(to)), "r"(pair_rank() ^ 1));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(other), "f"(v) : "memory");
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (PAIR)
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+  else
+    __syncthreads();
+}
 __device__ __forceinline__ float shuffled(float v, int m) { return v + __shfl_xor_sync(0xffffffffu, v, m); }
-__device__ __forceinline__ float row_sum(float v, Sums& sh, int& half) {
+template <bool PAIR, int WARPS>
+__device__ __forceinline__ float row_sum(float v, Sums<WARPS>& sh, int& half) {
 #pragma unroll
   for (int m = 16; m; m >>= 1) v = shuffled(v, m);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return v;
+  int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+  if (!PAIR && warps == 1) return v;
+  if constexpr (PAIR) {
+    if (pair_rank()) warp += warps;
+    warps *= 2;
+  }
   float* s = sh.one[half];
   half ^= 1;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
+  if ((threadIdx.x & 31) == 0) put<PAIR>(s + warp, v);
+  sync_all<PAIR>();
   v = 0.f;
   for (int w = 0; w < warps; w += 4) {
     const float4 a = *reinterpret_cast<const float4*>(s + w);
@@ -190,7 +233,8 @@ __device__ __forceinline__ float row_sum(float v, Sums& sh, int& half) {
   }
   return v;
 }
-__device__ __forceinline__ float4 row_sums(float4 v, Sums& sh, int& half) {
+template <bool PAIR, int WARPS>
+__device__ __forceinline__ float4 row_sums(float4 v, Sums<WARPS>& sh, int& half) {
   const int lane = threadIdx.x & 31;
   const bool odd = lane & 1, second = lane & 2;
   // Even lanes keep the sums of x and y, odd ones those of z and w; then one each.
@@ -199,14 +243,18 @@ __device__ __forceinline__ float4 row_sums(float4 v, Sums& sh, int& half) {
   float t = (second ? b : a) + __shfl_xor_sync(0xffffffffu, second ? a : b, 2);
 #pragma unroll
   for (int m = 4; m < 32; m <<= 1) t = shuffled(t, m);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1)  // lane 0 holds x's sum, 1 z's, 2 y's, 3 w's
+  int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+  if (!PAIR && warps == 1)  // lane 0 holds x's sum, 1 z's, 2 y's, 3 w's
     return make_float4(__shfl_sync(0xffffffffu, t, 0), __shfl_sync(0xffffffffu, t, 2), __shfl_sync(0xffffffffu, t, 1),
                        __shfl_sync(0xffffffffu, t, 3));
+  if constexpr (PAIR) {
+    if (pair_rank()) warp += warps;
+    warps *= 2;
+  }
   float4* s = sh.four[half];
   half ^= 1;
-  if (lane < 4) reinterpret_cast<float*>(s + (threadIdx.x >> 5))[(lane >> 1) | (lane & 1) << 1] = t;
-  __syncthreads();
+  if (lane < 4) put<PAIR>(reinterpret_cast<float*>(s + warp) + ((lane >> 1) | (lane & 1) << 1), t);
+  sync_all<PAIR>();
   float4 r = s[0];
   for (int w = 1; w < warps; ++w) {
     const float4 o = s[w];
@@ -252,19 +300,20 @@ __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_g
 template <int N>
 __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The tokens of a CTA: units of the launch in steps of the grid. A unit is one
+// The tokens of a CTA (or pair): units of the launch in steps of the grid. A unit is one
 // token, or of a shard `unit_rows` rows of a chunk (a run of at most kResNormChunk
 // rows): one, as rows have to spread over the SMs, or the whole chunk where chunks
 // are short (documents of a few tokens), whose units would otherwise mostly be empty.
+template <int PER = 1>
 struct RowWalk {
   int64_t unit;
   int row, end;
-  __device__ __forceinline__ RowWalk() : unit(blockIdx.x), row(0), end(0) {}
+  __device__ __forceinline__ RowWalk() : unit(blockIdx.x / PER), row(0), end(0) {}
   // The next token, or -1.
   __device__ __forceinline__ int64_t next(const ResNormParams& p) {
     if (!p.chunks) {
       const int64_t t = unit;
-      unit += gridDim.x;
+      unit += gridDim.x / PER;
       return t < p.units ? t : -1;
     }
     while (row >= end) {
@@ -272,7 +321,7 @@ struct RowWalk {
       const int per = kResNormChunk / p.unit_rows, sub = (int)(unit % per) * p.unit_rows;
       const int32_t* c = p.chunks + 2 * (unit / per);
       const int first = __ldg(c), n = __ldg(c + 1);
-      unit += gridDim.x;
+      unit += gridDim.x / PER;
       if constexpr (kDeviceChecks) {
         if (first < 0 || n < 0 || first > p.T - n) continue;
       }
@@ -298,13 +347,13 @@ constexpr int kFwdWords[2] = {3, 4}, kBwdWords[2] = {5, 7};  // bf16, fp32 resid
 template <int G, int THREADS, int CTAS, bool RING, bool F32, Gate GATE>
 __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormParams p) {
   extern __shared__ uint4 ring[];
-  __shared__ __align__(16) Sums sh;
+  __shared__ Sums<THREADS / 32> sh;
   init(sh);
   constexpr int kWords = kFwdWords[F32];
   const int step = blockDim.x;
   int half = 0, stage = 0;
   const float inv_n = 1.f / p.n;
-  RowWalk walk;
+  RowWalk<> walk;
   auto place = [&](int st, int c) { return ring + (st * G + c) * kWords * step + threadIdx.x; };
   auto fetch = [&](int st, int64_t t) {
     if constexpr (RING) {
@@ -318,6 +367,15 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormPa
         Raw<F32>::fetch(at_c + 2 * step, at(p.x, p.x_row, t), i, p.groups);
       }
       async_commit();
+    } else if (t >= 0) {
+#pragma unroll
+      for (int c = 0; c < G; ++c) {
+        const int i = threadIdx.x + c * step;
+        if (i >= p.groups) continue;
+        if (p.y) Raw<false>::ahead(at(p.y, p.y_row, t), i);
+        if constexpr (GATE != kNoGate) Raw<false>::ahead(at(p.gate, p.gate_row, t), i);
+        Raw<F32>::ahead(at(p.x, p.x_row, t), i);
+      }
     }
   };
   if constexpr (RING) {
@@ -361,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormPa
       for (int c = 0; c < G; ++c)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s2 = f2_fma(yr[c].pair(j), yr[c].pair(j), s2);
-      ry = rsqrtf(row_sum(sum_of(s2), sh, half) * inv_n + p.eps);
+      ry = rsqrtf(row_sum<false>(sum_of(s2), sh, half) * inv_n + p.eps);
     }
     const uint64_t a2 = both(p.res_scale), b2 = both(p.branch_scale * ry);
     uint64_t s2 = 0;
@@ -387,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormPa
       if (p.x_out && there) store8<F32>(at(p.x_out, p.x_out_row, t), i, x[c]);
     }
     if (!p.h) continue;
-    const uint64_t r2 = both(rsqrtf(row_sum(sum_of(s2), sh, half) * inv_n + p.eps));
+    const uint64_t r2 = both(rsqrtf(row_sum<false>(sum_of(s2), sh, half) * inv_n + p.eps));
 #pragma unroll
     for (int c = 0; c < G; ++c) {
       const int i = threadIdx.x + c * step;
@@ -402,13 +460,16 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_kernel(const ResNormPa
 
 // FULL: every operand but the gate is there and the weights are fp32, as in nearly
 // every call of a stack of layers: no branch for each group and operand.
-template <int G, int THREADS, int CTAS, bool RING, bool F32, Gate GATE, bool FULL>
+// PAIR: a row's first groups on one CTA of a cluster, the rest on the other.
+template <int G, int THREADS, int CTAS, bool PAIR, bool F32, Gate GATE, bool FULL>
 __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNormParams p) {
   extern __shared__ uint4 ring[];
-  __shared__ __align__(16) Sums sh;
+  __shared__ Sums<THREADS / 32 * (PAIR ? 2 : 1)> sh;
   init(sh);
+  if constexpr (PAIR) sync_all<true>();  // the other CTA is there, its zeros too
   constexpr int kWords = kBwdWords[F32], kRes = F32 ? 2 : 1;
-  const int step = blockDim.x;
+  const int step = blockDim.x, share = (p.groups + 1) / 2;
+  const int first = PAIR ? (int)pair_rank() * share : 0, last = PAIR ? min(p.groups, first + share) : p.groups;  // this CTA's groups
   int half = 0, half4 = 0, stage = 0;
   const float inv_n = 1.f / p.n;
   Pairs acc_pre[G], acc_post[G];
@@ -416,70 +477,54 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNo
   for (int c = 0; c < G; ++c)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc_pre[c].v[j] = acc_post[c].v[j] = 0;
-  RowWalk walk;
+  RowWalk<PAIR ? 2 : 1> walk;
   auto place = [&](int st, int c) { return ring + (st * G + c) * kWords * step + threadIdx.x; };
   auto fetch = [&](int st, int64_t t) {
-    if constexpr (RING) {
 #pragma unroll
-      for (int c = 0; c < G; ++c) {
-        const int i = threadIdx.x + c * step;
-        if (t < 0) continue;
-        uint4* at_c = place(st, c);
-        if (FULL || p.dh) {
-          Raw<false>::fetch(at_c, at(p.dh, p.dh_row, t), i, p.groups);
-          Raw<F32>::fetch(at_c + 3 * step, at(p.x, p.x_row, t), i, p.groups);
-        }
-        if (FULL || p.y) Raw<false>::fetch(at_c + step, at(p.y, p.y_row, t), i, p.groups);
-        if constexpr (GATE != kNoGate) Raw<false>::fetch(at_c + 2 * step, at(p.gate, p.gate_row, t), i, p.groups);
-        if (FULL || p.dx_out) Raw<F32>::fetch(at_c + (3 + kRes) * step, at(p.dx_out, p.dx_out_row, t), i, p.groups);
+    for (int c = 0; c < G; ++c) {
+      const int i = first + threadIdx.x + c * step;
+      if (t < 0) continue;
+      uint4* at_c = place(st, c);
+      if (FULL || p.dh) {
+        Raw<false>::fetch(at_c, at(p.dh, p.dh_row, t), i, last);
+        Raw<F32>::fetch(at_c + 3 * step, at(p.x, p.x_row, t), i, last);
       }
-      async_commit();
+      if (FULL || p.y) Raw<false>::fetch(at_c + step, at(p.y, p.y_row, t), i, last);
+      if constexpr (GATE != kNoGate) Raw<false>::fetch(at_c + 2 * step, at(p.gate, p.gate_row, t), i, last);
+      if (FULL || p.dx_out) Raw<F32>::fetch(at_c + (3 + kRes) * step, at(p.dx_out, p.dx_out_row, t), i, last);
     }
+    async_commit();
   };
-  if constexpr (RING) {
-    for (int c = 0; c < G; ++c)
-      for (int st = 0; st < 2 && threadIdx.x + c * step >= p.groups; ++st) {
-        for (int a = 0; a < 3; ++a) Raw<false>::clear(place(st, c) + a * step);
-        for (int a = 0; a < 2; ++a) Raw<F32>::clear(place(st, c) + (3 + a * kRes) * step);
-      }
-  }
+  for (int c = 0; c < G; ++c)
+    for (int st = 0; st < 2 && first + (int)threadIdx.x + c * step >= last; ++st) {
+      for (int a = 0; a < 3; ++a) Raw<false>::clear(place(st, c) + a * step);
+      for (int a = 0; a < 2; ++a) Raw<F32>::clear(place(st, c) + (3 + a * kRes) * step);
+    }
   int64_t t = walk.next(p);
   fetch(0, t);
   for (int64_t next; t >= 0; t = next, stage ^= 1) {
     next = walk.next(p);
-    if constexpr (RING && F32) __syncwarp();  // the lanes have read the last row
+    if constexpr (F32) __syncwarp();  // the lanes have read the last row
     fetch(stage ^ 1, next);
     Raw<F32> xr[G], dr[G];
     Raw<false> hr[G], yr[G], zr[G];
-    if constexpr (RING) async_wait<1>();
-    if constexpr (RING && F32) __syncwarp();
+    async_wait<1>();
+    if constexpr (F32) __syncwarp();
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * step;
       xr[c].zero(), hr[c].zero(), yr[c].zero(), dr[c].zero(), zr[c].zero();
-      if (!RING && i >= p.groups) continue;
-      if constexpr (RING) {
-        const uint4* at_c = place(stage, c);
-        if (FULL || p.dh) {
-          hr[c].take(at_c);
-          xr[c].take(at_c + 3 * step);
-        }
-        if (FULL || p.y) yr[c].take(at_c + step);
-      } else {
-        if (FULL || p.dh) {
-          xr[c].load(at(p.x, p.x_row, t), i);
-          hr[c].load(at(p.dh, p.dh_row, t), i);
-        }
-        if (FULL || p.y) yr[c].load(at(p.y, p.y_row, t), i);
-        if (FULL || p.dx_out) dr[c].load(at(p.dx_out, p.dx_out_row, t), i);
-        if constexpr (GATE != kNoGate) zr[c].load(at(p.gate, p.gate_row, t), i);
+      const uint4* at_c = place(stage, c);
+      if (FULL || p.dh) {
+        hr[c].take(at_c);
+        xr[c].take(at_c + 3 * step);
       }
+      if (FULL || p.y) yr[c].take(at_c + step);
     }
     uint64_t xx = 0, kx = 0, yy = 0;
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * step;
-      const Pairs w = load_w<FULL>(p.w_pre, p.w_f32, i < p.groups ? i : 0);
+      const int i = first + threadIdx.x + c * step;
+      const Pairs w = load_w<FULL>(p.w_pre, p.w_f32, i < last ? i : 0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint64_t x = xr[c].pair(j), y = yr[c].pair(j);
@@ -488,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNo
         yy = f2_fma(y, y, yy);
       }
     }
-    const float4 sums = row_sums(make_float4(sum_of(xx), sum_of(kx), sum_of(yy), 0.f), sh, half4);
+    const float4 sums = row_sums<PAIR>(make_float4(sum_of(xx), sum_of(kx), sum_of(yy), 0.f), sh, half4);
     const float r = FULL || p.dh ? rsqrtf(sums.x * inv_n + p.eps) : 0.f;
     const float ry = p.post_norm ? rsqrtf(sums.z * inv_n + p.eps) : 1.f;
     const uint64_t r2 = both(r), nm2 = both(-r * (r * r * (sums.y * inv_n))), ry2 = both(ry);
@@ -496,14 +541,12 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNo
     Pairs ee[G];  // e
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * step;
-      const bool there = i < p.groups;
+      const int i = first + threadIdx.x + c * step;
+      const bool there = i < last;
       Pairs w = load_w<FULL>(p.w_pre, p.w_f32, there ? i : 0), out;
-      if constexpr (RING) {  // what the sums did not need stayed in shared memory till now
-        const uint4* at_c = place(stage, c);
-        if constexpr (GATE != kNoGate) zr[c].take(at_c + 2 * step);
-        if (FULL || p.dx_out) dr[c].take(at_c + (3 + kRes) * step);
-      }
+      const uint4* at_c = place(stage, c);  // what the sums did not need stayed in shared memory till now
+      if constexpr (GATE != kNoGate) zr[c].take(at_c + 2 * step);
+      if (FULL || p.dx_out) dr[c].take(at_c + (3 + kRes) * step);
       Pairs d;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -529,20 +572,20 @@ __global__ void __launch_bounds__(THREADS, CTAS) res_norm_bwd_kernel(const ResNo
         if (there) store8<false>(at(p.dgate, p.dgate_row, t), i, out);
     }
     if (!FULL && !p.y) continue;
-    const float my = p.post_norm ? ry * (ry * ry * (row_sum(sum_of(ey), sh, half) * inv_n)) : 0.f;
+    const float my = p.post_norm ? ry * (ry * ry * (row_sum<PAIR>(sum_of(ey), sh, half) * inv_n)) : 0.f;
 #pragma unroll
     for (int c = 0; c < G; ++c) {
-      const int i = threadIdx.x + c * step;
+      const int i = first + threadIdx.x + c * step;
 #pragma unroll
       for (int j = 0; j < 4; ++j) ee[c].v[j] = f2_fma(yr[c].pair(j), both(-my), f2_mul(ee[c].v[j], ry2));
-      if (i < p.groups) store8<false>(at(p.dy, p.dy_row, t), i, ee[c]);
+      if (i < last) store8<false>(at(p.dy, p.dy_row, t), i, ee[c]);
     }
   }
-  float* part = p.partial + (size_t)blockIdx.x * 2 * p.n;
+  float* part = p.partial + (size_t)(blockIdx.x / (PAIR ? 2 : 1)) * 2 * p.n;
 #pragma unroll
   for (int c = 0; c < G; ++c) {
-    const int i = threadIdx.x + c * step;
-    if (i >= p.groups) continue;
+    const int i = first + threadIdx.x + c * step;
+    if (i >= last) continue;
     if (p.dw_post) store8<true>(part, i, acc_post[c]);
     if (p.dw_pre) store8<true>(part + p.n, i, acc_pre[c]);
   }
@@ -575,40 +618,64 @@ __global__ void __launch_bounds__(32 * kSumWarps) res_norm_dw_kernel(const float
 
 }  // namespace
 
-int64_t res_norm_ws_bytes(int n) { return (int64_t)most_ctas(n) * 2 * n * sizeof(float); }
+int64_t res_norm_ws_bytes(int n) { return (int64_t)most_sums(n) * 2 * n * sizeof(float); }
 
-// Starts the kernel; its CTAs, or 0 for an error.
+// Starts the kernel with CTAs, or clusters of `per`, up to `most`; their number, or 0
+// for an error.
 template <class Kernel>
-static int start(Kernel kernel, int bytes, int ctas, int most, int threads, const ResNormParams& p, cudaStream_t st) {
+static int start(Kernel kernel, int bytes, int sums, int ctas, int most, int threads, int per, const ResNormParams& p, cudaStream_t st) {
   if (bytes > 40 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return 0;
   // As many CTAs as are resident at once: by registers, by shared memory, and 32 an SM.
-  const int fit = std::max(1, std::min({ctas, 227 * 1024 / (bytes + 2048), 32}));
-  const int grid = (int)std::min({p.units, (int64_t)fit * p.num_sms, (int64_t)most});
-  kernel<<<grid, threads, bytes, st>>>(p);
-  return grid;
-}
-// Rows that do not fit the shared memory twice come straight from memory (RING
-// false): more than 8192 values.
-template <int G, int THREADS, int CTAS, bool RING, bool F32, Gate GATE, bool BWD>
-static int start(const ResNormParams& p, cudaStream_t st) {
-  const int threads = threads_of(p.n, BWD), ctas = CTAS * THREADS / threads;
-  const int bytes = RING ? 2 * G * (BWD ? kBwdWords : kFwdWords)[F32] * threads * 16 : 0;
-  if constexpr (BWD) {
-    const bool full = p.dh && p.y && p.dx_out && p.w_pre && p.w_post && p.w_f32;
-    if constexpr (!RING) return start(res_norm_bwd_kernel<G, THREADS, CTAS, RING, F32, GATE, false>, bytes, ctas, most_ctas(p.n), threads, p, st);
-    else return full ? start(res_norm_bwd_kernel<G, THREADS, CTAS, RING, F32, GATE, true>, bytes, ctas, most_ctas(p.n), threads, p, st)
-                : start(res_norm_bwd_kernel<G, THREADS, CTAS, RING, F32, GATE, false>, bytes, ctas, most_ctas(p.n), threads, p, st);
+  const int fit = std::max(1, std::min({ctas, 228 * 1024 / (bytes + sums + 1024), 32}));
+  const int grid = (int)std::min({p.units, std::max((int64_t)fit * p.num_sms / per, (int64_t)1), (int64_t)most});
+  if (per == 1) {
+    kernel<<<grid, threads, bytes, st>>>(p);
+    return grid;
   }
-  else return start(res_norm_kernel<G, THREADS, CTAS, RING, F32, GATE>, bytes, ctas, INT_MAX, threads, p, st);
+  cudaLaunchConfig_t config = {};
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim = {(unsigned)per, 1, 1};
+  config.gridDim = dim3(grid * per);
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = bytes;
+  config.stream = st;
+  config.attrs = &cluster;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, p) == cudaSuccess ? grid : 0;
 }
-template <int G, int THREADS, int CTAS, bool RING, bool BWD>
+template <int G, int THREADS, int CTAS, bool RING, bool F32, Gate GATE>
+static int start_fwd(const ResNormParams& p, int ring, cudaStream_t st) {
+  const int threads = threads_of(p.n, false), ctas = CTAS * THREADS / threads;
+  return start(res_norm_kernel<G, THREADS, CTAS, RING, F32, GATE>, RING ? ring : 0, sizeof(Sums<THREADS / 32>), ctas, INT_MAX, threads, 1, p, st);
+}
+template <int G, int THREADS, int CTAS, bool F32, Gate GATE>
+static int start_fwd(const ResNormParams& p, cudaStream_t st) {
+  const int ring = 2 * G * kFwdWords[F32] * threads_of(p.n, false) * 16;
+  if constexpr (THREADS == 1024)
+    if (ring > 224 * 1024) return start_fwd<G, THREADS, CTAS, false, F32, GATE>(p, ring, st);
+  return start_fwd<G, THREADS, CTAS, true, F32, GATE>(p, ring, st);
+}
+template <int G, int THREADS, int CTAS, bool PAIR, bool F32, Gate GATE>
+static int start_bwd(const ResNormParams& p, cudaStream_t st) {
+  const int threads = threads_of(p.n, true), ctas = CTAS * THREADS / threads, bytes = 2 * G * kBwdWords[F32] * threads * 16;
+  auto go = [&](auto kernel) { return start(kernel, bytes, sizeof(Sums<THREADS / 32 * (PAIR ? 2 : 1)>), ctas, most_sums(p.n), threads, PAIR ? 2 : 1, p, st); };
+  const bool full = p.dh && p.y && p.dx_out && p.w_pre && p.w_post && p.w_f32;
+  return full ? go(res_norm_bwd_kernel<G, THREADS, CTAS, PAIR, F32, GATE, true>)
+              : go(res_norm_bwd_kernel<G, THREADS, CTAS, PAIR, F32, GATE, false>);
+}
+// The variant for the residual's type and the gate.
+template <int G, int THREADS, int CTAS, bool BWD, bool PAIR = false>
 static int start(const ResNormParams& p, cudaStream_t st) {
+  auto one = [&](auto f32, auto gate) {
+    if constexpr (BWD) return start_bwd<G, THREADS, CTAS, PAIR, decltype(f32)::value, decltype(gate)::value>(p, st);
+    else return start_fwd<G, THREADS, CTAS, decltype(f32)::value, decltype(gate)::value>(p, st);
+  };
   auto gated = [&](auto f32) {
-    constexpr bool kF32 = decltype(f32)::value;
-    if (!p.gate) return start<G, THREADS, CTAS, RING, kF32, kNoGate, BWD>(p, st);
-    return p.gate_fn == FCP_GATE_SIGMOID ? start<G, THREADS, CTAS, RING, kF32, kSigmoidGate, BWD>(p, st)
-                                         : start<G, THREADS, CTAS, RING, kF32, kPlainGate, BWD>(p, st);
+    if (!p.gate) return one(f32, std::integral_constant<Gate, kNoGate>());
+    return p.gate_fn == FCP_GATE_SIGMOID ? one(f32, std::integral_constant<Gate, kSigmoidGate>())
+                                         : one(f32, std::integral_constant<Gate, kPlainGate>());
   };
   return p.res_f32 ? gated(std::true_type()) : gated(std::false_type());
 }
@@ -619,16 +686,16 @@ int launch_res_norm(const ResNormParams& a, cudaStream_t st) {
   int grid = 0;
   if (p.units > 0) {
     if (p.dx)
-      grid = p.n <= 1024   ? start<1, 128, 5, true, true>(p, st)
-             : p.n <= 2048 ? start<2, 128, 4, true, true>(p, st)
-             : p.n <= 4096 ? start<2, 256, 2, true, true>(p, st)
-             : p.n <= 8192 ? start<2, 512, 1, true, true>(p, st)
-                           : start<4, 512, 1, false, true>(p, st);
+      grid = p.n <= 1024   ? start<1, 128, 5, true>(p, st)
+             : p.n <= 2048 ? start<2, 128, 4, true>(p, st)
+             : p.n <= 4096 ? start<2, 256, 2, true>(p, st)
+             : p.n <= 8192 ? start<2, 512, 1, true>(p, st)
+                           : start<2, 512, 1, true, true>(p, st);
     else
-      grid = p.n <= 1024   ? start<1, 128, 8, true, false>(p, st)
-             : p.n <= 4096 ? start<2, 256, 4, true, false>(p, st)
-             : p.n <= 8192 ? start<2, 512, 2, true, false>(p, st)
-                           : start<2, 1024, 1, false, false>(p, st);
+      grid = p.n <= 1024   ? start<1, 128, 8, false>(p, st)
+             : p.n <= 4096 ? start<2, 256, 4, false>(p, st)
+             : p.n <= 8192 ? start<2, 512, 2, false>(p, st)
+                           : start<2, 1024, 1, false>(p, st);
     if (grid == 0) return FCP_ERR_CUDA;
   }
   // (A shard without tokens: no rows, whose sum is written as zero.)

@@ -325,3 +325,37 @@ def test_binding_refusals(cuda):
     from context_document_masked_gb300 import fcp
     with pytest.raises(fcp.FcpError):
         run_forward(s, x, KW, h=x["y"])
+
+
+# Rows of more than 8192 values: the forward's ring where it fits the shared memory, the gradient by pairs of CTAs. (A pair adds
+# T / 76 + 1 rows of a weight's gradient, and a warp of the last sum 3 of theirs, not 40: for T <= 5624 within the bound above.)
+@pytest.mark.parametrize("T,n", [(1, 8200), (200, 8208), (311, 9216), (90, 11464), (77, 12296), (160, 16384)])
+@pytest.mark.parametrize("res", [torch.bfloat16, torch.float32])
+def test_wide_rows(cuda, T, n, res):
+    check(session([T]), make(T, n, seed=n, res=res), KW)
+
+
+@pytest.mark.parametrize("gate,post_norm,w", [("plain", True, torch.bfloat16), (None, False, torch.float32), (None, True, None),
+                                              ("sigmoid", False, torch.float32)])
+def test_wide_forms(cuda, gate, post_norm, w):
+    x = make(170, 10008, gate=gate, w=w)
+    check(session([100, 70]), x, dict(KW, post_norm=post_norm, gate_fn=gate or "plain"))
+
+
+def test_wide_rows_without_a_block_of_shards_repeat(cuda):
+    docs = [1, 2, 5] * 210  # so many runs that they are taken whole
+    s, n, T = session(docs, 1, "wholedoc"), 8712, 8 * 210
+    x, kw = make(T, n, seed=3), dict(KW)
+    fwd, bwd = forward_reference(x, kw), backward_reference(x, kw)
+    first = run_backward(s, x, kw, shard=0)
+    again = run_backward(s, x, kw, shard=0)
+    for k, y in first.items():
+        assert torch.equal(y, again[k])
+        within(y, bwd[k], k)
+    for k, y in zip(("x_out", "h"), run_forward(s, x, kw, shard=0)):
+        within(y, fwd[k], k)
+    x = make(90, n, block=False, res=torch.float32)
+    kw = dict(KW, res_scale=1.0)
+    got, want = run_backward(session([90]), x, kw), backward_reference(x, kw)
+    within(got["dx"], want["dx"], "dx")
+    within(got["dw_pre"], want["dw_pre"], "dw_pre")
