@@ -61,8 +61,8 @@ BWD_TRAFFIC_SOURCES = [
     ("context_document_masked_gb300/csrc/tables.cpp", None, None),
 ]
 BWD_TRAFFIC = {   # workload -> {"sha256": ..., "bytes": ...}
-    5: {"sha256": "f4c159bc24554e6894682bd290b4aea0b0684f347e884b120b6693072a3e692a",
-        "bytes": (19.18 + 17.71 + 239.99 + 144.00) * 1e9},   # preprocess + main kernel
+    5: {"sha256": "4b11f850492b4987994ac675c3d683747d93932ec79e8f42b5e549c8d8e06141",
+        "bytes": (19.17 + 17.71 + 239.85 + 143.93) * 1e9},   # preprocess + main kernel
 }
 
 

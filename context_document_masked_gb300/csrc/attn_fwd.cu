@@ -66,7 +66,8 @@
 // chain of a unit, about 12,000 cycles for two key tiles (tensor pipe 25% busy, DRAM
 // 33%). Slower: the softmax by runs of 32 columns, those that nobody sees left out
 // (410 us for 308), or masked run by run (622): branches around parts of the row's
-// 128 registers make it spill.
+// 128 registers make it spill; the results stored by a warpgroup of their own, with registers
+// handed over (324), or by TMA out of shared memory, with four stages (321).
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -359,3 +359,32 @@ def test_wide_rows_without_a_block_of_shards_repeat(cuda):
     got, want = run_backward(session([90]), x, kw), backward_reference(x, kw)
     within(got["dx"], want["dx"], "dx")
     within(got["dw_pre"], want["dw_pre"], "dw_pre")
+
+
+def test_rows_past_32_bits(cuda):
+    """Columns of one tensor of 2.6 G values (5.2 GB): the same results as from tensors of their own, whose first and last
+    rows are the definition's."""
+    T, n, width = 40000, 64, 65536
+    s = session([15000, 25000], 2)
+    x = make(T, n, seed=11)
+    wide = torch.empty(T, width, dtype=torch.bfloat16, device="cuda")
+
+    def column(i, t=None):
+        c = wide[:, width - (i + 1) * n:width - i * n]
+        return c.fill_(-7) if t is None else c.copy_(t)
+    far = {k: column(i, x[k]) for i, k in enumerate(("x", "y", "gate", "dx_out", "dh"))}
+    far = dict(x, **far)
+    names = ("x_out", "h", "dx", "dy", "dgate")
+    outs = {k: column(5 + i) for i, k in enumerate(names)}
+    run_forward(s, far, KW, x_out=outs["x_out"], h=outs["h"])
+    dw = run_backward(s, far, KW, dx=outs["dx"], dy=outs["dy"], dgate=outs["dgate"])
+    near = dict(zip(names, run_forward(s, x, KW))) | run_backward(s, x, KW)
+    for k in names:
+        assert torch.equal(outs[k], near[k]), k
+    for k in ("dw_post", "dw_pre"):
+        assert torch.equal(dw[k], near[k])
+    for rows in (slice(0, 40), slice(T - 40, T)):
+        part = {k: t[rows] if t is not None and t.dim() == 2 else t for k, t in x.items()}
+        want = forward_reference(part, KW) | {k: v for k, v in backward_reference(part, KW).items() if not k.startswith("dw")}
+        for k in names:
+            within(near[k][rows], want[k], k)
