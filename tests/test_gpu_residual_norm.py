@@ -388,3 +388,9 @@ def test_rows_past_32_bits(cuda):
         want = forward_reference(part, KW) | {k: v for k, v in backward_reference(part, KW).items() if not k.startswith("dw")}
         for k in names:
             within(near[k][rows], want[k], k)
+
+
+@pytest.mark.parametrize("T,n", [(130, 256), (77, 1000), (9, 2056), (200, 4096), (33, 8192), (90, 9216)])
+@pytest.mark.parametrize("res", [torch.bfloat16, torch.float32])
+def test_bf16_weights(cuda, T, n, res):
+    check(session([T]), make(T, n, seed=n, res=res, w=torch.bfloat16), KW)
