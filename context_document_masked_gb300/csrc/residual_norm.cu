@@ -36,8 +36,8 @@
 // row is fetched into L2 (16384 rows of 16384: bf16 566 to 505 us, fp32 820 to 626; of 9216 396 to 296, 448
 // to 364). Gradient: a row on two CTAs of a cluster, which exchange their sums by each other's
 // shared memory, where one CTA with four groups a thread and no ring took 1392 us (now 1221), fp32 1806 (1456); at 9216
-// 929 (886), 1066 (953). Its 0.52 to 0.6 of the copy rate: both cluster barriers of a row are
-// waited for by every warp of an SM. Clusters of more and smaller CTAs, two an SM, were slower (1936 us).
+// 929 (886), 1066 (953). Its 0.52 to 0.6 of the copy rate: every warp of an SM waits for both cluster
+// barriers of a row, whose release waits for the row's stores. Clusters of more and smaller CTAs, two an SM, were slower (1936 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
