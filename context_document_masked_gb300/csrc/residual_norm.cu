@@ -24,20 +24,24 @@
 // way there instructions and, in the gradient, registers (its sums take 32 of a
 // thread's 128, which leaves 16 warps an SM). 65536 rows of 8192, bf16 residual,
 // sigmoid gate: 849 us, 6.32 TB/s (0.93 of the measured copy rate); gradient of
-// 32768 rows of 4096: 385 us, 5.58 TB/s (0.82; with an fp32 residual 470 us, 6.28 TB/s). From 1264 and 887: registers that a launch
-// bound of 1024 threads had cut to 64 (1103, 546), the ring (1058, 511), pairs of values an
-// instruction and four sums in six shuffles (952, 504), the gate's form at compile
-// time (898, 464), the operands' presence too, and zeros for groups past a row's end in
-// place of branches (884, 401), shared memory for a CTA's own number of warps (849, 385; fp32 585 to
+// 32768 rows of 4096: 385 us, 5.58 TB/s (0.82; with an fp32 residual 470 us, 6.28
+// TB/s). From 1264 and 887: registers that a launch bound of 1024 threads had cut to
+// 64 (1103, 546), the ring (1058, 511), pairs of values an instruction and four sums
+// in six shuffles (952, 504), the gate's form at compile time (898, 464), the
+// operands' presence too, and zeros for groups past a row's end in place of branches
+// (884, 401), shared memory for a CTA's own number of warps (849, 385; fp32 585 to
 // 470, two CTAs an SM). Slower in the gradient: four groups a thread (581: eight
 // warps an SM), one (1162: spills), fp32 pairs kept for raw bf16 (488).
 //
-// Rows of more than 8192 values. Forward: the ring where it fits the shared memory, else the next
-// row is fetched into L2 (16384 rows of 16384: bf16 566 to 505 us, fp32 820 to 626; of 9216 396 to 296, 448
-// to 364). Gradient: a row on two CTAs of a cluster, which exchange their sums by each other's
-// shared memory, where one CTA with four groups a thread and no ring took 1392 us (now 1221), fp32 1806 (1456); at 9216
-// 929 (886), 1066 (953). Its 0.52 to 0.6 of the copy rate: every warp of an SM waits for both cluster
-// barriers of a row, whose release waits for the row's stores. Clusters of more and smaller CTAs, two an SM, were slower (1936 us).
+// Rows of more than 8192 values. Forward: the ring where it fits the shared memory,
+// else the next row is fetched into L2 (16384 rows of 16384: bf16 566 to 505 us, fp32
+// 820 to 626; of 9216 396 to 296, 448 to 364). Gradient: a row on two CTAs of a
+// cluster, which exchange their sums by each other's shared memory, where one CTA
+// with four groups a thread and no ring took 1392 us (now 1221), fp32 1806 (1456); at
+// 9216 929 (886), 1066 (953); at 8200, with nine warps an SM, 1795 (1926), 2111 (2054).
+// Its 0.52 to 0.6 of the copy rate: every warp of an SM waits for both cluster
+// barriers of a row, whose release waits for the row's stores. Clusters of more and
+// smaller CTAs, two an SM, were slower (1936 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
