@@ -155,18 +155,14 @@ class CPAttention:
         with _on_stream(stream):
             if dq is None:
                 dq = torch.empty(self.T, self.hq, self.d, dtype=torch.float32, device=self.device)
-            if dk is None and dv is None:  # one fill for both
-                both = torch.zeros(2, self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
-                dk, dv = both[0], both[1]
-            else:
-                if dk is None:
-                    dk = torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
-                elif zero_kv_grads:
-                    dk.zero_()
-                if dv is None:
-                    dv = torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
-                elif zero_kv_grads:
-                    dv.zero_()
+            if dk is None:
+                dk = torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
+            elif zero_kv_grads:
+                dk.zero_()
+            if dv is None:
+                dv = torch.zeros(self.T, self.hkv, self.d, dtype=torch.float32, device=self.device)
+            elif zero_kv_grads:
+                dv.zero_()
         fcp.attn_bwd(q, k, v, self.kbuf, self.vbuf, out, lse, dout, self.dplan, shard, dq, dk, dv,
                      self.ws, scale=self.scale, stream=stream)
         return dq, dk, dv
