@@ -216,6 +216,8 @@ class CPAttention:
         y normed (post_norm), gated, scaled and added to the residual x, and that normed again (pre_norm;
         else h is None). x [T][n] bf16 or fp32, y and gate bf16; without y only the norm (x_out is then
         x itself where res_scale is 1 and it is not given)."""
+        if h is not None and not pre_norm:
+            raise ValueError("residual_norm: h is the norm's result: pre_norm = True with it")
         with _on_stream(stream):
             if x_out is None and (y is not None or res_scale != 1.0 or not pre_norm):
                 x_out = torch.empty(x.shape, dtype=x.dtype, device=self.device)
