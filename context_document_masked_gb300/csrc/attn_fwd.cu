@@ -76,6 +76,7 @@
 
 #include "bias.cuh"
 #include "kernels.h"
+#include "plan.h"
 #include "sm103.cuh"
 
 namespace fcp {
@@ -238,10 +239,9 @@ struct WorkItem {
 // role reads of the tables for each, four loads one after another, took longer
 // than a tile. There the producer decodes a unit while the one before it is
 // computed and puts what the others need into shared memory.
-constexpr int kUnitSegs = 6;  // key runs held; a unit of more reads the table
 struct WindowUnit {
-  int q_start, q_rows, q1, rows1, q_last, h0, h1, nt, doc, slots, lo, seg_begin, n_segs;  // nt: -1 skipped, -2 none left
-  int run[kUnitSegs][2];  // keys [begin, end) of the segments that hold any
+  int q_start, q_rows, q1, rows1, q_last, h0, h1, nt, doc, slots, n_runs;  // nt: -1 skipped, -2 none left
+  int run[kWindowSegs][2];  // keys [begin, end) of the segments that hold any
 };
 template <int R>
 struct UnitRing {
@@ -272,8 +272,13 @@ __device__ __forceinline__ void describe(const FwdParams& p, const WorkItem& it,
     if constexpr (kDeviceChecks) ok = segment_ok(p, g);
     const int ks = __ldg(g + 2), a = max(ks, it.lo), e = min(min(ks + __ldg(g + 3), p.kv_hi), q_last + 1);
     if (e <= a) continue;
-    if (segs < kUnitSegs) u->run[segs][0] = a, u->run[segs][1] = e;
-    ++segs;
+    if constexpr (kDeviceChecks)
+      if (segs == kWindowSegs) {
+        ok = false;
+        break;
+      }
+    u->run[segs][0] = a;
+    u->run[segs++][1] = e;
     n += (e - a + slots + 127) / 128;  // the first tile's sinks take `slots` of its rows
     slots = 0;
   }
@@ -286,9 +291,7 @@ __device__ __forceinline__ void describe(const FwdParams& p, const WorkItem& it,
   u->h1 = it.h1;
   u->doc = it.doc;
   u->slots = it.slots;
-  u->lo = it.lo;
-  u->seg_begin = it.seg_begin;
-  u->n_segs = segs > kUnitSegs ? -it.seg_count : segs;
+  u->n_runs = segs;
   u->nt = ok ? n + (slots > 0) : -1;
 }
 
@@ -296,26 +299,17 @@ __device__ __forceinline__ void describe(const FwdParams& p, const WorkItem& it,
 struct UnitWalker {
   int s, pos, end, slots;
   __device__ __forceinline__ explicit UnitWalker(const WindowUnit& u) : s(0), pos(0), end(0), slots(u.slots) {}
-  __device__ __forceinline__ void next(const FwdParams& p, const WindowUnit& u, int& key, int& n, int& off) {
+  __device__ __forceinline__ void next(const WindowUnit& u, int& key, int& n, int& off) {
     off = slots;
     slots = 0;
-    const int q_last = u.q_last;
-    while (pos >= end) {
-      if (s >= (u.n_segs < 0 ? -u.n_segs : u.n_segs)) {
-        key = q_last;
+    if (pos >= end) {
+      if (s >= u.n_runs) {
+        key = u.q_last;
         n = 0;
         return;
       }
-      if (u.n_segs >= 0) {
-        pos = u.run[s][0];
-        end = u.run[s][1];
-      } else {
-        const int* g = p.segs + 4 * (u.seg_begin + s);
-        const int ks = __ldg(g + 2);
-        pos = max(ks, u.lo);
-        end = min(min(ks + __ldg(g + 3), p.kv_hi), q_last + 1);
-      }
-      ++s;
+      pos = u.run[s][0];  // (no run is empty)
+      end = u.run[s++][1];
     }
     key = pos;
     n = min(128 - off, end - pos);
@@ -764,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (!kWindow)
           wk.init(p.segs, it.seg_begin, it.seg_count, q_last, p.kv_lo, p.kv_hi, p.kbuf_shift, p.seg_filter);
         for (int t = 0; t < nt; ++t) {
-          if constexpr (kWindow) wk.next(p, ring.unit[k % 4], key, n, off);
+          if constexpr (kWindow) wk.next(ring.unit[k % 4], key, n, off);
           else wk.next(src, row, key, n);
           // Bias of the tile: one bucket for all the warp's distances, or the
           // window of them. Set up before S is waited for, so its latency is

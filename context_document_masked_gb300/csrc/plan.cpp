@@ -369,6 +369,9 @@ int make_window_plan(const Plan& of, int32_t window, int32_t sinks, fcp_plan_t**
   for (const Shard& s : of.shards) pieces.push_back(s.pieces);
   p->finish(pieces);
   p->build_work_tables();
+  const int32_t* piece = p->dev.data() + p->tab_off[TB_PIECES];
+  for (int32_t i = 0; i < p->tab_cnt[TB_PIECES]; ++i, piece += 8)
+    if (piece[6] > kWindowSegs) return FCP_ERR_UNSUPPORTED;  // (no policy's shards have as many)
   *out = p.release();
   return FCP_OK;
 }

@@ -17,6 +17,12 @@ constexpr int kRowChunk = 128;
 // the rows after which the 128-byte swizzle begins again.
 inline int32_t sink_slots(int32_t sinks) { return (sinks + 7) / 8 * 8; }
 
+// Key segments of a piece under a window, at most: what the forward holds of a
+// unit. (A shard has two pieces of a document at most; the second's walk meets the
+// received sinks, keys received before the first, that, keys received between them
+// and itself.)
+constexpr int kWindowSegs = 6;
+
 struct Piece {
   int32_t doc, start, end;
 };

@@ -1,4 +1,5 @@
-"""Windowed plans without a GPU, more of them: the double query tiles with the rows that they read."""
+"""Windowed plans without a GPU, more of them: the double query tiles with the rows that they read, and how many key
+segments a piece has."""
 import ctypes as C
 
 import numpy as np
@@ -6,6 +7,8 @@ import pytest
 
 from test_window_plan import CASES, FAKE, PIECES, SEGS, mask, source_keys, tables
 
+POLICIES = ("llama3", "perdoc", "wholedoc", "hybrid", "hybrid_tiles")
+MOST_SEGS = 6  # what the forward holds of a unit
 # The last document ends before its sinks do, and is longer than the window.
 SHORT_LAST = [([100, 20], 1, "perdoc", 8, 33), ([40, 30], 2, "perdoc", 4, 64), ([5, 9], 1, "wholedoc", 2, 64)]
 
@@ -53,3 +56,22 @@ def test_double_tiles_read_the_keys_they_stand_for(lib, docs, cp, policy, window
                     seen[np.ix_(q, key)] += (key <= q[:, None]) & (q[:, None] - key < W0)
                     a += m
     assert (queries == 1).all() and np.array_equal(seen, mask(docs, window, sinks).astype(int))
+
+
+def test_segments_of_a_piece(lib):
+    """At most as many as the forward holds of a unit, under every policy, windows and sinks of all lengths among them."""
+    rng = np.random.default_rng(17)
+    most = 0
+    for _ in range(1500):
+        cp = int(rng.integers(1, 17))
+        docs = [int(x) for x in rng.integers(1, int(rng.choice([3, 12, 60, 400])), int(rng.integers(1, 12)))]
+        docs[-1] += -sum(docs) % (2 * cp)  # what every policy can shard
+        p = lib.Plan(docs, cp, str(rng.choice(POLICIES)))
+        sinks = int(rng.integers(0, 65))
+        w = p.windowed(int(2 ** rng.uniform(0, 9)), sinks)
+        pieces = tables(w, w.device_image())[PIECES]
+        most = max(most, int(pieces[:, 6].max()))
+        for j in range(cp):
+            doc = [x[0] for x in w.shard(j)["pieces"]]
+            assert all(doc.count(x) <= 2 for x in doc)
+    assert 4 <= most <= MOST_SEGS
