@@ -662,7 +662,9 @@ static int start_fwd(const ResNormParams& p, int ring, cudaStream_t st) {
 template <int G, int THREADS, int CTAS, bool F32, Gate GATE>
 static int start_fwd(const ResNormParams& p, cudaStream_t st) {
   const int ring = 2 * G * kFwdWords[F32] * threads_of(p.n, false) * 16;
-  if constexpr (THREADS == 1024)
+  // (Two stages of fp32 rows of more than 14336 values are too large; of bf16 ones none are.)
+  static_assert(2 * G * kFwdWords[0] * THREADS * 16 <= 224 * 1024, "a ring that does not fit");
+  if constexpr (THREADS == 1024 && F32)
     if (ring > 224 * 1024) return start_fwd<G, THREADS, CTAS, false, F32, GATE>(p, ring, st);
   return start_fwd<G, THREADS, CTAS, true, F32, GATE>(p, ring, st);
 }
