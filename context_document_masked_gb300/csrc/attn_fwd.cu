@@ -60,12 +60,14 @@
 //   (WindowUnit). 32K packed sequence (32/8 heads, d = 128), window 128: 323 -> 308 us.
 // - The head of an odd group that has no partner takes two query tiles instead of
 //   one tile twice: 16 heads of 64 without groups, window 256, 297 -> 214 us.
-// 32K packed sequence, 4 sinks: window 1024 661 us, 128 308 us; one document of 64K,
-// window 4096: 3.38 ms, 1.26 PFLOP/s of pairs that are seen. Bound: long windows as
-// without one (the softmax chain against the other head's MMAs); short ones by the
-// chain of a unit, about 12,000 cycles for two key tiles (tensor pipe 25% busy, DRAM
-// 33%). Slower: the softmax by runs of 32 columns, those that nobody sees left out
-// (410 us for 308), or masked run by run (622): branches around parts of the row's
+// 32K packed sequence, 4 sinks: window 1024 646 us, 128 294 us; one document of 64K,
+// window 4096: 3.34 ms, 1.28 PFLOP/s of pairs that are seen. Bound: long windows as
+// without one (the softmax chain against the other head's MMAs); medium ones also by what
+// the window adds to it (32K, 1024: 8.5 key tiles a unit, 69% of the computed pairs seen, 37% of
+// the tiles masked, whose softmax takes twice an open one's 1,070 cycles); short ones by the
+// chain of a unit, about 12,000 cycles for two key tiles, all masked (tensor pipe 25% busy, DRAM
+// 34%). Slower, beside 308 us at window 128: the softmax by runs of 32 columns, those that nobody
+// sees left out (410 us), or masked run by run (622): branches around parts of the row's
 // 128 registers make it spill; the results stored by a warpgroup of their own, with registers
 // handed over (324), or by TMA out of shared memory, with four stages (321).
 #include <cuda.h>

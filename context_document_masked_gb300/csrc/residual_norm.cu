@@ -33,15 +33,31 @@
 // 470, two CTAs an SM). Slower in the gradient: four groups a thread (581: eight
 // warps an SM), one (1162: spills), fp32 pairs kept for raw bf16 (488).
 //
+// Share of the copy rate by width (2^27 values, every operand, fp32 weights; residual bf16 / fp32):
+//   n         64        128       256       768       1024      2048      4096      5120
+//   forward   0.24/0.34 0.48/0.66 0.90/0.84 0.78/0.92 0.83/0.89 0.93/0.96 0.92/0.95 0.91/0.93
+//   gradient  0.19/0.26 0.38/0.49 0.71/0.79 0.75/0.85 0.80/0.86 0.86/0.92 0.82/0.92 0.62/0.72
+//   n         6144      7168      8192      8200      9216      12288     16384
+//   forward   0.85/0.94 0.86/0.95 0.89/0.87 0.61/0.72 0.75/0.85 0.76/0.89 0.75/0.85
+//   gradient  0.65/0.75 0.65/0.76 0.68/0.74 0.33/0.42 0.40/0.51 0.49/0.56 0.52/0.58
+// Below 256 values a part of the one warp's lanes hold none. The gradient of 4097 to 8191 values
+// has one CTA an SM, of 9 to 16 warps, which all wait at a row's two barriers (5120: ten
+// warps, 35% of the issue slots used). A width just above a step of the CTA's size leaves
+// lanes empty (2056: forward 0.72, gradient 0.65; 4104: 0.73, 0.50), and rows that are not
+// whole lines of 128 bytes cost a tenth beside a neighbour with as many warps (5000 for 5120:
+// gradient 0.53 for 0.62; 8200 for 8256: forward 0.61 for 0.69, gradient 0.33 for 0.35).
+//
 // Rows of more than 8192 values. Forward: the ring where it fits the shared memory,
-// else the next row is fetched into L2 (16384 rows of 16384: bf16 566 to 505 us, fp32
-// 820 to 626; of 9216 396 to 296, 448 to 364). Gradient: a row on two CTAs of a
+// else the next row is fetched into L2 (16384 rows of 16384: bf16 566 to 510 us, fp32
+// 820 to 624; of 9216 396 to 298, 448 to 364). Gradient: a row on two CTAs of a
 // cluster, which exchange their sums by each other's shared memory, where one CTA
-// with four groups a thread and no ring took 1392 us (now 1221), fp32 1806 (1456); at
-// 9216 929 (886), 1066 (953); at 8200, with nine warps an SM, 1795 (1926), 2111 (2054).
-// Its 0.52 to 0.6 of the copy rate: every warp of an SM waits for both cluster
-// barriers of a row, whose release waits for the row's stores. Clusters of more and
-// smaller CTAs, two an SM, were slower (1936 us).
+// had four groups a thread and no ring: 16384 rows of 16384 1392 to 1202 us, fp32 1806 to
+// 1461; of 9216 929 to 898, 1066 to 966; 32768 rows of 8200 1795 to 1926, 2111 to 2054 (the
+// pair loses 7% in bf16 there). A pair takes 4.5 us for a row of 8200, 4.2 of 9216 and
+// 5.6 of 16384: the two cluster barriers of a row, whose release waits for the row's stores,
+// not the bytes (of a warp's stalls the barriers have most: membar 1.9, barrier 0.7 an
+// issue; DRAM reads are the algorithmic ones at 8200 too). Clusters of more and smaller
+// CTAs, two an SM, were slower (1936 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

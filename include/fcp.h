@@ -155,7 +155,10 @@ void fcp_plan_free(fcp_plan_t* plan);
  * fcp_gather_kv, fcp_attn_fwd, fcp_attn_bwd, the head norm and rotation and the
  * residual norm take it like any other plan; fcp_attn_fwd_qk8, _ring, _noalloc
  * and _bias and fcp_attn_bwd_bias return FCP_ERR_UNSUPPORTED for it. eq4_tokens
- * and eq5_tokens stay those of whole prefixes, as the paper defines them.
+ * and eq5_tokens stay those of whole prefixes, as the paper defines them. Values of
+ * q, k, v and dout in a tile are computed with whether a query sees them or not, so
+ * one that is not finite can reach rows outside its window, and of a neighbouring
+ * document (P = 0 times NaN).
  * Errors: FCP_ERR_INVALID_ARG (null, window < 1, sinks < 0), FCP_ERR_UNSUPPORTED
  * (sinks > FCP_MAX_SINKS, T > 2^30), FCP_ERR_CAPACITY (no host memory).
  */
